@@ -57,8 +57,8 @@ typedef enum {
                                       device                                     */
     TMAGEMM_ERR_CUDA = -4,         /* a CUDA runtime/driver call failed          */
     TMAGEMM_ERR_TIMEOUT = -5,      /* a device-side pipeline wait timed out      */
-    TMAGEMM_ERR_WORKSPACE = -6,    /* split-K workspace missing, misaligned or
-                                      smaller than required                      */
+    TMAGEMM_ERR_WORKSPACE = -6,    /* workspace missing, misaligned or smaller
+                                      than required                              */
     TMAGEMM_ERR_SCRATCH_LIMIT = -7, /* gemm_f16_splitk_noalloc: the problem needs
                                       more than its fixed 32 MiB scratch         */
     TMAGEMM_ERR_CHECK = -8         /* checked build only: a kernel self-check
@@ -282,6 +282,122 @@ int tmagemm_set_small_m_route(int route);
 int gemm_bf16(int64_t M, int64_t N, int64_t K, const void* A, const void* B, void* D,
               void* stream);
 int gemv_bf16(int64_t N, int64_t K, const void* x, const void* W, void* y, void* stream);
+
+/*
+ * ---- Block-scaled 8-bit linear layers ----
+ *
+ * e4m3 codes with FP32 scales, one per block of 128 values along K: per row
+ * for activations (A: scale SA[m][k / 128]), per 128 x 128 values for weights
+ * (B: scale SB[n / 128][k / 128]).  A value is its code times its scale.
+ * Scales of rows are addressed as S[row * row_stride + block * block_stride]
+ * (strides in floats, any positive ones); consecutive rows next to each other
+ * (row_stride 1, block_stride >= M) is the layout the products read fastest.
+ * The pages have no counterpart of these entry points.
+ */
+
+/*
+ * Codes and scales of X (M x K, fp16, or bf16 when bf16 != 0, row-major):
+ *   a = max |x| over the block, at least 2^-100;  S = a / 448;
+ *   Q = e4m3(x * (448 / a)), to nearest even, each quotient and product
+ *   rounded to FP32.
+ * A NaN in a block makes its scale NaN, an infinity makes the scale infinite
+ * and its own code NaN; the rest of an infinite block gets code 0.
+ *   block_rows : 1 (one scale per row and 128 columns) or 128 (per 128 x 128).
+ *   Q          : device pointer, M x K e4m3 bytes, row-major.
+ *   S          : device pointer, ceil(M / block_rows) x ceil(K / 128) floats at
+ *                the given strides.
+ * Requirements: X, Q 16-byte, S 4-byte aligned; K % 8 == 0.  M = 0 is OK and
+ * writes nothing.
+ */
+int quantize_fp8(int64_t M, int64_t K, const void* X, int bf16, int block_rows, void* Q, float* S,
+                 int64_t s_row_stride, int64_t s_block_stride, void* stream);
+
+/*
+ * D[m][n] = sum_b SA[m][b] SB[n / 128][b] sum_{k in block b} A[m][k] B[n][k],
+ * summed in FP32 and rounded once to fp16 (bf16 when bf16 != 0).
+ *   A  : device pointer, M x K e4m3, row-major; SA its row scales (strides above).
+ *   B  : device pointer, N x K e4m3, row-major; SB its ceil(N / 128) x
+ *        ceil(K / 128) scales, dense row-major.
+ *   D  : device pointer, M x N, row-major; written, never read.
+ * Requirements: A, B, D 16-byte, SA, SB 4-byte aligned; K % 16 == 0;
+ * N % 8 == 0.  M = 0 is OK and writes nothing.  Deterministic.
+ * Status codes as gemm_f16.
+ */
+int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, const float* SA,
+             int64_t sa_row_stride, int64_t sa_block_stride, const void* B, const float* SB,
+             void* D, int bf16, void* stream);
+
+/*
+ * G products that share N and K, with the row offsets in DEVICE memory: group
+ * g owns rows [m_offsets[g], m_offsets[g + 1]) of A, SA and D and uses B[g]
+ * and SB[g], e.g. the tokens a router sent to expert g, sorted by expert.
+ * Nothing is copied to the host, so the call can follow the router on the
+ * stream and be captured in a CUDA graph.
+ *   G         : 1 <= G <= 384 (more: TMAGEMM_ERR_UNSUPPORTED).
+ *   m_offsets : device pointer, G + 1 int32, non-decreasing, within [0, M].
+ *               The kernels clamp each to [the previous one, M], so other
+ *               values give undefined rows but never an access out of range.
+ *   M         : rows of A and D.  Rows outside every group are not written.
+ *   B, SB     : G matrices of gemm_fp8's layout, back to back.
+ * Other arguments, requirements and results as gemm_fp8; m_offsets 4-byte
+ * aligned.
+ */
+int gemm_fp8_grouped(int64_t G, const int32_t* m_offsets, int64_t M, int64_t N, int64_t K,
+                     const void* A, const float* SA, int64_t sa_row_stride,
+                     int64_t sa_block_stride, const void* B, const float* SB, void* D, int bf16,
+                     void* stream);
+
+/*
+ * The norms around a block, its gate and its residual, in one pass over T rows
+ * of C channels (fp16, or bf16 when bf16 != 0), with FP32 arithmetic:
+ *   u  = y * rsqrt(mean(y^2) + eps) * w_post      (w_post NULL: u = y)
+ *   h' = h + alpha * gate * u                     (y NULL: h' = h, not written)
+ *   x  = h' * rsqrt(mean(h'^2) + eps) * w_pre     (w_pre NULL: no x)
+ * x is computed from the unrounded h' and leaves either in 16 bits (x) or as
+ * e4m3 codes and row scales (x NULL: q, scales at the given strides), the
+ * operands of gemm_fp8.
+ *   gate_mode : 0 none (gate ignored), 1 per channel (C), 2 per token (T),
+ *               3 per element (T x C); the gate has the type of h.
+ *   rstd_post, rstd_pre : T floats each, the two rsqrt factors; the forward
+ *               writes them where not NULL, the backward reads them.
+ * Zero the struct before filling it.  Requirements: 1 <= C <= 16384,
+ * C % 8 == 0; T = 0 is OK (nothing is written but zero sums over rows);
+ * pointers 16-byte aligned except scales, rstd_*, dw_* and a dgate of floats
+ * (4) and a per-token gate (2).  y or w_pre must be given.
+ */
+typedef struct tmagemm_norm {
+    int64_t T, C;
+    int32_t bf16, gate_mode;
+    float alpha, eps;
+    const void *h, *y, *gate, *w_post, *w_pre;
+    float *rstd_post, *rstd_pre;
+    /* forward results */
+    void *h_out, *x, *q;
+    float* scales;
+    int64_t s_row_stride, s_block_stride;
+    /* backward: gradients of h' (NULL: zero) and of x (given iff w_pre is) */
+    const void *dh_out, *dx;
+    /* backward results: gradients of h and y in their type; of the weights as C
+     * floats; of the gate as C floats (per channel), T floats (per token) or
+     * T x C in its type (per element) */
+    void *dh, *dy, *dgate;
+    float *dw_post, *dw_pre;
+} tmagemm_norm;
+
+int norm_residual(const tmagemm_norm* p, void* stream);
+
+/*
+ * Gradients of norm_residual, from its inputs, its two rsqrt factors and the
+ * gradients of its results (h' is recomputed, unrounded).  Sums over rows are
+ * FP32 in a fixed order (deterministic).  The results that the inputs call
+ * for must all be given: dh always, dy with y, dgate with a gate, dw_post with
+ * w_post, dw_pre with w_pre.  `workspace`: scratch of at least
+ * norm_residual_backward_workspace_size(T, C) bytes, 16-byte aligned, not
+ * shared by calls that overlap on the GPU.
+ */
+int norm_residual_backward(const tmagemm_norm* p, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+int64_t norm_residual_backward_workspace_size(int64_t T, int64_t C);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's sticky

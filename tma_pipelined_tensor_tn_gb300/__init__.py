@@ -18,6 +18,7 @@ from ._binding import (  # noqa: F401
     TMAGEMM_ERR_WORKSPACE,
     TMAGEMM_OK,
     TmaGemmError,
+    TmagemmNorm,
     TmagemmOptions,
     check,
     gemm,
@@ -57,6 +58,15 @@ from ._binding import (  # noqa: F401
     tmagemm_set_tile_n,
     tmagemm_tile_coord,
     tmagemm_version,
+)
+from .fp8 import (  # noqa: F401
+    NormGrads,
+    NormOut,
+    gemm_fp8,
+    gemm_fp8_grouped,
+    norm_residual,
+    norm_residual_backward,
+    quantize_fp8,
 )
 
 

@@ -36,10 +36,25 @@ class TmagemmOptions(ctypes.Structure):
         "plain_launch", "m1_route")]
 
 
+class TmagemmNorm(ctypes.Structure):
+    """struct tmagemm_norm: the operands and results of norm_residual and
+    norm_residual_backward (NULL leaves a part out)."""
+    _fields_ = ([(name, ctypes.c_int64) for name in ("T", "C")]
+                + [(name, ctypes.c_int32) for name in ("bf16", "gate_mode")]
+                + [(name, ctypes.c_float) for name in ("alpha", "eps")]
+                + [(name, ctypes.c_void_p) for name in (
+                    "h", "y", "gate", "w_post", "w_pre", "rstd_post", "rstd_pre", "h_out", "x",
+                    "q", "scales")]
+                + [(name, ctypes.c_int64) for name in ("s_row_stride", "s_block_stride")]
+                + [(name, ctypes.c_void_p) for name in (
+                    "dh_out", "dx", "dh", "dy", "dgate", "dw_post", "dw_pre")])
+
+
 # Every symbol include/tmagemm.h declares, with (argtypes, restype).
 _i64, _p, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 _P64 = ctypes.POINTER(ctypes.c_int64)
 _POPT = ctypes.POINTER(TmagemmOptions)
+_PNORM = ctypes.POINTER(TmagemmNorm)
 SIGNATURES = {
     "gemm_f16": ([_i64, _i64, _i64, _p, _p, _p, _p], _int),
     "gemm_f16_ex": ([_i64, _i64, _i64, _p, _p, _p, _POPT, _p], _int),
@@ -54,6 +69,13 @@ SIGNATURES = {
     "gemm_f16_splitk": ([_i64, _i64, _i64, _p, _p, _p, _i64, _p, _i64, _p], _int),
     "gemm_f16_splitk_workspace_size": ([_i64, _i64, _i64, _i64], _i64),
     "gemm_f16_splitk_noalloc": ([_i64, _i64, _i64, _p, _p, _p, _i64, _p], _int),
+    "quantize_fp8": ([_i64, _i64, _p, _int, _int, _p, _p, _i64, _i64, _p], _int),
+    "gemm_fp8": ([_i64, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _int, _p], _int),
+    "gemm_fp8_grouped": ([_i64, _p, _i64, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _int, _p],
+                         _int),
+    "norm_residual": ([_PNORM, _p], _int),
+    "norm_residual_backward": ([_PNORM, _p, _i64, _p], _int),
+    "norm_residual_backward_workspace_size": ([_i64, _i64], _i64),
     "tmagemm_check": ([_p], _int),
     "tmagemm_last_error_detail": ([], _int),
     "tmagemm_checked_unit_counts": ([ctypes.POINTER(ctypes.c_uint32), _i64, _p], _int),

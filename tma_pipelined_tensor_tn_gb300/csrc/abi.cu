@@ -19,6 +19,7 @@
 #include "../../include/tmagemm.h"
 #include "launch.h"
 #include "ptx.cuh"
+#include "fp8.cuh"
 #include "tile_sched.cuh"
 
 namespace tmagemm {
@@ -615,6 +616,190 @@ int gemm_f16_small_m(int64_t M, int64_t N, int64_t K, const void* X, const void*
     return e == cudaSuccess ? TMAGEMM_OK : TMAGEMM_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// gemm_fp8 (offsets == NULL, G = 1) and gemm_fp8_grouped.
+int gemm_fp8_impl(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                  const void* A, const float* SA, int64_t sa_row, int64_t sa_blk, const void* B,
+                  const float* SB, void* D, int bf16, void* stream) {
+    if (M < 0 || !B || !SB || (M > 0 && (!A || !SA || !D))) return TMAGEMM_ERR_INVALID;
+    if (sa_row <= 0 || sa_blk <= 0) return TMAGEMM_ERR_INVALID;
+    if (int s = validate_common(M > 0 ? M : 1, N, K)) return s;
+    if ((K % 16) != 0 || (N % 8) != 0 || !aligned16(A) || !aligned16(B) || !aligned16(D) ||
+        !aligned4(SA) || !aligned4(SB) || !aligned4(offsets))
+        return TMAGEMM_ERR_ALIGN;
+    // Tiles are counted in 32 bits.
+    if (G * N > (int64_t(1) << 31) - 1 ||
+        (ceil_div(M, 128) + G) * ceil_div(N, 128) > (int64_t(1) << 31) - 1)
+        return TMAGEMM_ERR_UNSUPPORTED;
+    if (M == 0) return TMAGEMM_OK;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    Fp8Gemm g{};
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.groups = G;
+    g.A = A;
+    g.SA = SA;
+    g.sa_row = sa_row;
+    g.sa_blk = sa_blk;
+    g.B = B;
+    g.SB = SB;
+    g.D = D;
+    g.offsets = offsets;
+    g.bf16 = bf16 != 0;
+    const Tuning t = process_tuning();
+    const Fp8Device dev{g_encode, d->sms, d->pairs, wait_limit_ns(), d->err_word, t.pdl()};
+    return launch_gemm_fp8(g, dev, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+// The checks norm_residual and its backward share, and the kernels' arguments.
+int norm_args(const tmagemm_norm* p, NormArgs* a) {
+    if (!p || p->T < 0 || p->C <= 0 || p->gate_mode < 0 || p->gate_mode > 3)
+        return TMAGEMM_ERR_INVALID;
+    if ((!p->y && !p->w_pre) || (p->T > 0 && !p->h)) return TMAGEMM_ERR_INVALID;
+    if (!p->y && (p->w_post || p->gate_mode != kGateNone)) return TMAGEMM_ERR_INVALID;
+    if (p->T > 0 && p->gate_mode != kGateNone && !p->gate) return TMAGEMM_ERR_INVALID;
+    if (p->C > 16384 || p->T > (int64_t(1) << 31) - 1) return TMAGEMM_ERR_UNSUPPORTED;
+    const void* aligned[] = {p->h, p->y, p->w_post, p->w_pre,
+                             p->gate_mode == kGateToken ? nullptr : p->gate};
+    for (const void* q : aligned)
+        if (!aligned16(q)) return TMAGEMM_ERR_ALIGN;
+    if ((p->C % 8) != 0 || (reinterpret_cast<uintptr_t>(p->gate) & 1u) != 0 ||
+        !aligned4(p->rstd_post) || !aligned4(p->rstd_pre))
+        return TMAGEMM_ERR_ALIGN;
+    *a = NormArgs{};
+    a->T = p->T;
+    a->C8 = static_cast<int32_t>(p->C / 8);
+    a->gate_mode = p->gate_mode;
+    a->alpha = p->alpha;
+    a->eps = p->eps;
+    a->h = static_cast<const uint4*>(p->h);
+    a->y = static_cast<const uint4*>(p->y);
+    a->w_post = static_cast<const uint4*>(p->w_post);
+    a->w_pre = static_cast<const uint4*>(p->w_pre);
+    a->gate = p->gate;
+    a->rstd_post = p->rstd_post;
+    a->rstd_pre = p->rstd_pre;
+    return TMAGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int quantize_fp8(int64_t M, int64_t K, const void* X, int bf16, int block_rows, void* Q, float* S,
+                 int64_t s_row_stride, int64_t s_block_stride, void* stream) {
+    if (M < 0 || (block_rows != 1 && block_rows != kFp8Block) || s_row_stride <= 0 ||
+        s_block_stride <= 0 || (M > 0 && (!X || !Q || !S)))
+        return TMAGEMM_ERR_INVALID;
+    if (int s = validate_common(M > 0 ? M : 1, K, 1)) return s;
+    if ((K % 8) != 0 || !aligned16(X) || !aligned16(Q) || !aligned4(S)) return TMAGEMM_ERR_ALIGN;
+    if (M == 0) return TMAGEMM_OK;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return launch_quantize(M, K, X, bf16 != 0, block_rows, Q, S, s_row_stride, s_block_stride,
+                           process_tuning().pdl(),
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, const float* SA,
+             int64_t sa_row_stride, int64_t sa_block_stride, const void* B, const float* SB,
+             void* D, int bf16, void* stream) {
+    return gemm_fp8_impl(1, nullptr, M, N, K, A, SA, sa_row_stride, sa_block_stride, B, SB, D,
+                         bf16, stream);
+}
+
+int gemm_fp8_grouped(int64_t G, const int32_t* m_offsets, int64_t M, int64_t N, int64_t K,
+                     const void* A, const float* SA, int64_t sa_row_stride,
+                     int64_t sa_block_stride, const void* B, const float* SB, void* D, int bf16,
+                     void* stream) {
+    if (!m_offsets || G <= 0) return TMAGEMM_ERR_INVALID;
+    if (G > kMaxFp8Groups) return TMAGEMM_ERR_UNSUPPORTED;
+    return gemm_fp8_impl(G, m_offsets, M, N, K, A, SA, sa_row_stride, sa_block_stride, B, SB, D,
+                         bf16, stream);
+}
+
+int norm_residual(const tmagemm_norm* p, void* stream) {
+    NormArgs a;
+    if (int s = norm_args(p, &a)) return s;
+    if (p->T == 0) return TMAGEMM_OK;
+    if (p->y && !p->h_out) return TMAGEMM_ERR_INVALID;
+    if (p->w_pre && !p->x &&
+        (!p->q || !p->scales || p->s_row_stride <= 0 || p->s_block_stride <= 0))
+        return TMAGEMM_ERR_INVALID;
+    if (!aligned16(p->h_out) || !aligned16(p->x) || !aligned16(p->q) || !aligned4(p->scales))
+        return TMAGEMM_ERR_ALIGN;
+    a.h_out = static_cast<uint4*>(p->h_out);
+    a.x = static_cast<uint4*>(p->x);
+    a.q = static_cast<uint2*>(p->q);
+    a.scales = p->scales;
+    a.s_row = p->s_row_stride;
+    a.s_blk = p->s_block_stride;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return launch_norm_forward(a, p->bf16 != 0, d->sms, process_tuning().pdl(),
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+int64_t norm_residual_backward_workspace_size(int64_t T, int64_t C) {
+    if (T < 0 || C <= 0) return TMAGEMM_ERR_INVALID;
+    if (C > 16384 || T > (int64_t(1) << 31) - 1) return TMAGEMM_ERR_UNSUPPORTED;
+    if (T == 0) return 0;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return static_cast<int64_t>(norm_backward_ctas(T, d->sms)) * 2 * C * 4;
+}
+
+int norm_residual_backward(const tmagemm_norm* p, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+    NormArgs a;
+    if (int s = norm_args(p, &a)) return s;
+    if ((p->w_pre != nullptr) != (p->dx != nullptr)) return TMAGEMM_ERR_INVALID;
+    if ((p->w_post && !p->dw_post) || (p->w_pre && !p->dw_pre)) return TMAGEMM_ERR_INVALID;
+    if (p->gate_mode != kGateNone && !p->dgate) return TMAGEMM_ERR_INVALID;
+    if (p->T > 0 && (!p->dh || (p->y && !p->dy) || (p->w_post && !p->rstd_post) ||
+                     (p->w_pre && !p->rstd_pre)))
+        return TMAGEMM_ERR_INVALID;
+    if (!aligned16(p->dh_out) || !aligned16(p->dx) || !aligned16(p->dh) || !aligned16(p->dy) ||
+        (p->gate_mode == kGateElement ? !aligned16(p->dgate) : !aligned4(p->dgate)) ||
+        !aligned4(p->dw_post) || !aligned4(p->dw_pre))
+        return TMAGEMM_ERR_ALIGN;
+    a.dh = static_cast<const uint4*>(p->dh_out);
+    a.dx = static_cast<const uint4*>(p->dx);
+    a.dh_in = static_cast<uint4*>(p->dh);
+    a.dy = static_cast<uint4*>(p->dy);
+    a.dgate = p->dgate;
+    a.dw_post = p->dw_post;
+    a.dw_pre = p->dw_pre;
+    a.partial = static_cast<float*>(workspace);
+    const int64_t need = norm_residual_backward_workspace_size(p->T, p->C);
+    if (need < 0) return static_cast<int>(need);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+        return TMAGEMM_ERR_WORKSPACE;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return launch_norm_backward(a, p->bf16 != 0, d->sms, process_tuning().pdl(),
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+}  // extern "C"
+
+extern "C" {
+
 int tmagemm_check(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return TMAGEMM_ERR_CUDA;
@@ -656,14 +841,15 @@ const char* tmagemm_strerror(int status) {
         case TMAGEMM_OK: return "ok";
         case TMAGEMM_ERR_INVALID: return "invalid argument (non-positive size or NULL pointer)";
         case TMAGEMM_ERR_ALIGN:
-            return "alignment: pointers must be 16-byte aligned, K % 8 == 0 and N % 8 == 0";
+            return "alignment: pointers must be 16-byte aligned, K % 8 == 0 and N % 8 == 0 "
+                   "(e4m3 products: K % 16 == 0; norms: C % 8 == 0)";
         case TMAGEMM_ERR_UNSUPPORTED: return "unsupported size or device";
         case TMAGEMM_ERR_CUDA: return "CUDA runtime or driver call failed";
         case TMAGEMM_ERR_TIMEOUT: return "device-side pipeline wait timed out";
         case TMAGEMM_ERR_CHECK:
             return "a self-check of the checked build failed (site in tmagemm_last_error_detail)";
         case TMAGEMM_ERR_WORKSPACE:
-            return "split-K workspace missing, not 16-byte aligned, or smaller than required";
+            return "workspace missing, not 16-byte aligned, or smaller than required";
         case TMAGEMM_ERR_SCRATCH_LIMIT:
             return "problem needs more split-K scratch than the fixed 32 MiB of the "
                    "no-allocation entry point";

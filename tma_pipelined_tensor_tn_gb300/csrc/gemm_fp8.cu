@@ -1,0 +1,632 @@
+// Block-scaled 8-bit products on tcgen05, dense and grouped by expert:
+//   D[m, n] = sum_b SA[m, b] SB[n / 128, b] sum_{k in block b} A[m, k] B[n, k]
+// with e4m3 A (M x K) and B (N x K), one FP32 scale per 128 values of a row of
+// A and per 128 x 128 values of B, FP32 sums and one rounding to fp16 or bf16.
+//
+// The scales change every 128 k, so the tensor cores cannot add over all of
+// K: each 128-k block's product (four K = 32 MMAs) goes to a TMEM accumulator
+// of its own, and the epilogue warps read it, multiply it by SA * SB (one
+// scalar per row and 128 columns) and add it to FP32 accumulators in their
+// registers, while the next block's MMAs fill another TMEM accumulator.
+//
+// Roles (one CTA per SM, three groups of four warps):
+//   warp 0      TMA producer: A and B k-blocks (128 bytes a row, 128B swizzle)
+//               into a ring of stages;
+//   warp 1      MMA issuer: per k-block four tcgen05.mma.kind::f8f6f4 into
+//               TMEM accumulator it % kAccs, then commits onto the stage's
+//               `empty` barrier and the accumulator's `acc_full` barrier;
+//   warps 4..11 scaling and epilogue: two warps per 32 rows, each half of the
+//               tile's columns.  Their accumulators (128 per thread for 256
+//               columns) take the registers that warps 0..3 (2 and 3 idle)
+//               give up.
+// What bounds it: per k-block of a 128 x 256 tile the MMAs take 512 cycles,
+// reading the accumulator 256 (32 lanes x 4 bytes per cycle and quarter) and
+// the scaling 128 packed multiply-adds in each of the two warps of a
+// scheduler, so the scaling fits under the MMAs.
+//
+// CTA pairs (PAIR): cta_group::2 MMAs on 256 x 256 tiles, each CTA holding 128
+// rows of A and half of B, as in the 16-bit kernel.
+//
+// Grouped: the rows of group g are [off[g], off[g + 1]) with the offsets in
+// device memory; every CTA derives the tile schedule from them, so a router's
+// result is used without a copy to the host.  A row tile may read rows of the
+// next group; they only reach accumulator rows that are not stored.
+//
+// Every mbarrier wait is bounded (ptx.cuh).
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "launch.h"
+#include "ptx.cuh"
+#include "fp8.cuh"
+#include "tile_sched.cuh"
+
+namespace tmagemm {
+
+namespace {
+
+template <int BN_, int STAGES_, bool PAIR_, bool GROUPED_, bool BF16_>
+struct Fp8Cfg {
+    static constexpr int BM = 128, BN = BN_, BK = kFp8Block, STAGES = STAGES_;
+    static constexpr bool kPair = PAIR_, kGrouped = GROUPED_, kBF16 = BF16_;
+    static constexpr int kTileM = PAIR_ ? 256 : 128;
+    static constexpr int kBRows = PAIR_ ? BN_ / 2 : BN_;   // rows of B in this CTA
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kThreads = 128 + 32 * kEpiWarps;
+    // Registers: 384 threads x 168 at launch; 128 x 56 + 256 x 224 afterwards,
+    // the same 64512.
+    static constexpr int kRoleRegs = 56, kEpiRegs = 224;
+    static_assert(128 * kRoleRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 168,
+                  "the shares fit what the block was launched with");
+    static constexpr int kCols = BN_ / 2;                  // columns of one epilogue warp
+    static constexpr int kAccs = 512 / BN_;                // TMEM accumulators
+    // A comes in boxes of 32 rows for grouped problems, where a tile may have
+    // few rows (a box without any is not loaded), else in one of 128.
+    static constexpr int kABoxRows = GROUPED_ ? 32 : 128;
+    static constexpr uint32_t kABytes = BM * BK;
+    static constexpr uint32_t kBBytes = kBRows * BK;
+    static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+    // Staging of D: per epilogue warp 32 rows x kCols, as store boxes of 64
+    // columns (one 128-byte swizzle span).
+    static constexpr uint32_t kBoxBytes = 32 * 128;
+    static constexpr int kBoxes = kCols / 64;
+    static constexpr uint32_t kOffD = STAGES * kStageBytes;
+    static constexpr uint32_t kOffBar = kOffD + kEpiWarps * kBoxes * kBoxBytes;
+    static constexpr uint32_t kNumBars = 2 * STAGES + 2 * kAccs + 1;
+    static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr uint32_t kOffStart = kOffMisc + 16;   // grouped: tile starts
+    static constexpr uint32_t kSmemBytes =
+        kOffStart + (GROUPED_ ? (kMaxFp8Groups + 1) * 4 : 0) + 1024;
+    static_assert(kSmemBytes <= 232448, "fits the 227 KB opt-in shared memory");
+    static_assert(kCols % 64 == 0 && BN <= 256, "whole store boxes");
+};
+
+// Instruction descriptor of kind::f8f6f4 with e4m3 operands and FP32 sums
+// (both K-major): the fields are those of kind::f16, with operand format 0 =
+// e4m3.
+constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// acc (two floats) += t (two accumulator words) * s.
+__device__ __forceinline__ void fma2(float2& acc, uint32_t t0, uint32_t t1, float s) {
+    uint64_t a, t, ss;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc.x), "f"(acc.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "r"(t0), "r"(t1));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(t), "l"(ss));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(acc.x), "=f"(acc.y) : "l"(a));
+}
+
+// Waits for this thread's TMEM loads and ties the loaded registers to the
+// wait, so that no use of them can be moved before it.
+__device__ __forceinline__ void tmem_ld_wait_regs(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                   "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+
+// Registers of this warp's group of four, lowered or raised within what the
+// block was launched with.
+template <int N>
+__device__ __forceinline__ void set_max_regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct Fp8Problem {
+    CUtensorMap tmA;   // A {K, rows}, box {128, kABoxRows}
+    CUtensorMap tmB;   // B {K, N, G}, box {128, kBRows, 1}
+    CUtensorMap tmD;   // D {N, rows}, box {64, 32}
+    const float* sa;   // scale of row m, block b: sa[m * sa_row + b * sa_blk]
+    int64_t sa_row, sa_blk;
+    const float* sb;   // [G][n_blocks][k_blocks]
+    uint16_t* d;
+    const int32_t* offsets;   // grouped: device array of groups + 1 row offsets
+    int32_t rows, N, k_blocks, n_blocks, groups, grid_n, group_m, num_tiles;
+};
+
+// A work unit: one output tile.
+struct Fp8Unit {
+    int32_t row0, row_end;   // the tile's rows are [row0, min(row0 + kTileM, row_end))
+    int32_t n0, group;
+};
+
+// Rows [lo, hi) of group g.  Offsets outside [0, rows] or decreasing ones are
+// clamped, so that no offset can lead outside the operands.
+struct RowRange {
+    int32_t lo, hi;
+};
+__device__ __forceinline__ RowRange group_rows(const Fp8Problem& p, int32_t g) {
+    RowRange r;
+    r.lo = min(max(p.offsets[g], 0), p.rows);
+    r.hi = min(max(p.offsets[g + 1], r.lo), p.rows);
+    return r;
+}
+
+template <class C>
+__device__ __forceinline__ Fp8Unit unit_of(const Fp8Problem& p, const int32_t* start, int32_t u) {
+    Fp8Unit t;
+    if constexpr (C::kGrouped) {
+        int32_t lo = 0, hi = p.groups;   // the last group whose first tile is <= u
+        while (hi - lo > 1) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (start[mid] <= u) lo = mid; else hi = mid;
+        }
+        const RowRange r = group_rows(p, lo);
+        const TileCoord tc = tile_coord(u - start[lo], (r.hi - r.lo + C::kTileM - 1) / C::kTileM,
+                                        p.grid_n, p.group_m);
+        t.row0 = r.lo + tc.m_blk * C::kTileM;
+        t.row_end = r.hi;
+        t.n0 = tc.n_blk * C::BN;
+        t.group = lo;
+    } else {
+        const TileCoord tc = tile_coord(u, (p.rows + C::kTileM - 1) / C::kTileM, p.grid_n,
+                                        p.group_m);
+        t.row0 = tc.m_blk * C::kTileM;
+        t.row_end = p.rows;
+        t.n0 = tc.n_blk * C::BN;
+        t.group = 0;
+    }
+    return t;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1)
+gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns,
+                uint32_t* __restrict__ err) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (sbase - raw);
+
+    const uint32_t bar0 = sbase + C::kOffBar;
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (C::STAGES + s); };
+    auto acc_full_bar = [&](uint32_t a) { return bar0 + 8u * (2 * C::STAGES + a); };
+    auto acc_empty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * C::STAGES + C::kAccs + a); };
+    const uint32_t mma_done_bar = bar0 + 8u * (2 * C::STAGES + 2 * C::kAccs);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    volatile uint32_t* ring_count = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
+    int32_t* start = reinterpret_cast<int32_t*>(smem + C::kOffStart);
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    const uint32_t rank = C::kPair ? cluster_ctarank() : 0u;
+    const int32_t unit0 = static_cast<int32_t>(blockIdx.x) / (C::kPair ? 2 : 1);
+    const int32_t unit_step = static_cast<int32_t>(gridDim.x) / (C::kPair ? 2 : 1);
+
+    grid_launch_dependents();
+
+    if (warp == 0) {
+        if (elect_one()) {
+            for (uint32_t s = 0; s < (uint32_t)C::STAGES; ++s) {
+                mbar_init(full_bar(s), 1);
+                mbar_init(empty_bar(s), 1);
+            }
+            for (uint32_t a = 0; a < (uint32_t)C::kAccs; ++a) {
+                mbar_init(acc_full_bar(a), 1);
+                // The leader's acc_empty collects the epilogue warps of both CTAs.
+                mbar_init(acc_empty_bar(a), (C::kPair ? 2 : 1) * C::kEpiWarps);
+            }
+            mbar_init(mma_done_bar, 1);
+            *abort_flag = 0;
+            if constexpr (kChecked) {
+                ring_count[0] = 0;
+                ring_count[1] = 0;
+            }
+            fence_mbarrier_init();
+            tma_prefetch_desc(&prob.tmA);
+            tma_prefetch_desc(&prob.tmB);
+            tma_prefetch_desc(&prob.tmD);
+        }
+        __syncwarp();
+    }
+    if (warp == 1) {
+        if constexpr (C::kPair) {
+            tmem_alloc_pair(smem_u32(tmem_holder), 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_holder), 512);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (C::kPair) cluster_sync_after_init();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    grid_dependency_wait();
+
+    int32_t num_units = prob.num_tiles;
+    if constexpr (C::kGrouped) {
+        // Tiles of each group, then their running sum by one warp.
+        for (int32_t g = static_cast<int32_t>(threadIdx.x); g < prob.groups; g += C::kThreads) {
+            const RowRange r = group_rows(prob, g);
+            start[g + 1] = (r.hi - r.lo + C::kTileM - 1) / C::kTileM * prob.grid_n;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int32_t carry = 0;
+            for (int32_t g0 = 0; g0 < prob.groups; g0 += 32) {
+                int32_t v = g0 + lane < prob.groups ? start[g0 + lane + 1] : 0;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+                    if (lane >= d) v += o;
+                }
+                if (g0 + lane < prob.groups) start[g0 + lane + 1] = carry + v;
+                carry += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (lane == 0) start[0] = 0;
+        }
+        __syncthreads();
+        num_units = start[prob.groups];
+    }
+
+    if (warp < 4) {
+        set_max_regs_dec<C::kRoleRegs>();
+    if (warp == 0) {
+        // ================= TMA producer =================
+        if (elect_one()) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int32_t u = unit0; ok && u < num_units; u += unit_step) {
+                const Fp8Unit t = unit_of<C>(prob, start, u);
+                // Boxes of A with at least one row, in this CTA and in all.
+                int32_t boxes = 1, all_boxes = C::kPair ? 2 : 1;
+                if constexpr (C::kGrouped) {
+                    constexpr int32_t kMost = C::BM / C::kABoxRows;
+                    auto count = [&](int32_t r) {
+                        const int32_t left = t.row_end - (t.row0 + r * C::BM);
+                        return min(max((left + C::kABoxRows - 1) / C::kABoxRows, 0), kMost);
+                    };
+                    boxes = count(static_cast<int32_t>(rank));
+                    all_boxes = C::kPair ? count(0) + count(1) : boxes;
+                }
+                const uint32_t bytes =
+                    static_cast<uint32_t>(all_boxes) * (C::kABoxRows * C::BK) +
+                    (C::kPair ? 2u : 1u) * C::kBBytes;
+                const int32_t a_row = t.row0 + static_cast<int32_t>(rank) * C::BM;
+                const int32_t b_row = t.n0 + static_cast<int32_t>(rank) * C::kBRows;
+                for (int32_t kb = 0; kb < prob.k_blocks; ++kb) {
+                    const uint32_t s = ring_stage(it, C::STAGES);
+                    const uint32_t ph = ring_phase(it, C::STAGES);
+                    if (!wait_or_abort(empty_bar(s), ph ^ 1u, abort_flag, err, kSiteProducerEmpty,
+                                       limit_ns) ||
+                        !check_ok(a_row >= 0 && b_row >= 0, err, kSiteCheckTma)) {
+                        *abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a_dst = sbase + s * C::kStageBytes;
+                    const uint32_t b_dst = a_dst + C::kABytes;
+                    if constexpr (C::kPair) {
+                        if (rank == 0) mbar_arrive_expect_tx(full_bar(s), bytes);
+                        const uint32_t bar = map_to_rank(full_bar(s), 0);
+                        for (int32_t i = 0; i < boxes; ++i)
+                            tma_load_2d_pair(a_dst + i * (C::kABoxRows * C::BK), &prob.tmA,
+                                             kb * C::BK, a_row + i * C::kABoxRows, bar);
+                        tma_load_3d_pair(b_dst, &prob.tmB, kb * C::BK, b_row, t.group, bar);
+                    } else {
+                        mbar_arrive_expect_tx(full_bar(s), bytes);
+                        for (int32_t i = 0; i < boxes; ++i)
+                            tma_load_2d(a_dst + i * (C::kABoxRows * C::BK), &prob.tmA, kb * C::BK,
+                                        a_row + i * C::kABoxRows, full_bar(s));
+                        tma_load_3d(b_dst, &prob.tmB, kb * C::BK, b_row, t.group, full_bar(s));
+                    }
+                    ++it;
+                }
+            }
+            if constexpr (kChecked) ring_count[0] = it;
+            // The last stages issued must have landed before shared memory is
+            // released (a pair: the leader's barriers count both CTAs' loads,
+            // and the peer stays until the final cluster barrier).
+            if (rank == 0) {
+                const uint32_t first = it > (uint32_t)C::STAGES ? it - C::STAGES : 0u;
+                for (uint32_t j = first; j < it; ++j)
+                    wait_bounded(full_bar(ring_stage(j, C::STAGES)), ring_phase(j, C::STAGES), err,
+                                 kSiteDrainFull, limit_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA issuer (the leader's, for a pair) =================
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t kIdesc = idesc_e4m3(C::kTileM, C::BN);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int32_t u = unit0; ok && u < num_units; u += unit_step) {
+                for (int32_t kb = 0; kb < prob.k_blocks; ++kb, ++it) {
+                    const uint32_t s = ring_stage(it, C::STAGES);
+                    const uint32_t a = ring_stage(it, C::kAccs);
+                    if (!wait_or_abort(acc_empty_bar(a), ring_phase(it, C::kAccs) ^ 1u, abort_flag,
+                                       err, kSiteMmaAccEmpty, limit_ns) ||
+                        !wait_or_abort(full_bar(s), ring_phase(it, C::STAGES), abort_flag, err,
+                                       kSiteMmaFull, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = sbase + s * C::kStageBytes;
+                    const uint32_t b_addr = a_addr + C::kABytes;
+                    const uint32_t d_tmem = tmem_base + a * C::BN;
+#pragma unroll
+                    for (int j = 0; j < C::BK / 32; ++j)
+                        mma_e4m3_ss<C::kPair>(d_tmem, umma_desc_sw128_kmajor(a_addr + 32u * j),
+                                              umma_desc_sw128_kmajor(b_addr + 32u * j), kIdesc,
+                                              j != 0 ? 1u : 0u);
+                    if constexpr (C::kPair) {
+                        mma_commit_pair(empty_bar(s), 0x3u);
+                        mma_commit_pair(acc_full_bar(a), 0x3u);
+                    } else {
+                        mma_commit(empty_bar(s));
+                        mma_commit(acc_full_bar(a));
+                    }
+                }
+            }
+            if constexpr (kChecked) ring_count[1] = it;
+            // All issued MMAs must finish before TMEM is released.
+            if constexpr (C::kPair)
+                mma_commit_pair(mma_done_bar, 0x1u);
+            else
+                mma_commit(mma_done_bar);
+            wait_bounded(mma_done_bar, 0, err, kSiteDrainMma, limit_ns);
+        }
+        __syncwarp();
+    }
+    } else {
+        set_max_regs_inc<C::kEpiRegs>();
+        // ================= scaling and epilogue (warps 4..11) =================
+        const uint32_t quarter = static_cast<uint32_t>(warp) & 3u;      // TMEM lane quarter
+        const uint32_t half = static_cast<uint32_t>(warp - 4) >> 2;     // column half
+        const uint32_t t_base = tmem_base + ((quarter * 32u) << 16) + half * C::kCols;
+        const uint32_t buf = sbase + C::kOffD +
+                             static_cast<uint32_t>(warp - 4) * (C::kBoxes * C::kBoxBytes);
+        uint32_t it = 0;
+        for (int32_t u = unit0; u < num_units; u += unit_step) {
+            const Fp8Unit t = unit_of<C>(prob, start, u);
+            // This warp's 32 rows and kCols columns of D.
+            const int32_t y = t.row0 + static_cast<int32_t>(rank * C::BM + quarter * 32u);
+            const int32_t x = t.n0 + static_cast<int32_t>(half) * C::kCols;
+            const bool row_ok = y + lane < t.row_end;
+            const float* sa = prob.sa + (row_ok ? (y + lane) * prob.sa_row : 0);
+            const int32_t nb = min(x / kFp8Block, prob.n_blocks - 1);
+            const float* sb = prob.sb + (static_cast<int64_t>(t.group) * prob.n_blocks + nb) *
+                                            prob.k_blocks;
+            float2 acc[C::kCols / 2];
+#pragma unroll
+            for (int i = 0; i < C::kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            // Scales are read four k-blocks ahead of their use.
+            float sa_next[4], sb_next[4];
+            auto fetch = [&](int j, int32_t kb) {
+                const bool in = kb < prob.k_blocks;
+                sa_next[j] = in && row_ok ? sa[kb * prob.sa_blk] : 0.0f;
+                sb_next[j] = in ? sb[kb] : 0.0f;
+            };
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fetch(j, j);
+            bool ok = true;
+            for (int32_t kb0 = 0; ok && kb0 < prob.k_blocks; kb0 += 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!ok || kb0 + j >= prob.k_blocks) break;
+                    const float s = sa_next[j] * sb_next[j];
+                    fetch(j, kb0 + j + 4);
+                    const uint32_t a = ring_stage(it, C::kAccs);
+                    ok = __all_sync(0xffffffffu,
+                                    wait_or_abort(acc_full_bar(a), ring_phase(it, C::kAccs),
+                                                  abort_flag, err, kSiteEpiAccFull, limit_ns));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t t_acc = t_base + a * C::BN;
+#pragma unroll
+                    for (int c = 0; c < C::kCols / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(t_acc + 32 * c, v);
+                        tmem_ld_wait_regs(v);
+                        if (c == C::kCols / 32 - 1) {
+                            // All read: the accumulator goes back to the MMA warp.
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if constexpr (C::kPair)
+                                    mbar_arrive_cluster(map_to_rank(acc_empty_bar(a), 0));
+                                else
+                                    mbar_arrive(acc_empty_bar(a));
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            fma2(acc[16 * c + i], v[2 * i], v[2 * i + 1], s);
+                    }
+                    ++it;
+                }
+            }
+            if (!ok) break;
+            // ---- round, stage in shared memory, store ----
+            if (lane == 0) bulk_wait_group_read<0>();   // the last tile's stores have left
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < C::kCols / 8; ++c) {
+                // Chunk c % 8 (8 columns, 16 bytes) of box c / 8; the 128-byte
+                // swizzle XORs the chunk with the row's low three bits.
+                const uint32_t at = buf + (c / 8) * C::kBoxBytes +
+                                    static_cast<uint32_t>(lane) * 128u +
+                                    (((c % 8) ^ (static_cast<uint32_t>(lane) & 7u)) << 4);
+                uint32_t p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    p[i] = pack2_rn<C::kBF16>(__float_as_uint(acc[4 * c + i].x),
+                                              __float_as_uint(acc[4 * c + i].y));
+                st_shared_v4(at, p[0], p[1], p[2], p[3]);
+            }
+            const int32_t left = t.row_end - y;   // rows of this warp that exist
+            const bool whole = !C::kGrouped || left >= 32;
+            if (whole) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && left > 0) {
+#pragma unroll
+                    for (int b = 0; b < C::kBoxes; ++b)
+                        if (x + 64 * b < prob.N &&
+                            check_ok((x & 7) == 0 && x >= 0 && y >= 0, err, kSiteCheckTma))
+                            tma_store_2d(&prob.tmD, buf + b * C::kBoxBytes, x + 64 * b, y);
+                    bulk_commit_group();
+                }
+            } else {
+                // The group ends inside these 32 rows: plain stores of the rows
+                // that exist, eight lanes a row (the next rows are another
+                // group's).
+                __syncwarp();
+                const int32_t chunk = lane & 7;
+                for (int32_t r = lane >> 3; r < left; r += 4) {
+#pragma unroll
+                    for (int b = 0; b < C::kBoxes; ++b) {
+                        const int32_t col = x + 64 * b + 8 * chunk;
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            smem + (buf - sbase) + b * C::kBoxBytes + r * 128 +
+                            ((chunk ^ (r & 7)) << 4));
+                        if (col < prob.N &&
+                            check_ok(y + r < prob.rows && col + 8 <= prob.N, err,
+                                     kSiteCheckBounds))
+                            *reinterpret_cast<uint4*>(
+                                prob.d + static_cast<int64_t>(y + r) * prob.N + col) = v;
+                    }
+                }
+                __syncwarp();
+            }
+            if (warp == 4 && lane == 0 && rank == 0) check_count_unit(err, u);
+        }
+        if (lane == 0) bulk_wait_group<0>();
+    }
+
+    // ---- teardown ----
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (kChecked) {
+        if (threadIdx.x == 0 && rank == 0 && !*abort_flag)
+            check_ok(ring_count[0] == ring_count[1], err, kSiteCheckRing);
+    }
+    if constexpr (C::kPair) cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (C::kPair)
+            tmem_dealloc_pair(tmem_base, 512);
+        else
+            tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// The tiles: 256 x 256 in CTA pairs for problems that fill the GPU with them,
+// 128 x 128 otherwise.
+template <bool G, bool T> using FpPair = Fp8Cfg<256, 5, true, G, T>;
+template <bool G, bool T> using FpTile = Fp8Cfg<128, 6, false, G, T>;
+
+int encode_fp8(EncodeTiled encode, CUtensorMap* map, CUtensorMapDataType type, int elem_bytes,
+               const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1) {
+    cuuint64_t dims[3] = {d0, d1, d2};
+    cuuint64_t strides[2] = {d0 * elem_bytes, d0 * d1 * elem_bytes};
+    cuuint32_t box[3] = {b0, b1, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const bool store = elem_bytes == 2;
+    return encode(map, type, d2 == 0 ? 2 : 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  store ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? 0
+               : -1;
+}
+
+template <class C>
+cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
+    Fp8Problem p;
+    const int64_t G = C::kGrouped ? g.groups : 1;
+    if (encode_fp8(dev.encode, &p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.A, g.K, g.M, 0, C::BK,
+                   C::kABoxRows) ||
+        encode_fp8(dev.encode, &p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.B, g.K, g.N, G, C::BK,
+                   C::kBRows) ||
+        encode_fp8(dev.encode, &p.tmD,
+                   C::kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   2, g.D, g.N, g.M, 0, 64, 32))
+        return cudaErrorInvalidValue;
+    p.sa = g.SA;
+    p.sa_row = g.sa_row;
+    p.sa_blk = g.sa_blk;
+    p.sb = g.SB;
+    p.d = static_cast<uint16_t*>(g.D);
+    p.offsets = g.offsets;
+    p.rows = static_cast<int32_t>(g.M);
+    p.N = static_cast<int32_t>(g.N);
+    p.k_blocks = static_cast<int32_t>(ceil_div(g.K, C::BK));
+    p.n_blocks = static_cast<int32_t>(ceil_div(g.N, kFp8Block));
+    p.groups = static_cast<int32_t>(G);
+    p.grid_n = static_cast<int32_t>(ceil_div(g.N, C::BN));
+    p.group_m = 8;
+    const int64_t grid_m = ceil_div(g.M, C::kTileM);
+    // Grouped: the most tiles the groups can have (each adds at most one
+    // partly filled row of tiles); the real number is read on the device.
+    int64_t tiles = grid_m * p.grid_n;
+    if (C::kGrouped) tiles = (g.M / C::kTileM + (G < g.M ? G : g.M)) * p.grid_n;
+    p.num_tiles = static_cast<int32_t>(tiles);
+    const int64_t slots = C::kPair ? dev.pairs : dev.sms;
+    const int64_t ctas = (tiles < slots ? tiles : slots) * (C::kPair ? 2 : 1);
+    static ContextMarks attr_done;
+    auto kernel = gemm_fp8_kernel<C>;
+    if (cudaError_t e = smem_opt_in(kernel, static_cast<int>(C::kSmemBytes), attr_done)) return e;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)), dim3(C::kThreads),
+                         C::kSmemBytes, stream, C::kPair ? 2 : 1, dev.pdl, p, dev.limit_ns,
+                         dev.err_word);
+}
+
+template <bool T>
+cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
+    if (g.offsets) {
+        // Whole 256-row tiles pay when the groups fill most of them.
+        if (dev.pairs > 0 && g.M >= 192 * g.groups)
+            return launch_cfg<FpPair<true, T>>(g, dev, stream);
+        return launch_cfg<FpTile<true, T>>(g, dev, stream);
+    }
+    const int64_t pair_tiles = ceil_div(g.M, 256) * ceil_div(g.N, 256);
+    if (dev.pairs > 0 && 2 * pair_tiles > dev.pairs)
+        return launch_cfg<FpPair<false, T>>(g, dev, stream);
+    return launch_cfg<FpTile<false, T>>(g, dev, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
+    return g.bf16 ? launch_typed<true>(g, dev, stream) : launch_typed<false>(g, dev, stream);
+}
+
+}  // namespace tmagemm

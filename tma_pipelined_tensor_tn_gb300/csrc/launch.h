@@ -178,6 +178,69 @@ cudaError_t launch_grouped(const GroupedLaunch& g, int num_sms, int num_pairs, c
 cudaError_t launch_gemv(int64_t N, int64_t K, const void* x, const void* W, void* y, bool bf16,
                         int num_sms, cudaStream_t stream, uint32_t* err, bool pdl);
 
+// Block quantisation to e4m3 (quantize.cu): X (M x K) -> codes Q and scales
+// S[row * s_row + block * s_blk], one per block_rows (1 or 128) x 128 values.
+cudaError_t launch_quantize(int64_t M, int64_t K, const void* X, bool bf16, int block_rows,
+                            void* Q, float* S, int64_t s_row, int64_t s_blk, bool pdl,
+                            cudaStream_t stream);
+
+// Block-scaled e4m3 product (gemm_fp8.cu).  offsets != nullptr: grouped, with
+// the row offsets of `groups` groups in device memory; B and SB then hold
+// `groups` weight matrices back to back.
+constexpr int kMaxFp8Groups = 384;
+struct Fp8Gemm {
+    int64_t M, N, K, groups;
+    const void* A;
+    const float* SA;            // scale of row m, block b: SA[m * sa_row + b * sa_blk]
+    int64_t sa_row, sa_blk;
+    const void* B;
+    const float* SB;            // [groups][ceil(N / 128)][ceil(K / 128)]
+    void* D;
+    const int32_t* offsets;
+    bool bf16;
+};
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+struct Fp8Device {
+    EncodeTiled encode;
+    int sms, pairs;
+    uint64_t limit_ns;
+    uint32_t* err_word;
+    bool pdl;
+};
+cudaError_t launch_gemm_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
+
+// Norms around a block fused with its gate and residual scale, and their
+// gradients (norm.cu).  Rows of C = 8 C8 channels; NULL leaves a part out.
+enum GateMode : int { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateElement = 3 };
+struct NormArgs {
+    int64_t T;
+    int32_t C8;
+    int gate_mode;
+    float alpha, eps;
+    const uint4 *h, *y, *w_post, *w_pre;
+    const void* gate;
+    float *rstd_post, *rstd_pre;   // written by the forward (may be NULL), read by the backward
+    // forward
+    uint4 *h_out, *x;              // x == NULL with w_pre: codes q and scales instead
+    uint2* q;
+    float* scales;
+    int64_t s_row, s_blk;
+    // backward
+    const uint4 *dh, *dx;          // gradients of h' (may be NULL) and x
+    uint4 *dh_in, *dy;             // gradients of h and y
+    void* dgate;
+    float *dw_post, *dw_pre;
+    float* partial;                // norm_backward_ctas x 2 x C
+};
+int norm_backward_ctas(int64_t T, int sms);
+cudaError_t launch_norm_forward(const NormArgs& p, bool bf16, int sms, bool pdl,
+                                cudaStream_t stream);
+cudaError_t launch_norm_backward(const NormArgs& p, bool bf16, int sms, bool pdl,
+                                 cudaStream_t stream);
+
 // cudaLaunchKernelEx with a cluster of `cluster_x` CTAs along x (1 = none)
 // and, when `pdl` is set, the programmatic-stream-serialization attribute
 // (programmatic dependent launch): the next kernel on the stream is scheduled
