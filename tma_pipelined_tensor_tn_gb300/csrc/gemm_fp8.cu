@@ -12,7 +12,7 @@
 // Roles (one CTA per SM, three groups of four warps):
 //   warp 0      TMA producer: A and B k-blocks (128 bytes a row, 128B swizzle)
 //               into a ring of stages;
-//   warp 1      MMA issuer: per k-block four tcgen05.mma.kind::f8f6f4 into
+//   warps 1, 2  MMA issuers, one per 128-column part of the tile: per k-block four tcgen05.mma.kind::f8f6f4 into
 //               TMEM accumulator it % kAccs, then commits onto the stage's
 //               `empty` barrier and the accumulator's `acc_full` barrier;
 //   warps 4..11 scaling and epilogue: two warps per 32 rows, each half of the
@@ -46,21 +46,30 @@ namespace tmagemm {
 
 namespace {
 
-template <int BN_, int STAGES_, bool PAIR_, bool GROUPED_, bool BF16_>
+template <int BN_, int COLS_, int STAGES_, bool PAIR_, bool GROUPED_, bool BF16_>
 struct Fp8Cfg {
     static constexpr int BM = 128, BN = BN_, BK = kFp8Block, STAGES = STAGES_;
     static constexpr bool kPair = PAIR_, kGrouped = GROUPED_, kBF16 = BF16_;
     static constexpr int kTileM = PAIR_ ? 256 : 128;
-    static constexpr int kBRows = PAIR_ ? BN_ / 2 : BN_;   // rows of B in this CTA
-    static constexpr int kEpiWarps = 8;
+    // Rows of B in this CTA; a pair's CTAs each hold half of every part.
+    static constexpr int kBRows = PAIR_ ? BN_ / 2 : BN_;
+    static constexpr int kBBoxRows = PAIR_ ? 64 : BN_;
+    // A k-block's product is made in parts of 128 columns, each in a TMEM
+    // accumulator of its own (four of them): the MMAs of one part run while
+    // the parts before it are scaled.
+    static constexpr int kAccCols = 128, kAccs = 4, kParts = BN_ / kAccCols;
+    static constexpr int kCols = COLS_;                    // columns of one epilogue warp
+    static constexpr int kEpiWarps = 4 * BN_ / kCols;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
-    // Registers: 384 threads x 168 at launch; 128 x 56 + 256 x 224 afterwards,
-    // the same 64512.
-    static constexpr int kRoleRegs = 56, kEpiRegs = 224;
-    static_assert(128 * kRoleRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * 168,
+    // 32-column TMEM loads a warp has in flight.
+    static constexpr int kBatch = 2;
+    // Registers: the role warps give up what the epilogue warps take.
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kRoleRegs = 56;
+    static constexpr int kEpiRegs =
+        (kThreads * kLaunchRegs - 128 * kRoleRegs) / (32 * kEpiWarps) / 8 * 8;
+    static_assert(128 * kRoleRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * kLaunchRegs,
                   "the shares fit what the block was launched with");
-    static constexpr int kCols = BN_ / 2;                  // columns of one epilogue warp
-    static constexpr int kAccs = 512 / BN_;                // TMEM accumulators
     // A comes in boxes of 32 rows for grouped problems, where a tile may have
     // few rows (a box without any is not loaded), else in one of 128.
     static constexpr int kABoxRows = GROUPED_ ? 32 : 128;
@@ -73,13 +82,13 @@ struct Fp8Cfg {
     static constexpr int kBoxes = kCols / 64;
     static constexpr uint32_t kOffD = STAGES * kStageBytes;
     static constexpr uint32_t kOffBar = kOffD + kEpiWarps * kBoxes * kBoxBytes;
-    static constexpr uint32_t kNumBars = 2 * STAGES + 2 * kAccs + 1;
+    static constexpr uint32_t kNumBars = 2 * STAGES + 2 * kAccs + kParts;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr uint32_t kOffStart = kOffMisc + 16;   // grouped: tile starts
+    static constexpr uint32_t kOffStart = kOffMisc + 32;   // grouped: tile starts
     static constexpr uint32_t kSmemBytes =
         kOffStart + (GROUPED_ ? (kMaxFp8Groups + 1) * 4 : 0) + 1024;
     static_assert(kSmemBytes <= 232448, "fits the 227 KB opt-in shared memory");
-    static_assert(kCols % 64 == 0 && BN <= 256, "whole store boxes");
+    static_assert((BN == 128 || BN == 256) && (kCols == 64 || kCols == 128), "parts and boxes");
 };
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 operands and FP32 sums
@@ -108,28 +117,25 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
             : "memory");
 }
 
-// acc (two floats) += t (two accumulator words) * s.
-__device__ __forceinline__ void fma2(float2& acc, uint32_t t0, uint32_t t1, float s) {
-    uint64_t a, t, ss;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc.x), "f"(acc.y));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "r"(t0), "r"(t1));
-    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(t), "l"(ss));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(acc.x), "=f"(acc.y) : "l"(a));
+// acc += t * s, with t from TMEM.  Volatile, so that it stays behind the wait
+// for the load that brought t.  (Multiply-adds of packed pairs are half as
+// many instructions for the same cycles, but each loaded register is then
+// copied to form its pair.)
+__device__ __forceinline__ void scale_add(float& acc, uint32_t t, float s) {
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(t)), "f"(s));
 }
 
-// Waits for this thread's TMEM loads and ties the loaded registers to the
-// wait, so that no use of them can be moved before it.
-__device__ __forceinline__ void tmem_ld_wait_regs(uint32_t (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
-                   "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
-                   "+r"(v[30]), "+r"(v[31])
-                 :
-                 : "memory");
+// One arrival on an mbarrier at a shared::cluster address by the threads whose
+// `p` is not 0; predicated rather than branched around, and relaxed (what it
+// hands over is a TMEM accumulator that has been read, behind a tcgen05 fence;
+// a release would wait for the loads of later scales in flight).
+__device__ __forceinline__ void mbar_arrive_if(uint32_t p, uint32_t cluster_addr) {
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "setp.ne.u32 P, %0, 0;\n\t"
+        "@P mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%1];\n\t}"
+        ::"r"(p), "r"(cluster_addr)
+        : "memory");
 }
 
 // Registers of this warp's group of four, lowered or raised within what the
@@ -145,7 +151,7 @@ __device__ __forceinline__ void set_max_regs_inc() {
 
 struct Fp8Problem {
     CUtensorMap tmA;   // A {K, rows}, box {128, kABoxRows}
-    CUtensorMap tmB;   // B {K, N, G}, box {128, kBRows, 1}
+    CUtensorMap tmB;   // B {K, N, G}, box {128, kBBoxRows, 1}
     CUtensorMap tmD;   // D {N, rows}, box {64, 32}
     const float* sa;   // scale of row m, block b: sa[m * sa_row + b * sa_blk]
     int64_t sa_row, sa_blk;
@@ -214,7 +220,9 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
     auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (C::STAGES + s); };
     auto acc_full_bar = [&](uint32_t a) { return bar0 + 8u * (2 * C::STAGES + a); };
     auto acc_empty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * C::STAGES + C::kAccs + a); };
-    const uint32_t mma_done_bar = bar0 + 8u * (2 * C::STAGES + 2 * C::kAccs);
+    auto mma_done_bar = [&](uint32_t h) {
+        return bar0 + 8u * (2 * C::STAGES + 2 * C::kAccs + h);
+    };
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     volatile uint32_t* ring_count = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc + 8);
@@ -232,18 +240,17 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         if (elect_one()) {
             for (uint32_t s = 0; s < (uint32_t)C::STAGES; ++s) {
                 mbar_init(full_bar(s), 1);
-                mbar_init(empty_bar(s), 1);
+                mbar_init(empty_bar(s), C::kParts);   // one commit per MMA issuer
             }
             for (uint32_t a = 0; a < (uint32_t)C::kAccs; ++a) {
                 mbar_init(acc_full_bar(a), 1);
                 // The leader's acc_empty collects the epilogue warps of both CTAs.
-                mbar_init(acc_empty_bar(a), (C::kPair ? 2 : 1) * C::kEpiWarps);
+                mbar_init(acc_empty_bar(a), (C::kPair ? 2 : 1) * (C::kEpiWarps / C::kParts));
             }
-            mbar_init(mma_done_bar, 1);
+            for (uint32_t h = 0; h < (uint32_t)C::kParts; ++h) mbar_init(mma_done_bar(h), 1);
             *abort_flag = 0;
             if constexpr (kChecked) {
-                ring_count[0] = 0;
-                ring_count[1] = 0;
+                for (int i = 0; i <= C::kParts; ++i) ring_count[i] = 0;
             }
             fence_mbarrier_init();
             tma_prefetch_desc(&prob.tmA);
@@ -318,11 +325,11 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                     static_cast<uint32_t>(all_boxes) * (C::kABoxRows * C::BK) +
                     (C::kPair ? 2u : 1u) * C::kBBytes;
                 const int32_t a_row = t.row0 + static_cast<int32_t>(rank) * C::BM;
-                const int32_t b_row = t.n0 + static_cast<int32_t>(rank) * C::kBRows;
+                const int32_t b_row = t.n0 + static_cast<int32_t>(rank) * C::kBBoxRows;
                 for (int32_t kb = 0; kb < prob.k_blocks; ++kb) {
                     const uint32_t s = ring_stage(it, C::STAGES);
                     const uint32_t ph = ring_phase(it, C::STAGES);
-                    if (!wait_or_abort(empty_bar(s), ph ^ 1u, abort_flag, err, kSiteProducerEmpty,
+                    if (!wait_many(empty_bar(s), ph ^ 1u, abort_flag, err, kSiteProducerEmpty,
                                        limit_ns) ||
                         !check_ok(a_row >= 0 && b_row >= 0, err, kSiteCheckTma)) {
                         *abort_flag = 1;
@@ -337,7 +344,10 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                         for (int32_t i = 0; i < boxes; ++i)
                             tma_load_2d_pair(a_dst + i * (C::kABoxRows * C::BK), &prob.tmA,
                                              kb * C::BK, a_row + i * C::kABoxRows, bar);
-                        tma_load_3d_pair(b_dst, &prob.tmB, kb * C::BK, b_row, t.group, bar);
+#pragma unroll
+                        for (int h = 0; h < C::kParts; ++h)
+                            tma_load_3d_pair(b_dst + h * (C::kBBoxRows * C::BK), &prob.tmB,
+                                             kb * C::BK, b_row + h * C::kAccCols, t.group, bar);
                     } else {
                         mbar_arrive_expect_tx(full_bar(s), bytes);
                         for (int32_t i = 0; i < boxes; ++i)
@@ -360,48 +370,57 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
-        // ================= MMA issuer (the leader's, for a pair) =================
+    } else if (warp <= C::kParts) {
+        // ===== MMA issuers (the leader's, for a pair): warp 1 + h part h =====
         if (rank == 0 && elect_one()) {
-            constexpr uint32_t kIdesc = idesc_e4m3(C::kTileM, C::BN);
+            constexpr uint32_t kIdesc = idesc_e4m3(C::kTileM, C::kAccCols);
+            // B rows (in this CTA) of one part.
+            constexpr uint32_t kPartBytes = (C::kBRows / C::kParts) * C::BK;
+            const uint32_t h = static_cast<uint32_t>(warp - 1);
             uint32_t it = 0;
             bool ok = true;
             for (int32_t u = unit0; ok && u < num_units; u += unit_step) {
                 for (int32_t kb = 0; kb < prob.k_blocks; ++kb, ++it) {
                     const uint32_t s = ring_stage(it, C::STAGES);
-                    const uint32_t a = ring_stage(it, C::kAccs);
-                    if (!wait_or_abort(acc_empty_bar(a), ring_phase(it, C::kAccs) ^ 1u, abort_flag,
-                                       err, kSiteMmaAccEmpty, limit_ns) ||
-                        !wait_or_abort(full_bar(s), ring_phase(it, C::STAGES), abort_flag, err,
-                                       kSiteMmaFull, limit_ns)) {
+                    const uint32_t part = it * C::kParts + h;
+                    const uint32_t a = ring_stage(part, C::kAccs);
+                    if (!wait_many(full_bar(s), ring_phase(it, C::STAGES), abort_flag, err,
+                                        kSiteMmaFull, limit_ns) ||
+                        !wait_many(acc_empty_bar(a), ring_phase(part, C::kAccs) ^ 1u,
+                                        abort_flag, err, kSiteMmaAccEmpty, limit_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t a_addr = sbase + s * C::kStageBytes;
-                    const uint32_t b_addr = a_addr + C::kABytes;
-                    const uint32_t d_tmem = tmem_base + a * C::BN;
+                    const uint64_t a_desc = umma_desc_sw128_kmajor(a_addr);
+                    const uint64_t b_desc =
+                        umma_desc_sw128_kmajor(a_addr + C::kABytes + h * kPartBytes);
+                    const uint32_t d_tmem = tmem_base + a * C::kAccCols;
+                    // Each step of 32 k is 32 bytes further along the rows (the
+                    // descriptors' address field counts 16 bytes).
 #pragma unroll
                     for (int j = 0; j < C::BK / 32; ++j)
-                        mma_e4m3_ss<C::kPair>(d_tmem, umma_desc_sw128_kmajor(a_addr + 32u * j),
-                                              umma_desc_sw128_kmajor(b_addr + 32u * j), kIdesc,
+                        mma_e4m3_ss<C::kPair>(d_tmem, a_desc + 2 * j, b_desc + 2 * j, kIdesc,
                                               j != 0 ? 1u : 0u);
+                    // The accumulator is full, and this part done with stage s
+                    // (in both CTAs of a pair), once these MMAs finish.
                     if constexpr (C::kPair) {
-                        mma_commit_pair(empty_bar(s), 0x3u);
                         mma_commit_pair(acc_full_bar(a), 0x3u);
+                        mma_commit_pair(empty_bar(s), 0x3u);
                     } else {
-                        mma_commit(empty_bar(s));
                         mma_commit(acc_full_bar(a));
+                        mma_commit(empty_bar(s));
                     }
                 }
             }
-            if constexpr (kChecked) ring_count[1] = it;
+            if constexpr (kChecked) ring_count[1 + h] = it;
             // All issued MMAs must finish before TMEM is released.
             if constexpr (C::kPair)
-                mma_commit_pair(mma_done_bar, 0x1u);
+                mma_commit_pair(mma_done_bar(h), 0x1u);
             else
-                mma_commit(mma_done_bar);
-            wait_bounded(mma_done_bar, 0, err, kSiteDrainMma, limit_ns);
+                mma_commit(mma_done_bar(h));
+            wait_bounded(mma_done_bar(h), 0, err, kSiteDrainMma, limit_ns);
         }
         __syncwarp();
     }
@@ -409,71 +428,106 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         set_max_regs_inc<C::kEpiRegs>();
         // ================= scaling and epilogue (warps 4..11) =================
         const uint32_t quarter = static_cast<uint32_t>(warp) & 3u;      // TMEM lane quarter
-        const uint32_t half = static_cast<uint32_t>(warp - 4) >> 2;     // column half
-        const uint32_t t_base = tmem_base + ((quarter * 32u) << 16) + half * C::kCols;
+        // Columns [kCols * group, + kCols) of the tile: part h, from column c0 of
+        // its accumulator.
+        const uint32_t col = (static_cast<uint32_t>(warp - 4) >> 2) * C::kCols;
+        const uint32_t h = col / C::kAccCols;
+        const uint32_t t_base = tmem_base + ((quarter * 32u) << 16) + col % C::kAccCols;
         const uint32_t buf = sbase + C::kOffD +
                              static_cast<uint32_t>(warp - 4) * (C::kBoxes * C::kBoxBytes);
-        uint32_t it = 0;
+        // The accumulator of this warp's next part: parts h, h + kParts, ... of
+        // the running count go round the kAccs accumulators.
+        uint32_t slot = h, parity = 0;
+        uint32_t full_at = acc_full_bar(h), t_acc = t_base + h * C::kAccCols;
+        const uint32_t empty0 = C::kPair ? map_to_rank(acc_empty_bar(0), 0) : acc_empty_bar(0);
+        uint32_t empty_at = empty0 + 8u * h;
+        auto next_acc = [&]() {
+            slot += C::kParts;
+            if (slot >= static_cast<uint32_t>(C::kAccs)) {
+                slot = h;
+                parity ^= 1u;
+            }
+            full_at = acc_full_bar(slot);
+            empty_at = empty0 + 8u * slot;
+            t_acc = t_base + slot * C::kAccCols;
+        };
         for (int32_t u = unit0; u < num_units; u += unit_step) {
             const Fp8Unit t = unit_of<C>(prob, start, u);
             // This warp's 32 rows and kCols columns of D.
             const int32_t y = t.row0 + static_cast<int32_t>(rank * C::BM + quarter * 32u);
-            const int32_t x = t.n0 + static_cast<int32_t>(half) * C::kCols;
-            const bool row_ok = y + lane < t.row_end;
-            const float* sa = prob.sa + (row_ok ? (y + lane) * prob.sa_row : 0);
+            const int32_t x = t.n0 + static_cast<int32_t>(col);
+            const int32_t last = prob.k_blocks - 1;
+            if (y >= t.row_end) {
+                // No row of this warp exists: it only hands the accumulators back.
+                for (int32_t kb = 0; kb <= last; ++kb) {
+                    if (!__all_sync(0xffffffffu,
+                                    wait_many(full_at, parity, abort_flag, err,
+                                                   kSiteEpiAccFull, limit_ns)))
+                        goto stop;
+                    mbar_arrive_if(lane == 0, empty_at);
+                    next_acc();
+                }
+                continue;
+            }
+            // Scales: the row's for four k-blocks at a time, read while the four
+            // before them are used (loads issued one by one as they are used
+            // would make every use wait for the newest: a warp waits for all
+            // loads it has in flight), and the weights' for 32, one per lane.
+            // Lanes past the last row read that row's (their sums are not
+            // stored), and blocks past the last read the last.
+            const float* sa = prob.sa + min(y + lane, t.row_end - 1) * prob.sa_row;
             const int32_t nb = min(x / kFp8Block, prob.n_blocks - 1);
             const float* sb = prob.sb + (static_cast<int64_t>(t.group) * prob.n_blocks + nb) *
                                             prob.k_blocks;
-            float2 acc[C::kCols / 2];
+            float sa_next[4], sb_lane = 0.0f, sb_next = sb[min(lane, last)];
+            auto fetch = [&](int32_t kb0) {
 #pragma unroll
-            for (int i = 0; i < C::kCols / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            // Scales are read four k-blocks ahead of their use.
-            float sa_next[4], sb_next[4];
-            auto fetch = [&](int j, int32_t kb) {
-                const bool in = kb < prob.k_blocks;
-                sa_next[j] = in && row_ok ? sa[kb * prob.sa_blk] : 0.0f;
-                sb_next[j] = in ? sb[kb] : 0.0f;
+                for (int j = 0; j < 4; ++j) sa_next[j] = sa[min(kb0 + j, last) * prob.sa_blk];
             };
+            fetch(0);
+            float acc[C::kCols];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fetch(j, j);
-            bool ok = true;
-            for (int32_t kb0 = 0; ok && kb0 < prob.k_blocks; kb0 += 4) {
+            for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
+            for (int32_t kb0 = 0; kb0 <= last; kb0 += 4) {
+                if ((kb0 & 31) == 0) sb_lane = sb_next;
+                float scales[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    scales[j] = sa_next[j] *
+                                __shfl_sync(0xffffffffu, sb_lane, (kb0 & 31) + j);
+                fetch(kb0 + 4);
+                if ((kb0 & 31) == 0) sb_next = sb[min(kb0 + 32 + lane, last)];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (!ok || kb0 + j >= prob.k_blocks) break;
-                    const float s = sa_next[j] * sb_next[j];
-                    fetch(j, kb0 + j + 4);
-                    const uint32_t a = ring_stage(it, C::kAccs);
-                    ok = __all_sync(0xffffffffu,
-                                    wait_or_abort(acc_full_bar(a), ring_phase(it, C::kAccs),
-                                                  abort_flag, err, kSiteEpiAccFull, limit_ns));
-                    if (!ok) break;
+                    if (kb0 + j > last) break;
+                    const float scale = scales[j];
+                    if (!__all_sync(0xffffffffu,
+                                    wait_many(full_at, parity, abort_flag, err,
+                                                   kSiteEpiAccFull, limit_ns)))
+                        goto stop;
                     tc_fence_after();
-                    const uint32_t t_acc = t_base + a * C::BN;
 #pragma unroll
-                    for (int c = 0; c < C::kCols / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(t_acc + 32 * c, v);
-                        tmem_ld_wait_regs(v);
-                        if (c == C::kCols / 32 - 1) {
-                            // All read: the accumulator goes back to the MMA warp.
+                    for (int c = 0; c < C::kCols; c += 32 * C::kBatch) {
+                        uint32_t v[C::kBatch][32];
+#pragma unroll
+                        for (int b = 0; b < C::kBatch; ++b)
+                            tmem_ld_32x32b_x32(t_acc + c + 32 * b, v[b]);
+                        tmem_ld_wait();
+                        if (c + 32 * C::kBatch == C::kCols) {
+                            // All read (by every lane: the wait is collective):
+                            // the accumulator goes back to the MMA warp.
                             tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if constexpr (C::kPair)
-                                    mbar_arrive_cluster(map_to_rank(acc_empty_bar(a), 0));
-                                else
-                                    mbar_arrive(acc_empty_bar(a));
-                            }
+                            mbar_arrive_if(lane == 0, empty_at);
                         }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            fma2(acc[16 * c + i], v[2 * i], v[2 * i + 1], s);
+                        for (int b = 0; b < C::kBatch; ++b)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                scale_add(acc[c + 32 * b + i], v[b][i], scale);
                     }
-                    ++it;
+                    next_acc();
                 }
             }
-            if (!ok) break;
             // ---- round, stage in shared memory, store ----
             if (lane == 0) bulk_wait_group_read<0>();   // the last tile's stores have left
             __syncwarp();
@@ -487,8 +541,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                 uint32_t p[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    p[i] = pack2_rn<C::kBF16>(__float_as_uint(acc[4 * c + i].x),
-                                              __float_as_uint(acc[4 * c + i].y));
+                    p[i] = pack2_rn<C::kBF16>(__float_as_uint(acc[8 * c + 2 * i]),
+                                              __float_as_uint(acc[8 * c + 2 * i + 1]));
                 st_shared_v4(at, p[0], p[1], p[2], p[3]);
             }
             const int32_t left = t.row_end - y;   // rows of this warp that exist
@@ -513,21 +567,21 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                 for (int32_t r = lane >> 3; r < left; r += 4) {
 #pragma unroll
                     for (int b = 0; b < C::kBoxes; ++b) {
-                        const int32_t col = x + 64 * b + 8 * chunk;
+                        const int32_t n = x + 64 * b + 8 * chunk;
                         const uint4 v = *reinterpret_cast<const uint4*>(
                             smem + (buf - sbase) + b * C::kBoxBytes + r * 128 +
                             ((chunk ^ (r & 7)) << 4));
-                        if (col < prob.N &&
-                            check_ok(y + r < prob.rows && col + 8 <= prob.N, err,
-                                     kSiteCheckBounds))
+                        if (n < prob.N && check_ok(y + r < prob.rows && n + 8 <= prob.N, err,
+                                                   kSiteCheckBounds))
                             *reinterpret_cast<uint4*>(
-                                prob.d + static_cast<int64_t>(y + r) * prob.N + col) = v;
+                                prob.d + static_cast<int64_t>(y + r) * prob.N + n) = v;
                     }
                 }
                 __syncwarp();
             }
             if (warp == 4 && lane == 0 && rank == 0) check_count_unit(err, u);
         }
+    stop:
         if (lane == 0) bulk_wait_group<0>();
     }
 
@@ -536,7 +590,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
     __syncthreads();
     if constexpr (kChecked) {
         if (threadIdx.x == 0 && rank == 0 && !*abort_flag)
-            check_ok(ring_count[0] == ring_count[1], err, kSiteCheckRing);
+            for (int h = 0; h < C::kParts; ++h)
+                check_ok(ring_count[0] == ring_count[1 + h], err, kSiteCheckRing);
     }
     if constexpr (C::kPair) cluster_sync();
     if (warp == 1) {
@@ -550,8 +605,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
 
 // The tiles: 256 x 256 in CTA pairs for problems that fill the GPU with them,
 // 128 x 128 otherwise.
-template <bool G, bool T> using FpPair = Fp8Cfg<256, 5, true, G, T>;
-template <bool G, bool T> using FpTile = Fp8Cfg<128, 6, false, G, T>;
+template <bool G, bool T> using FpPair = Fp8Cfg<256, 128, 5, true, G, T>;
+template <bool G, bool T> using FpTile = Fp8Cfg<128, 64, 6, false, G, T>;
 
 int encode_fp8(EncodeTiled encode, CUtensorMap* map, CUtensorMapDataType type, int elem_bytes,
                const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1) {
@@ -575,7 +630,7 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
     if (encode_fp8(dev.encode, &p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.A, g.K, g.M, 0, C::BK,
                    C::kABoxRows) ||
         encode_fp8(dev.encode, &p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.B, g.K, g.N, G, C::BK,
-                   C::kBRows) ||
+                   C::kBBoxRows) ||
         encode_fp8(dev.encode, &p.tmD,
                    C::kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                    2, g.D, g.N, g.M, 0, 64, 32))
@@ -617,7 +672,7 @@ cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t st
             return launch_cfg<FpPair<true, T>>(g, dev, stream);
         return launch_cfg<FpTile<true, T>>(g, dev, stream);
     }
-    const int64_t pair_tiles = ceil_div(g.M, 256) * ceil_div(g.N, 256);
+    const int64_t pair_tiles = ceil_div(g.M, 256) * ceil_div(g.N, FpPair<false, T>::BN);
     if (dev.pairs > 0 && 2 * pair_tiles > dev.pairs)
         return launch_cfg<FpPair<false, T>>(g, dev, stream);
     return launch_cfg<FpTile<false, T>>(g, dev, stream);
