@@ -212,6 +212,11 @@ struct Fp8Device {
 };
 cudaError_t launch_gemm_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
 
+// The same for M <= small_m_fp8_max_m(), dense (small_m_fp8.cu): weights
+// streamed into mma.sync register fragments, K split over clusters.
+int64_t small_m_fp8_max_m();
+cudaError_t launch_small_m_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
+
 // Norms around a block fused with its gate and residual scale, and their
 // gradients (norm.cu).  Rows of C = 8 C8 channels; NULL leaves a part out.
 enum GateMode : int { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateElement = 3 };

@@ -13,7 +13,6 @@ it after the work that makes them is the caller's.
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
 from typing import NamedTuple, Optional
 
 from ._binding import TMAGEMM_OK, TmaGemmError, TmagemmNorm, lib
@@ -26,24 +25,27 @@ def _blocks(n: int) -> int:
     return -(-n // FP8_BLOCK)
 
 
-def _on_stream(device, stream, inputs):
-    """A context in which `device` is current and, with an explicit stream, that
-    stream is (so that results are allocated on it), and the stream's handle."""
+def _launch(device, stream, inputs, body):
+    """body(handle) with `device` current and, for an explicit stream, that
+    stream current too, so that the results body() allocates belong to it."""
     import torch
     if stream is None:
-        ctx = (nullcontext() if device.index == torch.cuda.current_device()
-               else torch.cuda.device(device))
-        return ctx, torch.cuda.current_stream(device).cuda_stream
+        if device.index == torch.cuda.current_device():
+            # The raw handle: a Stream object costs as much as a launch.
+            return body(torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(device):
+            return body(torch.cuda.current_stream(device).cuda_stream)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     if stream != torch.cuda.current_stream(device):
         for t in inputs:
             if t is not None:
                 t.record_stream(stream)
-    return torch.cuda.stream(stream), stream.cuda_stream
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
-def _check(name, t, dtype, shape, device=None, contiguous=True):
+def _check(name, t, dtype, shape, device, contiguous=True):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -53,8 +55,14 @@ def _check(name, t, dtype, shape, device=None, contiguous=True):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (row-major)")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _matrix(name, t, dims=2):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise TypeError(f"{name} must be a CUDA tensor of {dims} dimensions")
 
 
 def _bf16(dtype) -> int:
@@ -64,14 +72,6 @@ def _bf16(dtype) -> int:
     if dtype == torch.float16:
         return 0
     raise TypeError(f"the type must be torch.float16 or torch.bfloat16, got {dtype}")
-
-
-def _strides2(t):
-    """(row, column) strides of a scale matrix; a stride that is never stepped
-    (a dimension of one) counts as 1.  Broadcast (zero) strides are refused by
-    the library."""
-    r, c = t.stride()
-    return (r if t.shape[0] > 1 else 1), (c if t.shape[1] > 1 else 1)
 
 
 def _raise(status, what):
@@ -88,26 +88,67 @@ def quantize_fp8(X, block_rows: int = 1, stream=None):
     the products read fastest; weight scales are row-major.
     """
     import torch
-    if not isinstance(X, torch.Tensor) or X.dim() != 2:
-        raise TypeError("X must be a CUDA matrix")
-    bf16 = _bf16(X.dtype)
-    _check("X", X, X.dtype, None)
+    _matrix("X", X)
+    dtype, dev = X.dtype, X.device
+    bf16 = _bf16(dtype)
+    _check("X", X, dtype, None, dev)
     if block_rows not in (1, FP8_BLOCK):
         raise ValueError("block_rows must be 1 or 128")
     M, K = X.shape
-    rows, blocks = -(-M // block_rows), _blocks(K)
-    ctx, handle = _on_stream(X.device, stream, (X,))
-    with ctx:
-        Q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=X.device)
+    blocks = _blocks(K)
+
+    def body(handle):
+        Q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
         if block_rows == 1:
-            S = torch.empty((blocks, rows), dtype=torch.float32, device=X.device)
-            s_row, s_blk = 1, max(rows, 1)
+            S = torch.empty_strided((M, blocks), (1, max(M, 1)), dtype=torch.float32, device=dev)
+            strides = 1, max(M, 1)
         else:
-            S = torch.empty((rows, blocks), dtype=torch.float32, device=X.device)
-            s_row, s_blk = max(blocks, 1), 1
+            S = torch.empty((_blocks(M), blocks), dtype=torch.float32, device=dev)
+            strides = max(blocks, 1), 1
         _raise(lib().quantize_fp8(M, K, X.data_ptr(), bf16, block_rows, Q.data_ptr(),
-                                  S.data_ptr(), s_row, s_blk, handle), "quantize_fp8")
-    return Q, (S.t() if block_rows == 1 else S)
+                                  S.data_ptr(), *strides, handle), "quantize_fp8")
+        return Q, S
+
+    return _launch(dev, stream, (X,), body)
+
+
+def _product(what, A, SA, B, SB, offsets, dtype, out, stream):
+    """The checks, result and call that gemm_fp8 and gemm_fp8_grouped share;
+    `offsets` None: dense."""
+    import torch
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    bf16 = _bf16(dtype)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    M, K = A.shape
+    N = B.shape[-2]
+    lead = tuple(B.shape[:-2])
+    dev = A.device
+    _check("A", A, f8, None, dev)
+    _check("B", B, f8, (*lead, N, K), dev)
+    _check("SA", SA, f32, (M, _blocks(K)), dev, contiguous=False)
+    _check("SB", SB, f32, (*lead, _blocks(N), _blocks(K)), dev)
+    if out is not None:
+        _check("out", out, dtype, (M, N), dev)
+    # A stride that is never stepped (a dimension of one) counts as 1.
+    # Broadcast (zero) strides are refused by the library.
+    sa_row, sa_blk = SA.stride()
+    if M <= 1:
+        sa_row = 1
+    if K <= FP8_BLOCK:
+        sa_blk = 1
+
+    def body(handle):
+        D = torch.empty((M, N), dtype=dtype, device=dev) if out is None else out
+        rest = (M, N, K, A.data_ptr(), SA.data_ptr(), sa_row, sa_blk, B.data_ptr(),
+                SB.data_ptr(), D.data_ptr(), bf16, handle)
+        if offsets is None:
+            _raise(lib().gemm_fp8(*rest), what)
+        else:
+            _raise(lib().gemm_fp8_grouped(lead[0], offsets.data_ptr(), *rest), what)
+        return D
+
+    return _launch(dev, stream, (A, SA, B, SB, offsets, out), body)
 
 
 def gemm_fp8(A, SA, B, SB, dtype=None, out=None, stream=None):
@@ -118,31 +159,9 @@ def gemm_fp8(A, SA, B, SB, dtype=None, out=None, stream=None):
     any strides, SB (ceil(N / 128), ceil(K / 128)) float32, row-major.
     K % 16 == 0 and N % 8 == 0.
     """
-    import torch
-    if out is not None:
-        dtype = out.dtype if dtype is None else dtype
-    bf16 = _bf16(dtype if dtype is not None else torch.bfloat16)
-    dtype = torch.bfloat16 if bf16 else torch.float16
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    if A.dim() != 2 or B.dim() != 2:
-        raise ValueError("A and B must be matrices")
-    M, K = A.shape
-    N = B.shape[0]
-    dev = A.device
-    _check("A", A, f8, None)
-    _check("B", B, f8, (N, K), dev)
-    _check("SA", SA, f32, (M, _blocks(K)), dev, contiguous=False)
-    _check("SB", SB, f32, (_blocks(N), _blocks(K)), dev)
-    sa_row, sa_blk = _strides2(SA)
-    ctx, handle = _on_stream(dev, stream, (A, SA, B, SB, out))
-    with ctx:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=dev)
-        else:
-            _check("out", out, dtype, (M, N), dev)
-        _raise(lib().gemm_fp8(M, N, K, A.data_ptr(), SA.data_ptr(), sa_row, sa_blk, B.data_ptr(),
-                              SB.data_ptr(), out.data_ptr(), bf16, handle), "gemm_fp8")
-    return out
+    _matrix("A", A)
+    _matrix("B", B)
+    return _product("gemm_fp8", A, SA, B, SB, None, dtype, out, stream)
 
 
 def gemm_fp8_grouped(A, SA, B, SB, m_offsets, dtype=None, out=None, stream=None):
@@ -155,32 +174,10 @@ def gemm_fp8_grouped(A, SA, B, SB, m_offsets, dtype=None, out=None, stream=None)
     ceil(K / 128)); the rest as for gemm_fp8.
     """
     import torch
-    if out is not None:
-        dtype = out.dtype if dtype is None else dtype
-    bf16 = _bf16(dtype if dtype is not None else torch.bfloat16)
-    dtype = torch.bfloat16 if bf16 else torch.float16
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    if A.dim() != 2 or B.dim() != 3:
-        raise ValueError("A must be a matrix and B a stack of matrices")
-    M, K = A.shape
-    G, N = B.shape[:2]
-    dev = A.device
-    _check("A", A, f8, None)
-    _check("B", B, f8, (G, N, K), dev)
-    _check("SA", SA, f32, (M, _blocks(K)), dev, contiguous=False)
-    _check("SB", SB, f32, (G, _blocks(N), _blocks(K)), dev)
-    _check("m_offsets", m_offsets, torch.int32, (G + 1,), dev)
-    sa_row, sa_blk = _strides2(SA)
-    ctx, handle = _on_stream(dev, stream, (A, SA, B, SB, m_offsets, out))
-    with ctx:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=dev)
-        else:
-            _check("out", out, dtype, (M, N), dev)
-        _raise(lib().gemm_fp8_grouped(G, m_offsets.data_ptr(), M, N, K, A.data_ptr(),
-                                      SA.data_ptr(), sa_row, sa_blk, B.data_ptr(), SB.data_ptr(),
-                                      out.data_ptr(), bf16, handle), "gemm_fp8_grouped")
-    return out
+    _matrix("A", A)
+    _matrix("B", B, 3)
+    _check("m_offsets", m_offsets, torch.int32, (B.shape[0] + 1,), A.device)
+    return _product("gemm_fp8_grouped", A, SA, B, SB, m_offsets, dtype, out, stream)
 
 
 class NormOut(NamedTuple):
@@ -203,36 +200,34 @@ class NormGrads(NamedTuple):
 
 def _norm_struct(h, y, gate, w_post, w_pre, alpha, eps):
     """The checked operands as a TmagemmNorm."""
-    import torch
-    if not isinstance(h, torch.Tensor) or h.dim() != 2:
-        raise TypeError("h must be a CUDA matrix (tokens, channels)")
+    _matrix("h", h)
     T, C = h.shape
     dt, dev = h.dtype, h.device
-    p = TmagemmNorm()
-    p.bf16 = _bf16(dt)
-    _check("h", h, dt, None)
+    bf16 = _bf16(dt)
+    _check("h", h, dt, None, dev)
     if y is None and (w_pre is None or w_post is not None or gate is not None):
         raise ValueError("without y there is neither w_post nor gate, and w_pre is needed")
-    for name, t, shape in (("y", y, (T, C)), ("w_post", w_post, (C,)), ("w_pre", w_pre, (C,))):
+    ptr = [None, None, None]
+    for i, (name, t, shape) in enumerate((("y", y, h.shape), ("w_post", w_post, (C,)),
+                                          ("w_pre", w_pre, (C,)))):
         if t is not None:
             _check(name, t, dt, shape, dev)
-            setattr(p, name, t.data_ptr())
-    p.T, p.C, p.alpha, p.eps, p.h = T, C, alpha, eps, h.data_ptr()
+            ptr[i] = t.data_ptr()
+    mode, gate_ptr = _GATE_NONE, None
     if gate is not None:
         shape = tuple(gate.shape)
-        if shape == (C,) or shape == (1, C):
-            # With one token, (1, C) is also that token's elements; the
-            # gradient is then the same but for its type.
-            p.gate_mode = _GATE_CHANNEL if shape == (C,) or T != 1 else _GATE_ELEMENT
-        elif shape == (T, C):
-            p.gate_mode = _GATE_ELEMENT
+        if shape == (T, C):
+            mode = _GATE_ELEMENT
+        elif shape == (C,) or shape == (1, C):
+            mode = _GATE_CHANNEL
         elif shape == (T, 1):
-            p.gate_mode = _GATE_TOKEN
+            mode = _GATE_TOKEN
         else:
             raise ValueError(f"gate must be (C,), (1, C), (T, 1) or (T, C), got {shape}")
         _check("gate", gate, dt, None, dev)
-        p.gate = gate.data_ptr()
-    return p
+        gate_ptr = gate.data_ptr()
+    return TmagemmNorm(T, C, bf16, mode, alpha, eps, h.data_ptr(), ptr[0], gate_ptr, ptr[1],
+                       ptr[2])
 
 
 def norm_residual(h, y=None, gate=None, w_post=None, w_pre=None, alpha: float = 1.0,
@@ -254,29 +249,31 @@ def norm_residual(h, y=None, gate=None, w_post=None, w_pre=None, alpha: float = 
         raise ValueError("quantize needs w_pre")
     T, C = h.shape
     dev = h.device
-    ctx, handle = _on_stream(dev, stream, (h, y, gate, w_post, w_pre))
-    h_out, x, scales, r_post, r_pre = h, None, None, None, None
-    with ctx:
+    f32 = torch.float32
+
+    def body(handle):
+        h_out, x, scales, r_post, r_pre = h, None, None, None, None
         if y is not None:
             h_out = torch.empty_like(h)
             p.h_out = h_out.data_ptr()
         if w_pre is not None and quantize:
             x = torch.empty((T, C), dtype=torch.float8_e4m3fn, device=dev)
-            scales = torch.empty((_blocks(C), T), dtype=torch.float32, device=dev)
+            scales = torch.empty_strided((T, _blocks(C)), (1, max(T, 1)), dtype=f32, device=dev)
             p.q, p.scales, p.s_row_stride, p.s_block_stride = (
                 x.data_ptr(), scales.data_ptr(), 1, max(T, 1))
-            scales = scales.t()
         elif w_pre is not None:
             x = torch.empty_like(h)
             p.x = x.data_ptr()
         if save_rstd and w_post is not None:
-            r_post = torch.empty((T,), dtype=torch.float32, device=dev)
+            r_post = torch.empty((T,), dtype=f32, device=dev)
             p.rstd_post = r_post.data_ptr()
         if save_rstd and w_pre is not None:
-            r_pre = torch.empty((T,), dtype=torch.float32, device=dev)
+            r_pre = torch.empty((T,), dtype=f32, device=dev)
             p.rstd_pre = r_pre.data_ptr()
         _raise(lib().norm_residual(ctypes.byref(p), handle), "norm_residual")
-    return NormOut(h_out, x, scales, r_post, r_pre)
+        return NormOut(h_out, x, scales, r_post, r_pre)
+
+    return _launch(dev, stream, (h, y, gate, w_post, w_pre), body)
 
 
 def norm_residual_backward(h, y=None, dh=None, dx=None, gate=None, w_post=None, w_pre=None,
@@ -304,9 +301,9 @@ def norm_residual_backward(h, y=None, dh=None, dx=None, gate=None, w_post=None, 
         if w is not None:
             _check(name, t, f32, (T,), dev)
             setattr(p, name, t.data_ptr())
-    ctx, handle = _on_stream(dev, stream, (h, y, dh, dx, gate, w_post, w_pre, rstd_post, rstd_pre))
-    dy = dgate = dw_post = dw_pre = None
-    with ctx:
+
+    def body(handle):
+        dy = dgate = dw_post = dw_pre = None
         need = lib().norm_residual_backward_workspace_size(T, C)
         if need < 0:
             raise TmaGemmError(int(need), "norm_residual_backward_workspace_size")
@@ -328,4 +325,6 @@ def norm_residual_backward(h, y=None, dh=None, dx=None, gate=None, w_post=None, 
             p.dw_pre = dw_pre.data_ptr()
         _raise(lib().norm_residual_backward(ctypes.byref(p), workspace.data_ptr(), need, handle),
                "norm_residual_backward")
-    return NormGrads(dh_in, dy, dgate, dw_post, dw_pre)
+        return NormGrads(dh_in, dy, dgate, dw_post, dw_pre)
+
+    return _launch(dev, stream, (h, y, dh, dx, gate, w_post, w_pre, rstd_post, rstd_pre), body)
