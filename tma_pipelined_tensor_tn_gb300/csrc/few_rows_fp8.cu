@@ -1,0 +1,361 @@
+// gemm_fp8 for few rows of activations on tcgen05, with the operands' roles
+// swapped: the weights are the 128-row MMA operand and the activations the
+// narrow one, in blocks of NP = 16, 32, 64 or 128 tokens (rows past M zero), so
+// the work follows the number of tokens and all 128 accumulator lanes hold
+// weight rows.  Bound by streaming the weights; K is split over the CTAs of a
+// cluster so that enough of them stream at once.
+//
+// As in the tile kernel each 128-k block's product has a TMEM accumulator of
+// its own (four of them).  Here a lane is a weight row and a column a token,
+// so a block's scale varies along the columns: the epilogue threads keep
+// SA[token] * SB (the tile's 128 weight rows share one SB per block) of four
+// blocks in shared memory, read as broadcasts, and add
+//   acc[token] += t[token] * scale[token].
+//
+// Roles: warp 0 TMA producer, warp 1 MMA issuer, then four scaling warps (eight
+// for 128 tokens, half of the columns each).  The CTAs of a cluster leave their
+// FP32 partial tiles [token][weight row] in shared memory (over the ring) and
+// each adds and stores a share of the outputs, in slice order: no workspace,
+// one launch, deterministic.
+//
+// Up to 64 tokens two CTAs share an SM (half the ring and at most 256 TMEM
+// columns each): while one sets up or reduces, the other streams.
+//
+// Measured on GB300 (device time, weights colder than L2): 1 x 4096 x 14336
+// 11.4 us (5.1 TB/s of weights), 32 x 14336 x 4096 12.8 us.  A kernel that
+// streamed the weights into mma.sync fragments, as the 16-bit few-row kernel
+// does, took 12.6 us at one token and 19.7 us at 16.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "launch.h"
+#include "ptx.cuh"
+#include "fp8.cuh"
+#include "tile_sched.cuh"
+
+namespace tmagemm {
+
+namespace {
+
+template <int NP_, int STAGES_, int EPI_WARPS_, int CTAS_PER_SM_, bool BF16_>
+struct FewCfg {
+    static constexpr int NP = NP_, STAGES = STAGES_, BN = 128, BK = kFp8Block;
+    static constexpr int kCtasPerSm = CTAS_PER_SM_;
+    static constexpr bool kBF16 = BF16_;
+    static constexpr int kEpiThreads = 32 * EPI_WARPS_;
+    static constexpr int kThreads = 64 + kEpiThreads, kAccs = 4;
+    static constexpr int kCols = NP_ / (EPI_WARPS_ / 4);   // tokens of one epilogue warp
+    static constexpr uint32_t kTmemCols = kAccs * NP;
+    static constexpr uint32_t kWBytes = BN * BK, kXBytes = NP * BK;
+    static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
+    static constexpr uint32_t kPartStride = BN + 4;   // floats; rows stay 16-byte aligned
+    static constexpr uint32_t kOffScale = STAGES * kStageBytes;   // [2][4][NP] floats
+    static constexpr uint32_t kOffBar = kOffScale + 2 * 4 * NP * 4;
+    static constexpr uint32_t kNumBars = 2 * STAGES + 2 * kAccs + 1;
+    static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
+    static_assert(kTmemCols * CTAS_PER_SM_ <= 512, "resident CTAs share TMEM");
+    static_assert((kSmemBytes + 1024) * CTAS_PER_SM_ <= 233472, "and shared memory");
+    static_assert(NP * kPartStride * 4 <= STAGES * kStageBytes, "partial tile over the ring");
+    static_assert(kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
+};
+
+constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {   // e4m3 operands, FP32 sums
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+struct FewProblem {
+    CUtensorMap tmW;   // B {K, N}, box {128, 128}
+    CUtensorMap tmX;   // A {K, M}, box {128, NP}
+    // blockIdx.x = (token block * n_tiles + weight tile) * splits + K slice
+    const float *sa, *sb;
+    int64_t sa_row, sa_blk;
+    uint16_t* d;
+    int32_t M, N, k_blocks, n_tiles, splits, slice;   // slice: k-blocks per CTA of a cluster
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
+few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limit_ns,
+                    uint32_t* __restrict__ err) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (sbase - raw);
+    const uint32_t bar0 = sbase + C::kOffBar;
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (C::STAGES + s); };
+    auto acc_full_bar = [&](uint32_t a) { return bar0 + 8u * (2 * C::STAGES + a); };
+    auto acc_empty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * C::STAGES + C::kAccs + a); };
+    const uint32_t mma_done_bar = bar0 + 8u * (2 * C::STAGES + 2 * C::kAccs);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    const uint32_t rank = cluster_ctarank();
+    const int32_t tile = static_cast<int32_t>(blockIdx.x) / prob.splits;
+    const int32_t n0 = tile % prob.n_tiles * C::BN, m0 = tile / prob.n_tiles * C::NP;
+    const int32_t tokens = min(C::NP, prob.M - m0);
+    const int32_t kb0 = static_cast<int32_t>(rank) * prob.slice;
+    const int32_t kb1 = min(prob.k_blocks, kb0 + prob.slice);   // may be <= kb0: no blocks
+
+    grid_launch_dependents();
+    if (warp == 0) {
+        if (elect_one()) {
+            for (uint32_t s = 0; s < (uint32_t)C::STAGES; ++s) {
+                mbar_init(full_bar(s), 1);
+                mbar_init(empty_bar(s), 1);
+            }
+            for (uint32_t a = 0; a < (uint32_t)C::kAccs; ++a) {
+                mbar_init(acc_full_bar(a), 1);
+                mbar_init(acc_empty_bar(a), C::kEpiThreads / 32);
+            }
+            mbar_init(mma_done_bar, 1);
+            *abort_flag = 0;
+            fence_mbarrier_init();
+            tma_prefetch_desc(&prob.tmW);
+            tma_prefetch_desc(&prob.tmX);
+            // Weights of the first k-blocks into L2 while the previous grid
+            // finishes (a prefetch cannot see stale data).
+            for (int32_t kb = kb0; kb < min(kb1, kb0 + C::STAGES); ++kb)
+                tma_prefetch_l2_2d(&prob.tmW, kb * C::BK, n0);
+        }
+        __syncwarp();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_holder), C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    grid_dependency_wait();
+
+    if (warp == 0) {
+        if (elect_one()) {
+            uint32_t it = 0;
+            for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
+                const uint32_t s = ring_stage(it, C::STAGES);
+                if (!wait_or_abort(empty_bar(s), ring_phase(it, C::STAGES) ^ 1u, abort_flag, err,
+                                   kSiteProducerEmpty, limit_ns))
+                    break;
+                mbar_arrive_expect_tx(full_bar(s), C::kStageBytes);
+                const uint32_t w = sbase + s * C::kStageBytes;
+                tma_load_2d(w, &prob.tmW, kb * C::BK, n0, full_bar(s));
+                tma_load_2d(w + C::kWBytes, &prob.tmX, kb * C::BK, m0, full_bar(s));
+            }
+            // The last stages issued must have landed before shared memory is reused.
+            const uint32_t first = it > (uint32_t)C::STAGES ? it - C::STAGES : 0u;
+            for (uint32_t j = first; j < it; ++j)
+                wait_bounded(full_bar(ring_stage(j, C::STAGES)), ring_phase(j, C::STAGES), err,
+                             kSiteDrainFull, limit_ns);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            constexpr uint32_t kIdesc = idesc_e4m3(C::BN, C::NP);
+            uint32_t it = 0;
+            for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
+                const uint32_t s = ring_stage(it, C::STAGES);
+                const uint32_t a = ring_stage(it, C::kAccs);
+                if (!wait_or_abort(full_bar(s), ring_phase(it, C::STAGES), abort_flag, err,
+                                   kSiteMmaFull, limit_ns) ||
+                    !wait_or_abort(acc_empty_bar(a), ring_phase(it, C::kAccs) ^ 1u, abort_flag,
+                                   err, kSiteMmaAccEmpty, limit_ns))
+                    break;
+                tc_fence_after();
+                const uint32_t w = sbase + s * C::kStageBytes;
+                const uint64_t w_desc = umma_desc_sw128_kmajor(w);
+                const uint64_t x_desc = umma_desc_sw128_kmajor(w + C::kWBytes);
+#pragma unroll
+                for (int j = 0; j < C::BK / 32; ++j)   // 32 k = 32 bytes = 2 address units
+                    mma_e4m3(tmem_base + a * C::NP, w_desc + 2 * j, x_desc + 2 * j, kIdesc,
+                             j != 0 ? 1u : 0u);
+                mma_commit(empty_bar(s));
+                mma_commit(acc_full_bar(a));
+            }
+            mma_commit(mma_done_bar);
+            wait_bounded(mma_done_bar, 0, err, kSiteDrainMma, limit_ns);
+        }
+        __syncwarp();
+    } else {
+        const uint32_t quarter = static_cast<uint32_t>(warp) & 3u;
+        const int tid = static_cast<int>(threadIdx.x) - 64;
+        const int col0 = ((warp - 2) >> 2) * C::kCols;   // this warp's first token
+        const uint32_t t_base = tmem_base + ((quarter * 32u) << 16) + col0;
+        float* scale = reinterpret_cast<float*>(smem + C::kOffScale);
+        // Token `tid`'s scales (and the tile's weight scales) of four blocks at
+        // a time, read while the four before them are used.
+        const bool token = tid < tokens;
+        const float* sa = prob.sa + (token ? (m0 + tid) * prob.sa_row : 0);
+        const float* sb = prob.sb + static_cast<int64_t>(n0 / kFp8Block) * prob.k_blocks;
+        float next[4];
+        auto fetch = [&](int32_t kb) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                next[j] = token && kb + j < kb1 ? sa[(kb + j) * prob.sa_blk] * sb[kb + j] : 0.0f;
+        };
+        fetch(kb0);
+        float acc[C::kCols] = {};
+        bool ok = true;
+        uint32_t it = 0;
+        for (int32_t kb = kb0; kb < kb1; kb += 4) {
+            float* sc = scale + ((kb - kb0) & 4) * C::NP;   // the two buffers in turn
+            if (tid < C::NP) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sc[j * C::NP + tid] = next[j];
+            }
+            // Also ends the loop in every warp once a wait has failed in one.
+            if (!named_bar_and(1, C::kEpiThreads, ok)) break;
+            fetch(kb + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (kb + j >= kb1 || !ok) break;
+                const uint32_t a = ring_stage(it, C::kAccs);
+                ok = __all_sync(0xffffffffu,
+                                wait_many(acc_full_bar(a), ring_phase(it, C::kAccs), abort_flag,
+                                          err, kSiteEpiAccFull, limit_ns));
+                if (!ok) break;
+                ++it;
+                tc_fence_after();
+                constexpr int kPart = C::kCols < 32 ? C::kCols : 32;
+#pragma unroll
+                for (int c = 0; c < C::kCols; c += kPart) {
+                    uint32_t v[kPart];
+                    if constexpr (kPart == 16)
+                        tmem_ld_32x32b_x16(t_base + a * C::NP + c, v);
+                    else
+                        tmem_ld_32x32b_x32(t_base + a * C::NP + c, v);
+                    tmem_ld_wait();
+                    if (c + kPart == C::kCols) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(acc_empty_bar(a));
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPart; i += 4) {
+                        const float4 f =
+                            *reinterpret_cast<const float4*>(sc + j * C::NP + col0 + c + i);
+                        scale_add(acc[c + i], v[i], f.x);
+                        scale_add(acc[c + i + 1], v[i + 1], f.y);
+                        scale_add(acc[c + i + 2], v[i + 2], f.z);
+                        scale_add(acc[c + i + 3], v[i + 3], f.w);
+                    }
+                }
+            }
+        }
+        // Every block has been multiplied, so every stage has been read: the
+        // partial tile goes over the ring, a column (token) per row of it.
+        // (After a failed wait stages may still be written: leave them alone.)
+        if (named_bar_and(1, C::kEpiThreads, ok)) {
+            float* part = reinterpret_cast<float*>(smem);
+            const uint32_t n = quarter * 32u + static_cast<uint32_t>(lane);
+#pragma unroll
+            for (int c = 0; c < C::kCols; ++c)
+                if (col0 + c < tokens) part[(col0 + c) * C::kPartStride + n] = acc[c];
+        }
+    }
+
+    tc_fence_before();
+    if (prob.splits > 1) cluster_sync(); else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::kTmemCols);
+    }
+    // Groups of four outputs of a token, dealt out evenly over the cluster's
+    // CTAs (N is a multiple of 8: a group is either whole or outside).
+    const int cols = min(C::BN, prob.N - n0) / 4;
+    const int total = tokens * cols;
+    const int end = (static_cast<int>(rank) + 1) * total / prob.splits;
+    for (int o = static_cast<int>(rank) * total / prob.splits + static_cast<int>(threadIdx.x);
+         o < end; o += C::kThreads) {
+        const int m = o / cols, n = 4 * (o % cols);
+        const uint32_t local = sbase + (m * C::kPartStride + n) * 4u;
+        float v[8][4];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < prob.splits) ld_shared_cluster_v4(map_to_rank(local, q), v[q]);
+        float s[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+            if (q < prob.splits)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] += v[q][e];
+        uint2 out;
+        out.x = pack2_rn<C::kBF16>(__float_as_uint(s[0]), __float_as_uint(s[1]));
+        out.y = pack2_rn<C::kBF16>(__float_as_uint(s[2]), __float_as_uint(s[3]));
+        if (check_ok(m0 + m < prob.M && n0 + n + 4 <= prob.N, err, kSiteCheckBounds))
+            *reinterpret_cast<uint2*>(prob.d + static_cast<int64_t>(m0 + m) * prob.N + n0 + n) =
+                out;
+    }
+    if (threadIdx.x == 0 && !*abort_flag)
+        check_count_unit(err, static_cast<int32_t>(blockIdx.x));
+    // Peers' shared memory stays alive until every CTA has read it.
+    if (prob.splits > 1) cluster_sync();
+}
+
+template <class C>
+cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
+    FewProblem p;
+    if (encode_fp8_operand(dev.encode, &p.tmW, g.B, g.K, g.N, 0, C::BN) ||
+        encode_fp8_operand(dev.encode, &p.tmX, g.A, g.K, g.M, 0, C::NP))
+        return cudaErrorInvalidValue;
+    p.sa = g.SA;
+    p.sb = g.SB;
+    p.sa_row = g.sa_row;
+    p.sa_blk = g.sa_blk;
+    p.d = static_cast<uint16_t*>(g.D);
+    p.M = static_cast<int32_t>(g.M);
+    p.N = static_cast<int32_t>(g.N);
+    p.k_blocks = static_cast<int32_t>(ceil_div(g.K, C::BK));
+    // As many K slices as keep all CTAs resident, each with at least two blocks.
+    p.n_tiles = static_cast<int32_t>(ceil_div(g.N, C::BN));
+    const int64_t tiles = p.n_tiles * ceil_div(g.M, C::NP);
+    const int64_t slots = static_cast<int64_t>(dev.sms) * C::kCtasPerSm;
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= slots && p.k_blocks >= 4 * splits) splits *= 2;
+    p.splits = splits;
+    p.slice = static_cast<int32_t>(ceil_div(p.k_blocks, splits));
+    static ContextMarks attr_done;
+    auto kernel = few_rows_fp8_kernel<C>;
+    if (cudaError_t e = smem_opt_in(kernel, static_cast<int>(C::kSmemBytes), attr_done)) return e;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles * splits)), dim3(C::kThreads),
+                         C::kSmemBytes, stream, static_cast<unsigned>(splits), dev.pdl, p,
+                         dev.limit_ns, dev.err_word);
+}
+
+template <bool T>
+cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
+    if (g.M <= 16) return launch_cfg<FewCfg<16, 6, 4, 2, T>>(g, dev, stream);
+    if (g.M <= 32) return launch_cfg<FewCfg<32, 5, 4, 2, T>>(g, dev, stream);
+    if (g.M <= 64) return launch_cfg<FewCfg<64, 4, 4, 2, T>>(g, dev, stream);
+    return launch_cfg<FewCfg<128, 6, 8, 1, T>>(g, dev, stream);
+}
+
+}  // namespace
+
+// One block of tokens, or more where the 128 x 128 tiles leave room to split K:
+// at 256 x 4096 x 4096 (64 tiles) 10.8 us against 14.8 us for the tile kernel,
+// at 512 x 4096 x 4096 (128 tiles, no split) 16.9 against 15.2 us.
+bool few_rows_fp8(int64_t M, int64_t N, int sms) {
+    return M <= 128 || 2 * ceil_div(M, 128) * ceil_div(N, 128) <= sms;
+}
+
+cudaError_t launch_few_rows_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
+    return g.bf16 ? launch_typed<true>(g, dev, stream) : launch_typed<false>(g, dev, stream);
+}
+
+}  // namespace tmagemm

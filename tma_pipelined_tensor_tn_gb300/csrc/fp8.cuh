@@ -78,4 +78,12 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
     return m;
 }
 
+// acc += t * s, with t from TMEM.  Volatile, so that it stays behind the wait
+// for the load that brought t.  (Multiply-adds of packed pairs are half as
+// many instructions for the same cycles, but each loaded register is then
+// copied to form its pair.)
+__device__ __forceinline__ void scale_add(float& acc, uint32_t t, float s) {
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(t)), "f"(s));
+}
+
 }  // namespace tmagemm

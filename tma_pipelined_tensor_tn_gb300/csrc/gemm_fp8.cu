@@ -117,14 +117,6 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
             : "memory");
 }
 
-// acc += t * s, with t from TMEM.  Volatile, so that it stays behind the wait
-// for the load that brought t.  (Multiply-adds of packed pairs are half as
-// many instructions for the same cycles, but each loaded register is then
-// copied to form its pair.)
-__device__ __forceinline__ void scale_add(float& acc, uint32_t t, float s) {
-    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(t)), "f"(s));
-}
-
 // One arrival on an mbarrier at a shared::cluster address by the threads whose
 // `p` is not 0; predicated rather than branched around, and relaxed (what it
 // hands over is a TMEM accumulator that has been read, behind a tcgen05 fence;
@@ -608,16 +600,16 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
 template <bool G, bool T> using FpPair = Fp8Cfg<256, 128, 5, true, G, T>;
 template <bool G, bool T> using FpTile = Fp8Cfg<128, 64, 6, false, G, T>;
 
-int encode_fp8(EncodeTiled encode, CUtensorMap* map, CUtensorMapDataType type, int elem_bytes,
-               const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1) {
-    cuuint64_t dims[3] = {d0, d1, d2};
-    cuuint64_t strides[2] = {d0 * elem_bytes, d0 * d1 * elem_bytes};
-    cuuint32_t box[3] = {b0, b1, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    const bool store = elem_bytes == 2;
-    return encode(map, type, d2 == 0 ? 2 : 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  store ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+// D {N, rows} in store boxes of 64 columns x 32 rows.
+int encode_output(EncodeTiled encode, CUtensorMap* map, void* base, uint64_t N, uint64_t rows,
+                  bool bf16) {
+    cuuint64_t dims[2] = {N, rows};
+    cuuint64_t strides[1] = {N * 2};
+    cuuint32_t box[2] = {64, 32};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? 0
                : -1;
@@ -627,13 +619,9 @@ template <class C>
 cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
     Fp8Problem p;
     const int64_t G = C::kGrouped ? g.groups : 1;
-    if (encode_fp8(dev.encode, &p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.A, g.K, g.M, 0, C::BK,
-                   C::kABoxRows) ||
-        encode_fp8(dev.encode, &p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.B, g.K, g.N, G, C::BK,
-                   C::kBBoxRows) ||
-        encode_fp8(dev.encode, &p.tmD,
-                   C::kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                   2, g.D, g.N, g.M, 0, 64, 32))
+    if (encode_fp8_operand(dev.encode, &p.tmA, g.A, g.K, g.M, 0, C::kABoxRows) ||
+        encode_fp8_operand(dev.encode, &p.tmB, g.B, g.K, g.N, G, C::kBBoxRows) ||
+        encode_output(dev.encode, &p.tmD, g.D, g.N, g.M, C::kBF16))
         return cudaErrorInvalidValue;
     p.sa = g.SA;
     p.sa_row = g.sa_row;
@@ -679,6 +667,20 @@ cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t st
 }
 
 }  // namespace
+
+int encode_fp8_operand(EncodeTiled encode, CUtensorMap* map, const void* base, uint64_t K,
+                       uint64_t rows, uint64_t mats, uint32_t box_rows) {
+    cuuint64_t dims[3] = {K, rows, mats};
+    cuuint64_t strides[2] = {K, K * rows};
+    cuuint32_t box[3] = {kFp8Block, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, mats == 0 ? 2 : 3, const_cast<void*>(base),
+                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? 0
+               : -1;
+}
 
 cudaError_t launch_gemm_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
     return g.bf16 ? launch_typed<true>(g, dev, stream) : launch_typed<false>(g, dev, stream);

@@ -212,10 +212,15 @@ struct Fp8Device {
 };
 cudaError_t launch_gemm_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
 
-// The same for M <= small_m_fp8_max_m(), dense (small_m_fp8.cu): weights
-// streamed into mma.sync register fragments, K split over clusters.
-int64_t small_m_fp8_max_m();
-cudaError_t launch_small_m_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
+// The same where few_rows_fp8(M, N, sms) (few_rows_fp8.cu): tcgen05 with the
+// weights as the 128-row operand, K split over clusters.
+bool few_rows_fp8(int64_t M, int64_t N, int sms);
+cudaError_t launch_few_rows_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
+
+// Map of an e4m3 operand {K, rows, mats} (mats 0: a single matrix, rank 2) in
+// boxes of 128 k x box_rows, 128-byte swizzle.  0, or -1 on failure.
+int encode_fp8_operand(EncodeTiled encode, CUtensorMap* map, const void* base, uint64_t K,
+                       uint64_t rows, uint64_t mats, uint32_t box_rows);
 
 // Norms around a block fused with its gate and residual scale, and their
 // gradients (norm.cu).  Rows of C = 8 C8 channels; NULL leaves a part out.
