@@ -760,7 +760,7 @@ int64_t norm_residual_backward_workspace_size(int64_t T, int64_t C) {
     if (T == 0) return 0;
     DeviceState* d = nullptr;
     if (int s = device_state(&d)) return s;
-    return static_cast<int64_t>(norm_backward_ctas(T, d->sms)) * 2 * C * 4;
+    return static_cast<int64_t>(norm_backward_ctas(T, C, d->sms)) * 2 * C * 4;
 }
 
 int norm_residual_backward(const tmagemm_norm* p, void* workspace, int64_t workspace_bytes,

@@ -245,7 +245,7 @@ struct NormArgs {
     float *dw_post, *dw_pre;
     float* partial;                // norm_backward_ctas x 2 x C
 };
-int norm_backward_ctas(int64_t T, int sms);
+int norm_backward_ctas(int64_t T, int64_t C, int sms);
 cudaError_t launch_norm_forward(const NormArgs& p, bool bf16, int sms, bool pdl,
                                 cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormArgs& p, bool bf16, int sms, bool pdl,

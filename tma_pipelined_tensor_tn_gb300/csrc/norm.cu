@@ -6,9 +6,12 @@
 // written, and x is computed from the unrounded h'.  x leaves in 16 bits or as
 // e4m3 codes with a scale per 128 channels (fp8.cuh), ready for gemm_fp8.
 //
-// Bound by memory: a row of C channels stays in the registers of one CTA
-// between the loads, the two sums and the stores, so each operand is read
-// once and each result written once.
+// Bound by memory, each operand read once and each result written once.  A CTA
+// walks rows blockIdx.x, + gridDim.x, ...; thread t owns the 8-channel vectors
+// t + i * blockDim.x of every row, so weights and column sums stay in its
+// registers, and it copies its own vectors of the next row into shared memory
+// (cp.async) while the CTA works on this one: no thread reads another's copy,
+// so only the two row sums need a barrier.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -51,94 +54,199 @@ __device__ __forceinline__ float to_float(uint16_t v) {
         return __half2float(__ushort_as_half(v));
 }
 
-// The gate of one row: per element of an 8-channel vector, or one number.
-template <bool BF16>
-__device__ __forceinline__ void gate8(const NormArgs& p, int64_t row, int32_t c, float (&g)[8]) {
-    if (p.gate_mode == kGateChannel) {
-        unpack8<BF16>(static_cast<const uint4*>(p.gate)[c], g);
-    } else if (p.gate_mode == kGateElement) {
-        unpack8<BF16>(static_cast<const uint4*>(p.gate)[row * p.C8 + c], g);
-    } else {
-        const float v = p.gate_mode == kGateToken
-                            ? to_float<BF16>(static_cast<const uint16_t*>(p.gate)[row])
-                            : 1.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = v;
-    }
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All copies of this thread but those of its latest N groups have arrived.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One CTA per row at a time; thread t holds the 8-channel vectors t + i *
-// blockDim.x, i < V, so the 16 lanes of a half warp hold one 128-channel block.
-template <bool BF16, int V>
-__global__ void __launch_bounds__(1024)
-norm_forward_kernel(const NormArgs p) {
-    __shared__ float slots[2][kMaxWarps];
-    grid_launch_dependents();
-    grid_dependency_wait();
-    uint32_t slot = 0;
-    const int32_t C8 = p.C8;
-    const float inv_c = 1.0f / (8.0f * static_cast<float>(C8));
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        float h[V][8], y[V][8];
+constexpr int kMaxRowInputs = 5;
+
+// The T x C operands of a row: their order in a stage, -1 where absent.
+struct RowInputs {
+    const uint4* base[kMaxRowInputs];
+    int n;
+    int h, y, gate, dh, dx;
+    int stages;   // rows in shared memory: 2, or 1 where two do not fit
+};
+
+// This thread's vectors of the rows of its CTA, in shared memory one row ahead
+// (with one stage, the next row's are fetched when this one is done):
+// vector i of operand a at ring[(stage * n + a) * V + i][thread].
+template <int V>
+struct RowPipe {
+    const RowInputs& in;
+    uint32_t base;    // shared-memory address of this thread's column
+    uint32_t step;    // bytes between consecutive vectors of a thread
+    int32_t C8;
+    uint32_t stage = 0;
+
+    __device__ __forceinline__ RowPipe(const RowInputs& inputs, uint4* ring, int32_t c8)
+        : in(inputs), base(smem_u32(ring) + threadIdx.x * 16u), step(blockDim.x * 16u), C8(c8) {}
+    __device__ __forceinline__ uint32_t at(uint32_t st, int a, int i) const {
+        return base + ((st * in.n + a) * V + i) * step;
+    }
+    __device__ __forceinline__ void issue(int64_t row, int64_t T, uint32_t st) {
+        if (row < T) {
+            for (int a = 0; a < in.n; ++a)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
+                    if (c < C8) cp_async_16(at(st, a, i), in.base[a] + row * C8 + c);
+                }
+        }
+        cp_async_commit();
+    }
+    // Before a row: starts on the copies of row `next`, waits for this row's.
+    __device__ __forceinline__ void begin(int64_t next, int64_t T) {
+        if (in.stages == 2) {
+            issue(next, T, stage ^ 1u);
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
+    }
+    // After a row (its vectors have been read).
+    __device__ __forceinline__ void end(int64_t next, int64_t T) {
+        if (in.stages == 2)
+            stage ^= 1u;
+        else
+            issue(next, T, 0);
+    }
+    template <bool BF16>
+    __device__ __forceinline__ void read(int a, int i, float (&v)[8]) const {
+        uint4 p;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(p.x), "=r"(p.y), "=r"(p.z), "=r"(p.w)
+                     : "r"(at(stage, a, i))
+                     : "memory");
+        unpack8<BF16>(p, v);
+    }
+};
+
+// This thread's vectors of the per-channel operands, kept packed.
+template <int V>
+struct Channels {
+    uint4 w_post[V], w_pre[V], gate[V];
+    __device__ __forceinline__ explicit Channels(const NormArgs& p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
             const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            unpack8<BF16>(c < C8 ? p.h[row * C8 + c] : z, h[i]);
-            if (p.y) unpack8<BF16>(c < C8 ? p.y[row * C8 + c] : z, y[i]);
+            w_post[i] = p.w_post && c < p.C8 ? p.w_post[c] : z;
+            w_pre[i] = p.w_pre && c < p.C8 ? p.w_pre[c] : z;
+            gate[i] = p.gate_mode == kGateChannel && c < p.C8
+                          ? static_cast<const uint4*>(p.gate)[c]
+                          : z;
         }
-        if (p.y) {
-            float r = 1.0f;
-            if (p.w_post) {
-                float ss = 0.0f;
+    }
+};
+
+// The gate of vector i of the current row; `token` is a per-token gate (or 1).
+template <bool BF16, int V>
+__device__ __forceinline__ void gate8(const NormArgs& p, const Channels<V>& ch,
+                                      const RowPipe<V>& pipe, float token, int i,
+                                      float (&g)[8]) {
+    if (p.gate_mode == kGateChannel) {
+        unpack8<BF16>(ch.gate[i], g);
+    } else if (p.gate_mode == kGateElement) {
+        pipe.template read<BF16>(pipe.in.gate, i, g);
+    } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(y[i][e], y[i][e], ss);
-                r = rsqrtf(cta_sum(ss, slots, slot) * inv_c + p.eps);
-                if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = r;
-            }
+        for (int e = 0; e < 8; ++e) g[e] = token;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float token_gate(const NormArgs& p, int64_t row) {
+    return p.gate_mode == kGateToken && row < p.T
+               ? to_float<BF16>(static_cast<const uint16_t*>(p.gate)[row])
+               : 1.0f;
+}
+
+// The 16 lanes of a half warp hold one 128-channel block, so its largest
+// magnitude takes four shuffles.
+template <bool BF16, int V, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS, 1)
+norm_forward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ RowInputs in) {
+    extern __shared__ uint4 ring[];
+    __shared__ float slots[2][kMaxWarps];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int32_t C8 = p.C8;
+    const float inv_c = 1.0f / (8.0f * static_cast<float>(C8));
+    uint32_t slot = 0;
+    RowPipe<V> pipe(in, ring, C8);
+    pipe.issue(blockIdx.x, p.T, 0);
+    float token_next = token_gate<BF16>(p, blockIdx.x);
+    const Channels<V> ch(p);
+    for (int64_t row = blockIdx.x; row < p.T; pipe.end(row + gridDim.x, p.T), row += gridDim.x) {
+        pipe.begin(row + gridDim.x, p.T);
+        const float token = token_next;
+        token_next = token_gate<BF16>(p, row + gridDim.x);
+        float h[V][8];
+        float r = 1.0f;
+        if (p.w_post) {
+            float ss = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-                if (c >= C8) continue;
-                float g[8], w[8];
-                gate8<BF16>(p, row, c, g);
-                if (p.w_post) {
-                    unpack8<BF16>(p.w_post[c], w);
+                if (static_cast<int32_t>(threadIdx.x + i * blockDim.x) >= C8) continue;
+                float y[8];
+                pipe.template read<BF16>(in.y, i, y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[i][e] = y[i][e] * r * w[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] = fmaf(p.alpha, g[e] * y[i][e], h[i][e]);
-                p.h_out[row * C8 + c] = pack8<BF16>(h[i]);
+                for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
             }
+            r = rsqrtf(cta_sum(ss, slots, slot) * inv_c + p.eps);
+            if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = r;
         }
-        if (!p.w_pre) continue;
         float ss = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
+            if (c >= C8) continue;
+            pipe.template read<BF16>(in.h, i, h[i]);
+            if (p.y) {
+                float y[8], g[8];
+                pipe.template read<BF16>(in.y, i, y);
+                gate8<BF16>(p, ch, pipe, token, i, g);
+                if (p.w_post) {
+                    float w[8];
+                    unpack8<BF16>(ch.w_post[i], w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[i][e] = fmaf(p.alpha, g[e] * y[e], h[i][e]);
+                p.h_out[row * C8 + c] = pack8<BF16>(h[i]);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
-        const float r = rsqrtf(cta_sum(ss, slots, slot) * inv_c + p.eps);
+        }
+        if (!p.w_pre) continue;
+        r = rsqrtf(cta_sum(ss, slots, slot) * inv_c + p.eps);
         if (p.rstd_pre && threadIdx.x == 0) p.rstd_pre[row] = r;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-            float x[8] = {};
-            if (c < C8) {
-                float w[8];
-                unpack8<BF16>(p.w_pre[c], w);
+            float x[8], w[8];
+            unpack8<BF16>(ch.w_pre[i], w);   // zeros past the last channel
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = h[i][e] * r * w[e];
-            }
+            for (int e = 0; e < 8; ++e) x[e] = h[i][e] * r * w[e];
             if (p.x) {
                 if (c < C8) p.x[row * C8 + c] = pack8<BF16>(x);
                 continue;
             }
             uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, magnitude_bits(x[e]));
+            for (int e = 0; e < 8; ++e) m = max(m, c < C8 ? magnitude_bits(x[e]) : 0u);
             const BlockScale b = block_scale(__uint_as_float(half_warp_max(m)));
             if (c < C8) {
 #pragma unroll
@@ -160,108 +268,128 @@ norm_forward_kernel(const NormArgs p) {
 // g; and with a per-channel gate both dw_post = g S and dgate = w_post S come
 // from the one column sum S = sum alpha t m.  So a row needs two sums and a
 // column two accumulators.  h' is recomputed from h and y, unrounded.
-// A CTA walks rows blockIdx.x, + gridDim.x, ... with the column accumulators
-// in registers, and leaves them in `partial` [CTA][2][C]; the second kernel
+// The column accumulators are left in `partial` [CTA][2][C]; the second kernel
 // adds them in CTA order, so the sums are the same from run to run.
-template <bool BF16, int V>
-__global__ void __launch_bounds__(V == 1 ? 512 : 1024)
-norm_backward_kernel(const NormArgs p) {
+template <bool BF16, int V, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS, 1)
+norm_backward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ RowInputs in) {
+    extern __shared__ uint4 ring[];
     __shared__ float slots[2][kMaxWarps];
     grid_launch_dependents();
     grid_dependency_wait();
-    uint32_t slot = 0;
     const int32_t C8 = p.C8;
     const float inv_c = 1.0f / (8.0f * static_cast<float>(C8));
+    uint32_t slot = 0;
+    RowPipe<V> pipe(in, ring, C8);
+    pipe.issue(blockIdx.x, p.T, 0);
+    // The row's two factors and its gate, one row ahead like its operands.
+    float token_next, ry_next, rh_next;
+    auto fetch = [&](int64_t row) {
+        token_next = token_gate<BF16>(p, row);
+        ry_next = p.w_post && row < p.T ? p.rstd_post[row] : 1.0f;
+        rh_next = p.w_pre && row < p.T ? p.rstd_pre[row] : 1.0f;
+    };
+    fetch(blockIdx.x);
+    const Channels<V> ch(p);
+    // With a gate that is one number per row, c2 below leaves it out.
+    const bool g_row = p.gate_mode == kGateNone || p.gate_mode == kGateToken;
     float col_a[V][8] = {}, col_b[V][8] = {};
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-        const float ry = p.w_post ? p.rstd_post[row] : 1.0f;
-        const float rh = p.w_pre ? p.rstd_pre[row] : 1.0f;
+    for (int64_t row = blockIdx.x; row < p.T; pipe.end(row + gridDim.x, p.T), row += gridDim.x) {
+        pipe.begin(row + gridDim.x, p.T);
+        const float token = token_next, ry = ry_next, rh = rh_next;
+        fetch(row + gridDim.x);
         float u[V][8], t[V][8], n[V][8];
-        float sum1 = 0.0f;
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-            const bool in = c < C8;
-            float hv[8], g[8], w[8];
-            unpack8<BF16>(in ? p.h[row * C8 + c] : z, hv);
-            unpack8<BF16>(in && p.y ? p.y[row * C8 + c] : z, u[i]);
-            unpack8<BF16>(in && p.dh ? p.dh[row * C8 + c] : z, t[i]);
-            if (p.w_post) {
-                unpack8<BF16>(in ? p.w_post[c] : z, w);
+            if (static_cast<int32_t>(threadIdx.x + i * blockDim.x) >= C8) continue;
+            float w[8];
+            if (in.y >= 0) {
+                pipe.template read<BF16>(in.y, i, u[i]);
+                if (p.w_post) {
+                    unpack8<BF16>(ch.w_post[i], w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[i][e] = u[i][e] * ry * w[e];
+                    for (int e = 0; e < 8; ++e) u[i][e] = u[i][e] * ry * w[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[i][e] = 0.0f;
+            }
+            if (in.dh >= 0) {
+                pipe.template read<BF16>(in.dh, i, t[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[i][e] = 0.0f;
             }
             if (p.w_pre) {
-                float dx[8];
-                if (in) gate8<BF16>(p, row, c, g);
-                unpack8<BF16>(in ? p.dx[row * C8 + c] : z, dx);
-                unpack8<BF16>(in ? p.w_pre[c] : z, w);
+                float dx[8], g[8];
+                pipe.template read<BF16>(in.h, i, n[i]);
+                gate8<BF16>(p, ch, pipe, token, i, g);
+                pipe.template read<BF16>(in.dx, i, dx);
+                unpack8<BF16>(ch.w_pre[i], w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float h2 = in ? fmaf(p.alpha, g[e] * u[i][e], hv[e]) : 0.0f;
-                    n[i][e] = h2 * rh;
+                    n[i][e] = fmaf(p.alpha, g[e] * u[i][e], n[i][e]) * rh;
                     col_b[i][e] = fmaf(dx[e], n[i][e], col_b[i][e]);
-                    sum1 = fmaf(dx[e] * w[e], n[i][e], sum1);
-                    t[i][e] = fmaf(rh, dx[e] * w[e], t[i][e]);
+                    dx[e] *= w[e];
+                    sum = fmaf(dx[e], n[i][e], sum);
+                    t[i][e] = fmaf(rh, dx[e], t[i][e]);
                 }
             }
         }
-        if (p.w_pre) {
-            const float c1 = cta_sum(sum1, slots, slot) * inv_c;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[i][e] = fmaf(-rh * c1, n[i][e], t[i][e]);
-        }
-        // sum of alpha t u (times g, where g differs within the row)
-        float sum2 = 0.0f;
-        const bool g_row = p.gate_mode == kGateNone || p.gate_mode == kGateToken;
+        float c1 = 0.0f;
+        if (p.w_pre) c1 = -rh * (cta_sum(sum, slots, slot) * inv_c);
+        // t, and the sum of alpha t u (times g, where g differs within the row)
+        sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
             if (c >= C8) continue;
-            p.dh_in[row * C8 + c] = pack8<BF16>(t[i]);
-            if (!p.y) continue;
-            float g[8];
-            gate8<BF16>(p, row, c, g);
+            if (p.w_pre) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum2 = fmaf(p.alpha * t[i][e], g_row ? u[i][e] : g[e] * u[i][e], sum2);
+                for (int e = 0; e < 8; ++e) t[i][e] = fmaf(c1, n[i][e], t[i][e]);
+            }
+            p.dh_in[row * C8 + c] = pack8<BF16>(t[i]);
+            if (in.y < 0) continue;
+            float g[8];
+            gate8<BF16>(p, ch, pipe, token, i, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                t[i][e] *= p.alpha;
+                sum = fmaf(t[i][e], g_row ? u[i][e] : g[e] * u[i][e], sum);
+            }
         }
-        if (!p.y) continue;
+        if (in.y < 0) continue;
         float c2 = 0.0f;
         if (p.w_post || p.gate_mode == kGateToken) {
-            c2 = cta_sum(sum2, slots, slot);
-            if (p.gate_mode == kGateToken) {
-                if (threadIdx.x == 0) static_cast<float*>(p.dgate)[row] = c2;
-                c2 *= to_float<BF16>(static_cast<const uint16_t*>(p.gate)[row]);
-            }
-            c2 *= inv_c;
+            c2 = cta_sum(sum, slots, slot);
+            if (p.gate_mode == kGateToken && threadIdx.x == 0)
+                static_cast<float*>(p.dgate)[row] = c2;
+            c2 *= token * inv_c;   // (a per-row gate's factor; else 1)
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
             if (c >= C8) continue;
             float g[8], w[8], m[8], dy[8], dg[8];
-            gate8<BF16>(p, row, c, g);
-            unpack8<BF16>(p.y[row * C8 + c], m);
-            if (p.w_post) unpack8<BF16>(p.w_post[c], w);
+            gate8<BF16>(p, ch, pipe, token, i, g);
+            pipe.template read<BF16>(in.y, i, m);
+            if (p.w_post) unpack8<BF16>(ch.w_post[i], w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float at = p.alpha * t[i][e];
-                dg[e] = at * u[i][e];
-                const float du = at * g[e];
+                dg[e] = t[i][e] * u[i][e];
+                const float du = t[i][e] * g[e];
+                dy[e] = du;
                 if (p.w_post) {
                     m[e] *= ry;
                     dy[e] = ry * (du * w[e] - m[e] * c2);
-                } else {
-                    dy[e] = du;
                 }
-                col_a[i][e] = fmaf(p.gate_mode == kGateChannel ? at : du, m[e], col_a[i][e]);
+                col_a[i][e] =
+                    fmaf(p.gate_mode == kGateChannel ? t[i][e] : du, m[e], col_a[i][e]);
             }
             p.dy[row * C8 + c] = pack8<BF16>(dy);
-            if (p.gate_mode == kGateElement) static_cast<uint4*>(p.dgate)[row * C8 + c] = pack8<BF16>(dg);
+            if (p.gate_mode == kGateElement)
+                static_cast<uint4*>(p.dgate)[row * C8 + c] = pack8<BF16>(dg);
         }
     }
     float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 16 * C8;
@@ -270,9 +398,11 @@ norm_backward_kernel(const NormArgs p) {
         const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
         if (c >= C8) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            part[8 * c + e] = col_a[i][e];
-            part[8 * (C8 + c) + e] = col_b[i][e];
+        for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4*>(part + 8 * c + e) =
+                make_float4(col_a[i][e], col_a[i][e + 1], col_a[i][e + 2], col_a[i][e + 3]);
+            *reinterpret_cast<float4*>(part + 8 * (C8 + c) + e) =
+                make_float4(col_b[i][e], col_b[i][e + 1], col_b[i][e + 2], col_b[i][e + 3]);
         }
     }
 }
@@ -311,32 +441,67 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormArgs p, int
             p.w_post ? v * to_float<BF16>(reinterpret_cast<const uint16_t*>(p.w_post)[col]) : v;
 }
 
-unsigned row_threads(int64_t C8, int V) {
-    return static_cast<unsigned>(((C8 + V - 1) / V + 31) / 32 * 32);
+// Threads of a CTA whose threads own V vectors of each row.
+int row_threads(int64_t C8, int V) {
+    return static_cast<int>(((C8 + V - 1) / V + 31) / 32 * 32);
+}
+
+RowInputs row_inputs(const NormArgs& p, bool backward) {
+    RowInputs in{};
+    auto add = [&](const void* q) {
+        if (!q) return -1;
+        in.base[in.n] = static_cast<const uint4*>(q);
+        return in.n++;
+    };
+    in.h = add(!backward || p.w_pre ? p.h : nullptr);   // dh' alone needs no h
+    in.y = add(p.y);
+    in.gate = add(p.gate_mode == kGateElement ? p.gate : nullptr);
+    in.dh = add(backward ? p.dh : nullptr);
+    in.dx = add(backward ? p.dx : nullptr);
+    return in;
+}
+
+template <class K>
+cudaError_t launch_rows(K kernel, ContextMarks& done, const NormArgs& p, RowInputs in,
+                        int64_t ctas, int threads, int V, bool pdl, cudaStream_t stream) {
+    constexpr int kMost = 227 * 1024 - 1024;   // dynamic shared memory, beside the static
+    const int row = in.n * V * threads * 16;   // at most 160 KB (five operands, 16384 channels)
+    in.stages = 2 * row <= kMost ? 2 : 1;
+    const size_t smem = static_cast<size_t>(in.stages) * row;
+    if (cudaError_t e = smem_opt_in(kernel, kMost, done, false)) return e;
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)),
+                         dim3(static_cast<unsigned>(threads)), smem, stream, 1, pdl, p, in);
 }
 
 template <bool BF16>
 cudaError_t forward_typed(const NormArgs& p, int sms, bool pdl, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>(p.T < (1 << 30) ? p.T : (1 << 30));
-    const bool one = p.C8 <= 1024 && (p.C8 <= 128 || p.T <= 2 * sms);
-    if (one)
-        return launch_kernel(norm_forward_kernel<BF16, 1>, dim3(grid), dim3(row_threads(p.C8, 1)),
-                             0, stream, 1, pdl, p);
-    return launch_kernel(norm_forward_kernel<BF16, 2>, dim3(grid), dim3(row_threads(p.C8, 2)), 0,
-                         stream, 1, pdl, p);
+    const RowInputs in = row_inputs(p, false);
+    // Few rows: a vector per thread, the shortest time for one row.
+    static ContextMarks done1, done512, done1024;
+    if (p.C8 <= 1024 && (p.C8 <= 32 || p.T <= sms))
+        return launch_rows(norm_forward_kernel<BF16, 1, 1024>, done1, p, in,
+                           p.T < 8 * sms ? p.T : 8 * sms, row_threads(p.C8, 1), 1, pdl, stream);
+    const int threads = row_threads(p.C8, 2);
+    const int64_t most = static_cast<int64_t>(sms) * (threads < 1024 ? 1024 / threads : 1);
+    const int64_t ctas = p.T < most ? p.T : most;
+    return threads <= 512 ? launch_rows(norm_forward_kernel<BF16, 2, 512>, done512, p, in, ctas,
+                                        threads, 2, pdl, stream)
+                          : launch_rows(norm_forward_kernel<BF16, 2, 1024>, done1024, p, in, ctas,
+                                        threads, 2, pdl, stream);
 }
 
 template <bool BF16>
-cudaError_t backward_typed(const NormArgs& p, int ctas, bool pdl, cudaStream_t stream) {
+cudaError_t backward_typed(const NormArgs& p, int sms, bool pdl, cudaStream_t stream) {
+    const int ctas = norm_backward_ctas(p.T, 8ll * p.C8, sms);
+    const int threads = row_threads(p.C8, 2);
+    const RowInputs in = row_inputs(p, true);
+    static ContextMarks done512, done1024;
     cudaError_t e = cudaSuccess;
-    if (ctas == 0) {
-        // no rows: the column sums below come out as zeros
-    } else if (p.C8 <= 512)
-        e = launch_kernel(norm_backward_kernel<BF16, 1>, dim3(ctas), dim3(row_threads(p.C8, 1)), 0,
-                          stream, 1, pdl, p);
-    else
-        e = launch_kernel(norm_backward_kernel<BF16, 2>, dim3(ctas), dim3(row_threads(p.C8, 2)), 0,
-                          stream, 1, pdl, p);
+    if (ctas > 0)   // (no rows: the column sums come out as zeros)
+        e = threads <= 512 ? launch_rows(norm_backward_kernel<BF16, 2, 512>, done512, p, in, ctas,
+                                         threads, 2, pdl, stream)
+                           : launch_rows(norm_backward_kernel<BF16, 2, 1024>, done1024, p, in, ctas,
+                                         threads, 2, pdl, stream);
     const bool columns = p.dw_pre || p.dw_post || p.gate_mode == kGateChannel;
     if (e != cudaSuccess || !columns) return e;
     return launch_kernel(norm_columns_kernel<BF16>, dim3((16 * p.C8 + 31) / 32), dim3(256), 0,
@@ -345,8 +510,9 @@ cudaError_t backward_typed(const NormArgs& p, int ctas, bool pdl, cudaStream_t s
 
 }  // namespace
 
-int norm_backward_ctas(int64_t T, int sms) {
-    const int64_t most = 2 * static_cast<int64_t>(sms);
+int norm_backward_ctas(int64_t T, int64_t C, int sms) {
+    const int threads = row_threads(C / 8, 2);
+    const int64_t most = static_cast<int64_t>(sms) * (threads < 512 ? 512 / threads : 1);
     return static_cast<int>(T < most ? T : most);
 }
 
@@ -358,9 +524,8 @@ cudaError_t launch_norm_forward(const NormArgs& p, bool bf16, int sms, bool pdl,
 
 cudaError_t launch_norm_backward(const NormArgs& p, bool bf16, int sms, bool pdl,
                                  cudaStream_t stream) {
-    const int ctas = norm_backward_ctas(p.T, sms);
-    return bf16 ? backward_typed<true>(p, ctas, pdl, stream)
-                : backward_typed<false>(p, ctas, pdl, stream);
+    return bf16 ? backward_typed<true>(p, sms, pdl, stream)
+                : backward_typed<false>(p, sms, pdl, stream);
 }
 
 }  // namespace tmagemm
