@@ -172,8 +172,8 @@ __device__ __forceinline__ float token_gate(const NormArgs& p, int64_t row) {
 
 // The 16 lanes of a half warp hold one 128-channel block, so its largest
 // magnitude takes four shuffles.
-template <bool BF16, int V, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS, 1)
+template <bool BF16, int V, int MAX_THREADS, int MIN_CTAS>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
 norm_forward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ RowInputs in) {
     extern __shared__ uint4 ring[];
     __shared__ float slots[2][kMaxWarps];
@@ -270,9 +270,13 @@ norm_forward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ 
 // column two accumulators.  h' is recomputed from h and y, unrounded.
 // The column accumulators are left in `partial` [CTA][2][C]; the second kernel
 // adds them in CTA order, so the sums are the same from run to run.
-template <bool BF16, int V, int MAX_THREADS>
+// POST (w_post given) and GATE are fixed at compile time: read at run time they
+// cost half as many instructions again.
+template <bool BF16, bool POST, int GATE, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS, 1)
 norm_backward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ RowInputs in) {
+    constexpr int V = 2;
+    constexpr bool kTokenLike = GATE == kGateNone || GATE == kGateToken;   // one gate per row
     extern __shared__ uint4 ring[];
     __shared__ float slots[2][kMaxWarps];
     grid_launch_dependents();
@@ -283,53 +287,50 @@ norm_backward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__
     RowPipe<V> pipe(in, ring, C8);
     pipe.issue(blockIdx.x, p.T, 0);
     // The row's two factors and its gate, one row ahead like its operands.
-    float token_next, ry_next, rh_next;
+    float token_next = 1.0f, ry_next = 1.0f, rh_next = 1.0f;
     auto fetch = [&](int64_t row) {
-        token_next = token_gate<BF16>(p, row);
-        ry_next = p.w_post && row < p.T ? p.rstd_post[row] : 1.0f;
-        rh_next = p.w_pre && row < p.T ? p.rstd_pre[row] : 1.0f;
+        if (row >= p.T) return;
+        if constexpr (GATE == kGateToken) token_next = token_gate<BF16>(p, row);
+        if constexpr (POST) ry_next = p.rstd_post[row];
+        if (p.w_pre) rh_next = p.rstd_pre[row];
     };
     fetch(blockIdx.x);
     const Channels<V> ch(p);
-    // With a gate that is one number per row, c2 below leaves it out.
-    const bool g_row = p.gate_mode == kGateNone || p.gate_mode == kGateToken;
     float col_a[V][8] = {}, col_b[V][8] = {};
     for (int64_t row = blockIdx.x; row < p.T; pipe.end(row + gridDim.x, p.T), row += gridDim.x) {
         pipe.begin(row + gridDim.x, p.T);
-        const float token = token_next, ry = ry_next, rh = rh_next;
+        // alpha times the row's gate where that is one number
+        const float ry = ry_next, rh = rh_next, ag = p.alpha * token_next;
         fetch(row + gridDim.x);
-        float u[V][8], t[V][8], n[V][8];
+        // alpha g of vector i
+        auto scaled_gate = [&](int i, float (&g)[8]) {
+            if constexpr (GATE == kGateChannel) unpack8<BF16>(ch.gate[i], g);
+            if constexpr (GATE == kGateElement) pipe.template read<BF16>(in.gate, i, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = kTokenLike ? ag : p.alpha * g[e];
+        };
+        float u[V][8] = {}, t[V][8] = {}, n[V][8];
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             if (static_cast<int32_t>(threadIdx.x + i * blockDim.x) >= C8) continue;
             float w[8];
-            if (in.y >= 0) {
-                pipe.template read<BF16>(in.y, i, u[i]);
-                if (p.w_post) {
-                    unpack8<BF16>(ch.w_post[i], w);
+            if (POST || in.y >= 0) pipe.template read<BF16>(in.y, i, u[i]);
+            if constexpr (POST) {
+                unpack8<BF16>(ch.w_post[i], w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) u[i][e] = u[i][e] * ry * w[e];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[i][e] = 0.0f;
+                for (int e = 0; e < 8; ++e) u[i][e] *= ry * w[e];
             }
-            if (in.dh >= 0) {
-                pipe.template read<BF16>(in.dh, i, t[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t[i][e] = 0.0f;
-            }
+            if (in.dh >= 0) pipe.template read<BF16>(in.dh, i, t[i]);
             if (p.w_pre) {
                 float dx[8], g[8];
                 pipe.template read<BF16>(in.h, i, n[i]);
-                gate8<BF16>(p, ch, pipe, token, i, g);
+                scaled_gate(i, g);
                 pipe.template read<BF16>(in.dx, i, dx);
                 unpack8<BF16>(ch.w_pre[i], w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    n[i][e] = fmaf(p.alpha, g[e] * u[i][e], n[i][e]) * rh;
+                    n[i][e] = fmaf(g[e], u[i][e], n[i][e]) * rh;
                     col_b[i][e] = fmaf(dx[e], n[i][e], col_b[i][e]);
                     dx[e] *= w[e];
                     sum = fmaf(dx[e], n[i][e], sum);
@@ -339,7 +340,7 @@ norm_backward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__
         }
         float c1 = 0.0f;
         if (p.w_pre) c1 = -rh * (cta_sum(sum, slots, slot) * inv_c);
-        // t, and the sum of alpha t u (times g, where g differs within the row)
+        // t, and the sum of t u (times alpha g where g differs within the row)
         sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -350,46 +351,51 @@ norm_backward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__
                 for (int e = 0; e < 8; ++e) t[i][e] = fmaf(c1, n[i][e], t[i][e]);
             }
             p.dh_in[row * C8 + c] = pack8<BF16>(t[i]);
-            if (in.y < 0) continue;
-            float g[8];
-            gate8<BF16>(p, ch, pipe, token, i, g);
+            if constexpr (kTokenLike) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t[i][e] *= p.alpha;
-                sum = fmaf(t[i][e], g_row ? u[i][e] : g[e] * u[i][e], sum);
+                for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e], u[i][e], sum);
+            } else if constexpr (POST) {
+                float g[8];
+                scaled_gate(i, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e] * g[e], u[i][e], sum);
             }
         }
-        if (in.y < 0) continue;
+        if (!POST && in.y < 0) continue;
         float c2 = 0.0f;
-        if (p.w_post || p.gate_mode == kGateToken) {
+        if constexpr (POST || GATE == kGateToken) {
             c2 = cta_sum(sum, slots, slot);
-            if (p.gate_mode == kGateToken && threadIdx.x == 0)
-                static_cast<float*>(p.dgate)[row] = c2;
-            c2 *= token * inv_c;   // (a per-row gate's factor; else 1)
+            if (GATE == kGateToken && threadIdx.x == 0)
+                static_cast<float*>(p.dgate)[row] = p.alpha * c2;
+            c2 *= -inv_c * ry * ry * (kTokenLike ? ag : 1.0f);
         }
+        // dy = ry (du w_post - (y ry) mean(q m)), the last product through c2
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
             if (c >= C8) continue;
-            float g[8], w[8], m[8], dy[8], dg[8];
-            gate8<BF16>(p, ch, pipe, token, i, g);
-            pipe.template read<BF16>(in.y, i, m);
-            if (p.w_post) unpack8<BF16>(ch.w_post[i], w);
+            float g[8], w[8], y[8], out[8];
+            scaled_gate(i, g);
+            if constexpr (GATE == kGateElement) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) out[e] = p.alpha * t[i][e] * u[i][e];
+                static_cast<uint4*>(p.dgate)[row * C8 + c] = pack8<BF16>(out);
+            }
+            if constexpr (POST) unpack8<BF16>(ch.w_post[i], w);
+            pipe.template read<BF16>(in.y, i, y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                dg[e] = t[i][e] * u[i][e];
-                const float du = t[i][e] * g[e];
-                dy[e] = du;
-                if (p.w_post) {
-                    m[e] *= ry;
-                    dy[e] = ry * (du * w[e] - m[e] * c2);
+                out[e] = t[i][e] * g[e];   // du
+                // (a column of a per-channel gate's du m, without the gate)
+                const float s = GATE == kGateChannel ? p.alpha * t[i][e] : out[e];
+                if constexpr (POST) {
+                    col_a[i][e] = fmaf(s * ry, y[e], col_a[i][e]);
+                    out[e] = fmaf(out[e] * ry, w[e], c2 * y[e]);
+                } else if constexpr (GATE == kGateChannel) {
+                    col_a[i][e] = fmaf(s, y[e], col_a[i][e]);
                 }
-                col_a[i][e] =
-                    fmaf(p.gate_mode == kGateChannel ? t[i][e] : du, m[e], col_a[i][e]);
             }
-            p.dy[row * C8 + c] = pack8<BF16>(dy);
-            if (p.gate_mode == kGateElement)
-                static_cast<uint4*>(p.dgate)[row * C8 + c] = pack8<BF16>(dg);
+            p.dy[row * C8 + c] = pack8<BF16>(out);
         }
     }
     float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 16 * C8;
@@ -407,27 +413,38 @@ norm_backward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__
     }
 }
 
-// Column sums of the partials, in CTA order: 32 columns x 8 slices of the CTAs
-// per block, the slices added in order.
+// Column sums of the partials in a fixed order: 32 columns x 32 slices of the
+// CTAs per block, each slice a run of CTAs read eight at a time, the slices
+// added in order.
+constexpr int kSlices = 32;
+
 template <bool BF16>
-__global__ void __launch_bounds__(256) norm_columns_kernel(const NormArgs p, int32_t ctas) {
-    __shared__ float s[8][32];
+__global__ void __launch_bounds__(32 * kSlices) norm_columns_kernel(const NormArgs p,
+                                                                    int32_t ctas) {
+    __shared__ float s[kSlices][32];
     grid_launch_dependents();
     grid_dependency_wait();
     const int32_t C = 8 * p.C8;
     const int lane = static_cast<int>(threadIdx.x) & 31, slice = static_cast<int>(threadIdx.x) >> 5;
     const int32_t col = static_cast<int32_t>(blockIdx.x) * 32 + lane;   // 0 .. 2 C
-    const int32_t per = (ctas + 7) / 8;
+    const int32_t per = (ctas + kSlices - 1) / kSlices;
+    const int32_t end = min(ctas, (slice + 1) * per);
     float v = 0.0f;
     if (col < 2 * C)
-        for (int32_t i = slice * per; i < min(ctas, (slice + 1) * per); ++i)
-            v += p.partial[static_cast<int64_t>(i) * 2 * C + col];
+        for (int32_t i = slice * per; i < end; i += 8) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = i + k < end ? p.partial[static_cast<int64_t>(i + k) * 2 * C + col] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += x[k];
+        }
     s[slice][lane] = v;
     __syncthreads();
     if (slice != 0 || col >= 2 * C) return;
     v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += s[i][lane];
+    for (int i = 0; i < kSlices; ++i) v += s[i][lane];
     if (col >= C) {
         if (p.dw_pre) p.dw_pre[col - C] = v;
         return;
@@ -477,35 +494,62 @@ template <bool BF16>
 cudaError_t forward_typed(const NormArgs& p, int sms, bool pdl, cudaStream_t stream) {
     const RowInputs in = row_inputs(p, false);
     // Few rows: a vector per thread, the shortest time for one row.
-    static ContextMarks done1, done512, done1024;
+    static ContextMarks done1, done256, done512, done1024;
     if (p.C8 <= 1024 && (p.C8 <= 32 || p.T <= sms))
-        return launch_rows(norm_forward_kernel<BF16, 1, 1024>, done1, p, in,
+        return launch_rows(norm_forward_kernel<BF16, 1, 1024, 1>, done1, p, in,
                            p.T < 8 * sms ? p.T : 8 * sms, row_threads(p.C8, 1), 1, pdl, stream);
+    // Two CTAs of 256 threads with 128 registers, or two of 512 with 64: at 8192
+    // x 4096 55 us against 66 us for four of 256 with 64 registers, at 4096 x
+    // 8192 43 us against 50 us for one of 512 with 128.
     const int threads = row_threads(p.C8, 2);
-    const int64_t most = static_cast<int64_t>(sms) * (threads < 1024 ? 1024 / threads : 1);
+    const int64_t most = static_cast<int64_t>(sms) * (threads < 256 ? 512 / threads
+                                                      : threads <= 512 ? 2 : 1);
     const int64_t ctas = p.T < most ? p.T : most;
-    return threads <= 512 ? launch_rows(norm_forward_kernel<BF16, 2, 512>, done512, p, in, ctas,
-                                        threads, 2, pdl, stream)
-                          : launch_rows(norm_forward_kernel<BF16, 2, 1024>, done1024, p, in, ctas,
-                                        threads, 2, pdl, stream);
+    if (threads <= 256)
+        return launch_rows(norm_forward_kernel<BF16, 2, 256, 2>, done256, p, in, ctas, threads, 2,
+                           pdl, stream);
+    if (threads <= 512)
+        return launch_rows(norm_forward_kernel<BF16, 2, 512, 2>, done512, p, in, ctas, threads, 2,
+                           pdl, stream);
+    return launch_rows(norm_forward_kernel<BF16, 2, 1024, 1>, done1024, p, in, ctas, threads, 2,
+                       pdl, stream);
+}
+
+template <bool BF16, bool POST, int GATE>
+cudaError_t backward_rows(const NormArgs& p, int64_t ctas, int threads, bool pdl,
+                          cudaStream_t stream) {
+    const RowInputs in = row_inputs(p, true);
+    static ContextMarks done512, done1024;
+    if (threads <= 512)
+        return launch_rows(norm_backward_kernel<BF16, POST, GATE, 512>, done512, p, in, ctas,
+                           threads, 2, pdl, stream);
+    return launch_rows(norm_backward_kernel<BF16, POST, GATE, 1024>, done1024, p, in, ctas,
+                       threads, 2, pdl, stream);
+}
+
+template <bool BF16, bool POST>
+cudaError_t backward_gated(const NormArgs& p, int64_t ctas, int threads, bool pdl,
+                           cudaStream_t stream) {
+    switch (p.gate_mode) {
+        case kGateChannel: return backward_rows<BF16, POST, kGateChannel>(p, ctas, threads, pdl, stream);
+        case kGateToken: return backward_rows<BF16, POST, kGateToken>(p, ctas, threads, pdl, stream);
+        case kGateElement: return backward_rows<BF16, POST, kGateElement>(p, ctas, threads, pdl, stream);
+        default: return backward_rows<BF16, POST, kGateNone>(p, ctas, threads, pdl, stream);
+    }
 }
 
 template <bool BF16>
 cudaError_t backward_typed(const NormArgs& p, int sms, bool pdl, cudaStream_t stream) {
     const int ctas = norm_backward_ctas(p.T, 8ll * p.C8, sms);
     const int threads = row_threads(p.C8, 2);
-    const RowInputs in = row_inputs(p, true);
-    static ContextMarks done512, done1024;
     cudaError_t e = cudaSuccess;
     if (ctas > 0)   // (no rows: the column sums come out as zeros)
-        e = threads <= 512 ? launch_rows(norm_backward_kernel<BF16, 2, 512>, done512, p, in, ctas,
-                                         threads, 2, pdl, stream)
-                           : launch_rows(norm_backward_kernel<BF16, 2, 1024>, done1024, p, in, ctas,
-                                         threads, 2, pdl, stream);
+        e = p.w_post ? backward_gated<BF16, true>(p, ctas, threads, pdl, stream)
+                     : backward_gated<BF16, false>(p, ctas, threads, pdl, stream);
     const bool columns = p.dw_pre || p.dw_post || p.gate_mode == kGateChannel;
     if (e != cudaSuccess || !columns) return e;
-    return launch_kernel(norm_columns_kernel<BF16>, dim3((16 * p.C8 + 31) / 32), dim3(256), 0,
-                         stream, 1, pdl, p, static_cast<int32_t>(ctas));
+    return launch_kernel(norm_columns_kernel<BF16>, dim3((16 * p.C8 + 31) / 32),
+                         dim3(32 * kSlices), 0, stream, 1, pdl, p, static_cast<int32_t>(ctas));
 }
 
 }  // namespace
