@@ -707,7 +707,7 @@ int quantize_fp8(int64_t M, int64_t K, const void* X, int bf16, int block_rows, 
     DeviceState* d = nullptr;
     if (int s = device_state(&d)) return s;
     return launch_quantize(M, K, X, bf16 != 0, block_rows, Q, S, s_row_stride, s_block_stride,
-                           process_tuning().pdl(),
+                           d->sms, process_tuning().pdl(),
                            static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TMAGEMM_OK
                : TMAGEMM_ERR_CUDA;

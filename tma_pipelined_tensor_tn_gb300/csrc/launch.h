@@ -181,7 +181,7 @@ cudaError_t launch_gemv(int64_t N, int64_t K, const void* x, const void* W, void
 // Block quantisation to e4m3 (quantize.cu): X (M x K) -> codes Q and scales
 // S[row * s_row + block * s_blk], one per block_rows (1 or 128) x 128 values.
 cudaError_t launch_quantize(int64_t M, int64_t K, const void* X, bool bf16, int block_rows,
-                            void* Q, float* S, int64_t s_row, int64_t s_blk, bool pdl,
+                            void* Q, float* S, int64_t s_row, int64_t s_blk, int sms, bool pdl,
                             cudaStream_t stream);
 
 // Block-scaled e4m3 product (gemm_fp8.cu).  offsets != nullptr: grouped, with
