@@ -15,10 +15,14 @@ from __future__ import annotations
 import ctypes
 from typing import NamedTuple, Optional
 
+import torch
+
 from ._binding import TMAGEMM_OK, TmaGemmError, TmagemmNorm, lib
 
 FP8_BLOCK = 128
 _GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_ELEMENT = range(4)
+_F8, _F32 = torch.float8_e4m3fn, torch.float32
+_IS_BF16 = {torch.bfloat16: 1, torch.float16: 0}
 
 
 def _blocks(n: int) -> int:
@@ -28,7 +32,6 @@ def _blocks(n: int) -> int:
 def _launch(device, stream, inputs, body):
     """body(handle) with `device` current and, for an explicit stream, that
     stream current too, so that the results body() allocates belong to it."""
-    import torch
     if stream is None:
         if device.index == torch.cuda.current_device():
             # The raw handle: a Stream object costs as much as a launch.
@@ -46,32 +49,34 @@ def _launch(device, stream, inputs, body):
 
 
 def _check(name, t, dtype, shape, device, contiguous=True):
-    import torch
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device
+            and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (row-major)")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous (row-major)")
 
 
-def _matrix(name, t, dims=2):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dim() != dims:
-        raise TypeError(f"{name} must be a CUDA tensor of {dims} dimensions")
+def _first(name, t, dims):
+    """The device of a call's first operand: a CUDA tensor of `dims` dimensions."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return t.device
 
 
 def _bf16(dtype) -> int:
-    import torch
-    if dtype == torch.bfloat16:
-        return 1
-    if dtype == torch.float16:
-        return 0
-    raise TypeError(f"the type must be torch.float16 or torch.bfloat16, got {dtype}")
+    flag = _IS_BF16.get(dtype)
+    if flag is None:
+        raise TypeError(f"the type must be torch.float16 or torch.bfloat16, got {dtype}")
+    return flag
 
 
 def _raise(status, what):
@@ -87,23 +92,22 @@ def quantize_fp8(X, block_rows: int = 1, stream=None):
     scales are laid out with consecutive rows next to each other, the layout
     the products read fastest; weight scales are row-major.
     """
-    import torch
-    _matrix("X", X)
-    dtype, dev = X.dtype, X.device
-    bf16 = _bf16(dtype)
-    _check("X", X, dtype, None, dev)
+    dev = _first("X", X, 2)
+    bf16 = _bf16(X.dtype)
+    if not X.is_contiguous():
+        raise ValueError("X must be contiguous (row-major)")
     if block_rows not in (1, FP8_BLOCK):
         raise ValueError("block_rows must be 1 or 128")
     M, K = X.shape
     blocks = _blocks(K)
 
     def body(handle):
-        Q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        Q = torch.empty_like(X, dtype=_F8)
         if block_rows == 1:
-            S = torch.empty_strided((M, blocks), (1, max(M, 1)), dtype=torch.float32, device=dev)
+            S = torch.empty_strided((M, blocks), (1, max(M, 1)), dtype=_F32, device=dev)
             strides = 1, max(M, 1)
         else:
-            S = torch.empty((_blocks(M), blocks), dtype=torch.float32, device=dev)
+            S = torch.empty((_blocks(M), blocks), dtype=_F32, device=dev)
             strides = max(blocks, 1), 1
         _raise(lib().quantize_fp8(M, K, X.data_ptr(), bf16, block_rows, Q.data_ptr(),
                                   S.data_ptr(), *strides, handle), "quantize_fp8")
@@ -115,19 +119,17 @@ def quantize_fp8(X, block_rows: int = 1, stream=None):
 def _product(what, A, SA, B, SB, offsets, dtype, out, stream):
     """The checks, result and call that gemm_fp8 and gemm_fp8_grouped share;
     `offsets` None: dense."""
-    import torch
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     bf16 = _bf16(dtype)
-    f8, f32 = torch.float8_e4m3fn, torch.float32
+    dev = _first("A", A, 2)
     M, K = A.shape
-    N = B.shape[-2]
-    lead = tuple(B.shape[:-2])
-    dev = A.device
-    _check("A", A, f8, None, dev)
-    _check("B", B, f8, (*lead, N, K), dev)
-    _check("SA", SA, f32, (M, _blocks(K)), dev, contiguous=False)
-    _check("SB", SB, f32, (*lead, _blocks(N), _blocks(K)), dev)
+    *lead, N, _ = B.shape
+    blocks = _blocks(K)
+    _check("A", A, _F8, None, dev)
+    _check("B", B, _F8, (*lead, N, K), dev)
+    _check("SA", SA, _F32, (M, blocks), dev, contiguous=False)
+    _check("SB", SB, _F32, (*lead, _blocks(N), blocks), dev)
     if out is not None:
         _check("out", out, dtype, (M, N), dev)
     # A stride that is never stepped (a dimension of one) counts as 1.
@@ -159,8 +161,7 @@ def gemm_fp8(A, SA, B, SB, dtype=None, out=None, stream=None):
     any strides, SB (ceil(N / 128), ceil(K / 128)) float32, row-major.
     K % 16 == 0 and N % 8 == 0.
     """
-    _matrix("A", A)
-    _matrix("B", B)
+    _first("B", B, 2)
     return _product("gemm_fp8", A, SA, B, SB, None, dtype, out, stream)
 
 
@@ -173,10 +174,8 @@ def gemm_fp8_grouped(A, SA, B, SB, m_offsets, dtype=None, out=None, stream=None)
     (undefined in a new result).  A (M, K), B (G, N, K), SB (G, ceil(N / 128),
     ceil(K / 128)); the rest as for gemm_fp8.
     """
-    import torch
-    _matrix("A", A)
-    _matrix("B", B, 3)
-    _check("m_offsets", m_offsets, torch.int32, (B.shape[0] + 1,), A.device)
+    _first("B", B, 3)
+    _check("m_offsets", m_offsets, torch.int32, (B.shape[0] + 1,), B.device)
     return _product("gemm_fp8_grouped", A, SA, B, SB, m_offsets, dtype, out, stream)
 
 
@@ -200,34 +199,38 @@ class NormGrads(NamedTuple):
 
 def _norm_struct(h, y, gate, w_post, w_pre, alpha, eps):
     """The checked operands as a TmagemmNorm."""
-    _matrix("h", h)
-    T, C = h.shape
-    dt, dev = h.dtype, h.device
+    dev = _first("h", h, 2)
+    shape = T, C = h.shape
+    dt = h.dtype
     bf16 = _bf16(dt)
     _check("h", h, dt, None, dev)
     if y is None and (w_pre is None or w_post is not None or gate is not None):
         raise ValueError("without y there is neither w_post nor gate, and w_pre is needed")
-    ptr = [None, None, None]
-    for i, (name, t, shape) in enumerate((("y", y, h.shape), ("w_post", w_post, (C,)),
-                                          ("w_pre", w_pre, (C,)))):
-        if t is not None:
-            _check(name, t, dt, shape, dev)
-            ptr[i] = t.data_ptr()
-    mode, gate_ptr = _GATE_NONE, None
+    mode = _GATE_NONE
+    ptr = dict.fromkeys(("y", "w_post", "w_pre", "gate"))
+    if y is not None:
+        _check("y", y, dt, shape, dev)
+        ptr["y"] = y.data_ptr()
+    if w_post is not None:
+        _check("w_post", w_post, dt, (C,), dev)
+        ptr["w_post"] = w_post.data_ptr()
+    if w_pre is not None:
+        _check("w_pre", w_pre, dt, (C,), dev)
+        ptr["w_pre"] = w_pre.data_ptr()
     if gate is not None:
-        shape = tuple(gate.shape)
-        if shape == (T, C):
+        _check("gate", gate, dt, None, dev)
+        if gate.shape == shape:
             mode = _GATE_ELEMENT
-        elif shape == (C,) or shape == (1, C):
+        elif gate.shape == (C,) or gate.shape == (1, C):
             mode = _GATE_CHANNEL
-        elif shape == (T, 1):
+        elif gate.shape == (T, 1):
             mode = _GATE_TOKEN
         else:
-            raise ValueError(f"gate must be (C,), (1, C), (T, 1) or (T, C), got {shape}")
-        _check("gate", gate, dt, None, dev)
-        gate_ptr = gate.data_ptr()
-    return TmagemmNorm(T, C, bf16, mode, alpha, eps, h.data_ptr(), ptr[0], gate_ptr, ptr[1],
-                       ptr[2])
+            raise ValueError(f"gate must be (C,), (1, C), (T, 1) or (T, C), got "
+                             f"{tuple(gate.shape)}")
+        ptr["gate"] = gate.data_ptr()
+    return TmagemmNorm(T, C, bf16, mode, alpha, eps, h.data_ptr(), ptr["y"], ptr["gate"],
+                       ptr["w_post"], ptr["w_pre"])
 
 
 def norm_residual(h, y=None, gate=None, w_post=None, w_pre=None, alpha: float = 1.0,
@@ -243,13 +246,11 @@ def norm_residual(h, y=None, gate=None, w_post=None, w_pre=None, alpha: float = 
     ``quantize`` makes x float8_e4m3fn codes with row scales, the operands of
     gemm_fp8; ``save_rstd`` keeps the two rsqrt factors for the backward.
     """
-    import torch
     p = _norm_struct(h, y, gate, w_post, w_pre, alpha, eps)
     if quantize and w_pre is None:
         raise ValueError("quantize needs w_pre")
     T, C = h.shape
     dev = h.device
-    f32 = torch.float32
 
     def body(handle):
         h_out, x, scales, r_post, r_pre = h, None, None, None, None
@@ -257,18 +258,18 @@ def norm_residual(h, y=None, gate=None, w_post=None, w_pre=None, alpha: float = 
             h_out = torch.empty_like(h)
             p.h_out = h_out.data_ptr()
         if w_pre is not None and quantize:
-            x = torch.empty((T, C), dtype=torch.float8_e4m3fn, device=dev)
-            scales = torch.empty_strided((T, _blocks(C)), (1, max(T, 1)), dtype=f32, device=dev)
+            x = torch.empty_like(h, dtype=_F8)
+            scales = torch.empty_strided((T, _blocks(C)), (1, max(T, 1)), dtype=_F32, device=dev)
             p.q, p.scales, p.s_row_stride, p.s_block_stride = (
                 x.data_ptr(), scales.data_ptr(), 1, max(T, 1))
         elif w_pre is not None:
             x = torch.empty_like(h)
             p.x = x.data_ptr()
         if save_rstd and w_post is not None:
-            r_post = torch.empty((T,), dtype=f32, device=dev)
+            r_post = torch.empty((T,), dtype=_F32, device=dev)
             p.rstd_post = r_post.data_ptr()
         if save_rstd and w_pre is not None:
-            r_pre = torch.empty((T,), dtype=f32, device=dev)
+            r_pre = torch.empty((T,), dtype=_F32, device=dev)
             p.rstd_pre = r_pre.data_ptr()
         _raise(lib().norm_residual(ctypes.byref(p), handle), "norm_residual")
         return NormOut(h_out, x, scales, r_post, r_pre)
@@ -286,11 +287,9 @@ def norm_residual_backward(h, y=None, dh=None, dx=None, gate=None, w_post=None, 
     dh, dy and a (T, C) gate's gradient have the type of h; the weights' and the
     other gates' gradients are float32 sums.
     """
-    import torch
     p = _norm_struct(h, y, gate, w_post, w_pre, alpha, 0.0)
     T, C = h.shape
     dt, dev = h.dtype, h.device
-    f32 = torch.float32
     if (dx is None) != (w_pre is None):
         raise ValueError("dx is given if and only if w_pre is")
     for name, field, t in (("dh", "dh_out", dh), ("dx", "dx", dx)):
@@ -299,7 +298,7 @@ def norm_residual_backward(h, y=None, dh=None, dx=None, gate=None, w_post=None, 
             setattr(p, field, t.data_ptr())
     for name, t, w in (("rstd_post", rstd_post, w_post), ("rstd_pre", rstd_pre, w_pre)):
         if w is not None:
-            _check(name, t, f32, (T,), dev)
+            _check(name, t, _F32, (T,), dev)
             setattr(p, name, t.data_ptr())
 
     def body(handle):
@@ -315,13 +314,13 @@ def norm_residual_backward(h, y=None, dh=None, dx=None, gate=None, w_post=None, 
             p.dy = dy.data_ptr()
         if gate is not None:
             dgate = torch.empty(gate.shape, device=dev,
-                                dtype=dt if p.gate_mode == _GATE_ELEMENT else f32)
+                                dtype=dt if p.gate_mode == _GATE_ELEMENT else _F32)
             p.dgate = dgate.data_ptr()
         if w_post is not None:
-            dw_post = torch.empty((C,), dtype=f32, device=dev)
+            dw_post = torch.empty((C,), dtype=_F32, device=dev)
             p.dw_post = dw_post.data_ptr()
         if w_pre is not None:
-            dw_pre = torch.empty((C,), dtype=f32, device=dev)
+            dw_pre = torch.empty((C,), dtype=_F32, device=dev)
             p.dw_pre = dw_pre.data_ptr()
         _raise(lib().norm_residual_backward(ctypes.byref(p), workspace.data_ptr(), need, handle),
                "norm_residual_backward")
