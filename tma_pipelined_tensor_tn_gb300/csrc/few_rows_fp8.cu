@@ -144,20 +144,29 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
     const uint32_t tmem_base = *tmem_holder;
     grid_dependency_wait();
 
+    // Both role warps walk their loops whole (the control flow and addresses are
+    // the same in every lane); one lane issues.
     if (warp == 0) {
-        if (elect_one()) {
-            uint32_t it = 0;
-            for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
-                const uint32_t s = ring_stage(it, C::STAGES);
-                if (!wait_or_abort(empty_bar(s), ring_phase(it, C::STAGES) ^ 1u, abort_flag, err,
-                                   kSiteProducerEmpty, limit_ns))
-                    break;
+        const bool lead = elect_one();
+        uint32_t s = 0, phase = 0, it = 0;
+        for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
+            if (!__all_sync(0xffffffffu, wait_many(empty_bar(s), phase ^ 1u, abort_flag, err,
+                                                   kSiteProducerEmpty, limit_ns)))
+                break;
+            if (lead) {
                 mbar_arrive_expect_tx(full_bar(s), C::kStageBytes);
                 const uint32_t w = sbase + s * C::kStageBytes;
                 tma_load_2d(w, &prob.tmW, kb * C::BK, n0, full_bar(s));
                 tma_load_2d(w + C::kWBytes, &prob.tmX, kb * C::BK, m0, full_bar(s));
             }
-            // The last stages issued must have landed before shared memory is reused.
+            __syncwarp();
+            if (++s == (uint32_t)C::STAGES) {
+                s = 0;
+                phase ^= 1u;
+            }
+        }
+        // The last stages issued must have landed before shared memory is reused.
+        if (lead) {
             const uint32_t first = it > (uint32_t)C::STAGES ? it - C::STAGES : 0u;
             for (uint32_t j = first; j < it; ++j)
                 wait_bounded(full_bar(ring_stage(j, C::STAGES)), ring_phase(j, C::STAGES), err,
@@ -165,21 +174,22 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (elect_one()) {
-            constexpr uint32_t kIdesc = idesc_e4m3(C::BN, C::NP);
-            uint32_t it = 0;
-            for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
-                const uint32_t s = ring_stage(it, C::STAGES);
-                const uint32_t a = ring_stage(it, C::kAccs);
-                if (!wait_or_abort(full_bar(s), ring_phase(it, C::STAGES), abort_flag, err,
-                                   kSiteMmaFull, limit_ns) ||
-                    !wait_or_abort(acc_empty_bar(a), ring_phase(it, C::kAccs) ^ 1u, abort_flag,
-                                   err, kSiteMmaAccEmpty, limit_ns))
-                    break;
-                tc_fence_after();
-                const uint32_t w = sbase + s * C::kStageBytes;
-                const uint64_t w_desc = umma_desc_sw128_kmajor(w);
-                const uint64_t x_desc = umma_desc_sw128_kmajor(w + C::kWBytes);
+        constexpr uint32_t kIdesc = idesc_e4m3(C::BN, C::NP);
+        const bool lead = elect_one();
+        const uint64_t w_desc0 = umma_desc_sw128_kmajor(sbase);
+        const uint64_t x_desc0 = umma_desc_sw128_kmajor(sbase + C::kWBytes);
+        uint32_t s = 0, phase = 0, a = 0, a_phase = 1;
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xffffffffu,
+                            wait_many(acc_empty_bar(a), a_phase, abort_flag, err,
+                                      kSiteMmaAccEmpty, limit_ns) &&
+                                wait_many(full_bar(s), phase, abort_flag, err, kSiteMmaFull,
+                                          limit_ns)))
+                break;
+            tc_fence_after();
+            if (lead) {
+                const uint64_t w_desc = w_desc0 + s * (C::kStageBytes / 16);
+                const uint64_t x_desc = x_desc0 + s * (C::kStageBytes / 16);
 #pragma unroll
                 for (int j = 0; j < C::BK / 32; ++j)   // 32 k = 32 bytes = 2 address units
                     mma_e4m3(tmem_base + a * C::NP, w_desc + 2 * j, x_desc + 2 * j, kIdesc,
@@ -187,6 +197,17 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
                 mma_commit(empty_bar(s));
                 mma_commit(acc_full_bar(a));
             }
+            __syncwarp();
+            if (++s == (uint32_t)C::STAGES) {
+                s = 0;
+                phase ^= 1u;
+            }
+            if (++a == (uint32_t)C::kAccs) {
+                a = 0;
+                a_phase ^= 1u;
+            }
+        }
+        if (lead) {
             mma_commit(mma_done_bar);
             wait_bounded(mma_done_bar, 0, err, kSiteDrainMma, limit_ns);
         }

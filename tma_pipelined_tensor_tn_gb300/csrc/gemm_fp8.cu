@@ -46,23 +46,26 @@ namespace tmagemm {
 
 namespace {
 
-template <int BN_, int COLS_, int STAGES_, bool PAIR_, bool GROUPED_, bool BF16_>
+template <int BN_, int ACC_COLS_, int COLS_, int STAGES_, bool PAIR_, bool GROUPED_, bool BF16_>
 struct Fp8Cfg {
     static constexpr int BM = 128, BN = BN_, BK = kFp8Block, STAGES = STAGES_;
     static constexpr bool kPair = PAIR_, kGrouped = GROUPED_, kBF16 = BF16_;
     static constexpr int kTileM = PAIR_ ? 256 : 128;
+    // A k-block's product is made in parts of kAccCols columns, each in a TMEM
+    // accumulator of its own: the MMAs of one part run while the parts before
+    // it are scaled.
+    static constexpr int kAccCols = ACC_COLS_, kAccs = 4, kParts = BN_ / ACC_COLS_;
     // Rows of B in this CTA; a pair's CTAs each hold half of every part.
     static constexpr int kBRows = PAIR_ ? BN_ / 2 : BN_;
-    static constexpr int kBBoxRows = PAIR_ ? 64 : BN_;
-    // A k-block's product is made in parts of 128 columns, each in a TMEM
-    // accumulator of its own (four of them): the MMAs of one part run while
-    // the parts before it are scaled.
-    static constexpr int kAccCols = 128, kAccs = 4, kParts = BN_ / kAccCols;
+    static constexpr int kBBoxRows = PAIR_ ? ACC_COLS_ / 2 : ACC_COLS_;
     static constexpr int kCols = COLS_;                    // columns of one epilogue warp
     static constexpr int kEpiWarps = 4 * BN_ / kCols;
     static constexpr int kThreads = 128 + 32 * kEpiWarps;
-    // 32-column TMEM loads a warp has in flight.
-    static constexpr int kBatch = 2;
+    // A warp's columns are 32-column pieces; each lies in one 128-column block
+    // of weight scales, and all of them in at most two.
+    static constexpr int kPieces = COLS_ / 32;
+    static constexpr int kBatch = kPieces % 2 ? kPieces : 2;   // pieces read from TMEM at once
+    static constexpr bool kTwoBlocks = BN_ % kFp8Block != 0;
     // Registers: the role warps give up what the epilogue warps take.
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
     static constexpr int kRoleRegs = 56;
@@ -76,11 +79,18 @@ struct Fp8Cfg {
     static constexpr uint32_t kABytes = BM * BK;
     static constexpr uint32_t kBBytes = kBRows * BK;
     static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-    // Staging of D: per epilogue warp 32 rows x kCols, as store boxes of 64
-    // columns (one 128-byte swizzle span).
-    static constexpr uint32_t kBoxBytes = 32 * 128;
-    static constexpr int kBoxes = kCols / 64;
+    // Staging of D: per epilogue warp 32 rows x kCols, as store boxes of one
+    // swizzle span (64 columns in 128 bytes, or 32 in 64).
+    static constexpr int kBoxCols = COLS_ % 64 == 0 ? 64 : 32;
+    static constexpr int kBoxes = COLS_ / kBoxCols;
+    static constexpr uint32_t kBoxRowBytes = kBoxCols * 2, kBoxChunks = kBoxRowBytes / 16;
+    static constexpr uint32_t kBoxBytes = 32 * kBoxRowBytes;
     static constexpr uint32_t kOffD = STAGES * kStageBytes;
+    // Byte offset in a box of 16-byte chunk c of row r: the swizzle XORs the
+    // chunk with the address bits from 7 up.
+    static __device__ __forceinline__ uint32_t box_at(uint32_t r, uint32_t c) {
+        return r * kBoxRowBytes + ((c ^ ((r * kBoxRowBytes / 128) % kBoxChunks)) << 4);
+    }
     static constexpr uint32_t kOffBar = kOffD + kEpiWarps * kBoxes * kBoxBytes;
     static constexpr uint32_t kNumBars = 2 * STAGES + 2 * kAccs + kParts;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
@@ -88,7 +98,13 @@ struct Fp8Cfg {
     static constexpr uint32_t kSmemBytes =
         kOffStart + (GROUPED_ ? (kMaxFp8Groups + 1) * 4 : 0) + 1024;
     static_assert(kSmemBytes <= 232448, "fits the 227 KB opt-in shared memory");
-    static_assert((BN == 128 || BN == 256) && (kCols == 64 || kCols == 128), "parts and boxes");
+    static_assert((kParts == 1 || kParts == 2) && kAccs % kParts == 0,
+                  "an MMA issuer (warp 1 or 2) and accumulators of its own per part");
+    static_assert(kAccs * kAccCols <= 512, "TMEM columns");
+    static_assert(BN_ % ACC_COLS_ == 0 && ACC_COLS_ % COLS_ == 0 && COLS_ % 32 == 0 &&
+                      ACC_COLS_ % 16 == 0 && kBBoxRows % 8 == 0,
+                  "whole parts, epilogue warps, pieces and swizzle atoms");
+    static_assert(kStageBytes % 1024 == 0 && kBoxBytes % 1024 == 0, "atoms stay aligned");
 };
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 operands and FP32 sums
@@ -144,7 +160,7 @@ __device__ __forceinline__ void set_max_regs_inc() {
 struct Fp8Problem {
     CUtensorMap tmA;   // A {K, rows}, box {128, kABoxRows}
     CUtensorMap tmB;   // B {K, N, G}, box {128, kBBoxRows, 1}
-    CUtensorMap tmD;   // D {N, rows}, box {64, 32}
+    CUtensorMap tmD;   // D {N, rows}, box {kBoxCols, 32}
     const float* sa;   // scale of row m, block b: sa[m * sa_row + b * sa_blk]
     int64_t sa_row, sa_blk;
     const float* sb;   // [G][n_blocks][k_blocks]
@@ -297,37 +313,37 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         set_max_regs_dec<C::kRoleRegs>();
     if (warp == 0) {
         // ================= TMA producer =================
-        if (elect_one()) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int32_t u = unit0; ok && u < num_units; u += unit_step) {
-                const Fp8Unit t = unit_of<C>(prob, start, u);
-                // Boxes of A with at least one row, in this CTA and in all.
-                int32_t boxes = 1, all_boxes = C::kPair ? 2 : 1;
-                if constexpr (C::kGrouped) {
-                    constexpr int32_t kMost = C::BM / C::kABoxRows;
-                    auto count = [&](int32_t r) {
-                        const int32_t left = t.row_end - (t.row0 + r * C::BM);
-                        return min(max((left + C::kABoxRows - 1) / C::kABoxRows, 0), kMost);
-                    };
-                    boxes = count(static_cast<int32_t>(rank));
-                    all_boxes = C::kPair ? count(0) + count(1) : boxes;
+        // The whole warp walks the loop (its control flow and addresses are the
+        // same in every lane); one lane issues.
+        const bool lead = elect_one();
+        uint32_t s = 0, phase = 0, it = 0;
+        bool ok = true;
+        for (int32_t u = unit0; ok && u < num_units; u += unit_step) {
+            const Fp8Unit t = unit_of<C>(prob, start, u);
+            // Boxes of A with at least one row, in this CTA and in all.
+            int32_t boxes = 1, all_boxes = C::kPair ? 2 : 1;
+            if constexpr (C::kGrouped) {
+                constexpr int32_t kMost = C::BM / C::kABoxRows;
+                auto count = [&](int32_t r) {
+                    const int32_t left = t.row_end - (t.row0 + r * C::BM);
+                    return min(max((left + C::kABoxRows - 1) / C::kABoxRows, 0), kMost);
+                };
+                boxes = count(static_cast<int32_t>(rank));
+                all_boxes = C::kPair ? count(0) + count(1) : boxes;
+            }
+            const uint32_t bytes = static_cast<uint32_t>(all_boxes) * (C::kABoxRows * C::BK) +
+                                   (C::kPair ? 2u : 1u) * C::kBBytes;
+            const int32_t a_row = t.row0 + static_cast<int32_t>(rank) * C::BM;
+            const int32_t b_row = t.n0 + static_cast<int32_t>(rank) * C::kBBoxRows;
+            for (int32_t kb = 0; kb < prob.k_blocks; ++kb, ++it) {
+                ok = __all_sync(0xffffffffu, wait_many(empty_bar(s), phase ^ 1u, abort_flag, err,
+                                                       kSiteProducerEmpty, limit_ns)) &&
+                     check_ok(a_row >= 0 && b_row >= 0, err, kSiteCheckTma);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
                 }
-                const uint32_t bytes =
-                    static_cast<uint32_t>(all_boxes) * (C::kABoxRows * C::BK) +
-                    (C::kPair ? 2u : 1u) * C::kBBytes;
-                const int32_t a_row = t.row0 + static_cast<int32_t>(rank) * C::BM;
-                const int32_t b_row = t.n0 + static_cast<int32_t>(rank) * C::kBBoxRows;
-                for (int32_t kb = 0; kb < prob.k_blocks; ++kb) {
-                    const uint32_t s = ring_stage(it, C::STAGES);
-                    const uint32_t ph = ring_phase(it, C::STAGES);
-                    if (!wait_many(empty_bar(s), ph ^ 1u, abort_flag, err, kSiteProducerEmpty,
-                                       limit_ns) ||
-                        !check_ok(a_row >= 0 && b_row >= 0, err, kSiteCheckTma)) {
-                        *abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
+                if (lead) {
                     const uint32_t a_dst = sbase + s * C::kStageBytes;
                     const uint32_t b_dst = a_dst + C::kABytes;
                     if constexpr (C::kPair) {
@@ -347,74 +363,92 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                                         a_row + i * C::kABoxRows, full_bar(s));
                         tma_load_3d(b_dst, &prob.tmB, kb * C::BK, b_row, t.group, full_bar(s));
                     }
-                    ++it;
+                }
+                __syncwarp();
+                if (++s == (uint32_t)C::STAGES) {
+                    s = 0;
+                    phase ^= 1u;
                 }
             }
-            if constexpr (kChecked) ring_count[0] = it;
-            // The last stages issued must have landed before shared memory is
-            // released (a pair: the leader's barriers count both CTAs' loads,
-            // and the peer stays until the final cluster barrier).
-            if (rank == 0) {
-                const uint32_t first = it > (uint32_t)C::STAGES ? it - C::STAGES : 0u;
-                for (uint32_t j = first; j < it; ++j)
-                    wait_bounded(full_bar(ring_stage(j, C::STAGES)), ring_phase(j, C::STAGES), err,
-                                 kSiteDrainFull, limit_ns);
-            }
+        }
+        if constexpr (kChecked) ring_count[0] = it;
+        // The last stages issued must have landed before shared memory is
+        // released (a pair: the leader's barriers count both CTAs' loads, and
+        // the peer stays until the final cluster barrier).
+        if (rank == 0 && lead) {
+            const uint32_t first = it > (uint32_t)C::STAGES ? it - C::STAGES : 0u;
+            for (uint32_t j = first; j < it; ++j)
+                wait_bounded(full_bar(ring_stage(j, C::STAGES)), ring_phase(j, C::STAGES), err,
+                             kSiteDrainFull, limit_ns);
         }
         __syncwarp();
     } else if (warp <= C::kParts) {
         // ===== MMA issuers (the leader's, for a pair): warp 1 + h part h =====
-        if (rank == 0 && elect_one()) {
+        if (rank == 0) {
             constexpr uint32_t kIdesc = idesc_e4m3(C::kTileM, C::kAccCols);
             // B rows (in this CTA) of one part.
             constexpr uint32_t kPartBytes = (C::kBRows / C::kParts) * C::BK;
+            const bool lead = elect_one();
             const uint32_t h = static_cast<uint32_t>(warp - 1);
-            uint32_t it = 0;
+            const uint64_t a_desc0 = umma_desc_sw128_kmajor(sbase);
+            const uint64_t b_desc0 = umma_desc_sw128_kmajor(sbase + C::kABytes + h * kPartBytes);
+            // The stage and its phase; the accumulator (parts h, h + kParts, ...
+            // of the running count go round the kAccs) and the phase in which
+            // its use before this one is read (the first time: at once).
+            uint32_t s = 0, phase = 0, a = h, a_phase = 1, it = 0;
             bool ok = true;
             for (int32_t u = unit0; ok && u < num_units; u += unit_step) {
                 for (int32_t kb = 0; kb < prob.k_blocks; ++kb, ++it) {
-                    const uint32_t s = ring_stage(it, C::STAGES);
-                    const uint32_t part = it * C::kParts + h;
-                    const uint32_t a = ring_stage(part, C::kAccs);
-                    if (!wait_many(full_bar(s), ring_phase(it, C::STAGES), abort_flag, err,
-                                        kSiteMmaFull, limit_ns) ||
-                        !wait_many(acc_empty_bar(a), ring_phase(part, C::kAccs) ^ 1u,
-                                        abort_flag, err, kSiteMmaAccEmpty, limit_ns)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xffffffffu,
+                                    wait_many(acc_empty_bar(a), a_phase, abort_flag, err,
+                                              kSiteMmaAccEmpty, limit_ns) &&
+                                        wait_many(full_bar(s), phase, abort_flag, err,
+                                                  kSiteMmaFull, limit_ns));
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a_addr = sbase + s * C::kStageBytes;
-                    const uint64_t a_desc = umma_desc_sw128_kmajor(a_addr);
-                    const uint64_t b_desc =
-                        umma_desc_sw128_kmajor(a_addr + C::kABytes + h * kPartBytes);
-                    const uint32_t d_tmem = tmem_base + a * C::kAccCols;
-                    // Each step of 32 k is 32 bytes further along the rows (the
-                    // descriptors' address field counts 16 bytes).
+                    if (lead) {
+                        // Each step of 32 k is 32 bytes further along the rows (the
+                        // descriptors' address field counts 16 bytes).
+                        const uint64_t a_desc = a_desc0 + s * (C::kStageBytes / 16);
+                        const uint64_t b_desc = b_desc0 + s * (C::kStageBytes / 16);
+                        const uint32_t d_tmem = tmem_base + a * C::kAccCols;
 #pragma unroll
-                    for (int j = 0; j < C::BK / 32; ++j)
-                        mma_e4m3_ss<C::kPair>(d_tmem, a_desc + 2 * j, b_desc + 2 * j, kIdesc,
-                                              j != 0 ? 1u : 0u);
-                    // The accumulator is full, and this part done with stage s
-                    // (in both CTAs of a pair), once these MMAs finish.
-                    if constexpr (C::kPair) {
-                        mma_commit_pair(acc_full_bar(a), 0x3u);
-                        mma_commit_pair(empty_bar(s), 0x3u);
-                    } else {
-                        mma_commit(acc_full_bar(a));
-                        mma_commit(empty_bar(s));
+                        for (int j = 0; j < C::BK / 32; ++j)
+                            mma_e4m3_ss<C::kPair>(d_tmem, a_desc + 2 * j, b_desc + 2 * j, kIdesc,
+                                                  j != 0 ? 1u : 0u);
+                        // The accumulator is full, and this part done with stage
+                        // s (in both CTAs of a pair), once these MMAs finish.
+                        if constexpr (C::kPair) {
+                            mma_commit_pair(acc_full_bar(a), 0x3u);
+                            mma_commit_pair(empty_bar(s), 0x3u);
+                        } else {
+                            mma_commit(acc_full_bar(a));
+                            mma_commit(empty_bar(s));
+                        }
+                    }
+                    __syncwarp();
+                    if (++s == (uint32_t)C::STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                    a += C::kParts;
+                    if (a >= (uint32_t)C::kAccs) {
+                        a = h;
+                        a_phase ^= 1u;
                     }
                 }
             }
             if constexpr (kChecked) ring_count[1 + h] = it;
             // All issued MMAs must finish before TMEM is released.
-            if constexpr (C::kPair)
-                mma_commit_pair(mma_done_bar(h), 0x1u);
-            else
-                mma_commit(mma_done_bar(h));
-            wait_bounded(mma_done_bar(h), 0, err, kSiteDrainMma, limit_ns);
+            if (lead) {
+                if constexpr (C::kPair)
+                    mma_commit_pair(mma_done_bar(h), 0x1u);
+                else
+                    mma_commit(mma_done_bar(h));
+                wait_bounded(mma_done_bar(h), 0, err, kSiteDrainMma, limit_ns);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
     } else {
         set_max_regs_inc<C::kEpiRegs>();
@@ -430,16 +464,17 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         // The accumulator of this warp's next part: parts h, h + kParts, ... of
         // the running count go round the kAccs accumulators.
         uint32_t slot = h, parity = 0;
-        uint32_t full_at = acc_full_bar(h), t_acc = t_base + h * C::kAccCols;
+        const uint32_t full0 = acc_full_bar(0);
         const uint32_t empty0 = C::kPair ? map_to_rank(acc_empty_bar(0), 0) : acc_empty_bar(0);
-        uint32_t empty_at = empty0 + 8u * h;
+        uint32_t full_at = full0 + 8u * slot, empty_at = empty0 + 8u * slot;
+        uint32_t t_acc = t_base + slot * C::kAccCols;
         auto next_acc = [&]() {
             slot += C::kParts;
             if (slot >= static_cast<uint32_t>(C::kAccs)) {
                 slot = h;
                 parity ^= 1u;
             }
-            full_at = acc_full_bar(slot);
+            full_at = full0 + 8u * slot;
             empty_at = empty0 + 8u * slot;
             t_acc = t_base + slot * C::kAccCols;
         };
@@ -469,9 +504,19 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
             // stored), and blocks past the last read the last.
             const float* sa = prob.sa + min(y + lane, t.row_end - 1) * prob.sa_row;
             const int32_t nb = min(x / kFp8Block, prob.n_blocks - 1);
-            const float* sb = prob.sb + (static_cast<int64_t>(t.group) * prob.n_blocks + nb) *
+            const int32_t nb2 = min(nb + 1, prob.n_blocks - 1);
+            const float* sb = prob.sb + static_cast<int64_t>(t.group) * prob.n_blocks *
                                             prob.k_blocks;
-            float sa_next[4], sb_lane = 0.0f, sb_next = sb[min(lane, last)];
+            // The first piece in the second block of weight scales.
+            const int32_t second = (kFp8Block - x % kFp8Block) / 32;
+            float sa_next[4], sb_lane[2] = {}, sb_next[2] = {};
+            auto fetch_sb = [&](int32_t kb) {
+                sb_next[0] = sb[static_cast<int64_t>(nb) * prob.k_blocks + min(kb + lane, last)];
+                if constexpr (C::kTwoBlocks)
+                    sb_next[1] =
+                        sb[static_cast<int64_t>(nb2) * prob.k_blocks + min(kb + lane, last)];
+            };
+            fetch_sb(0);
             auto fetch = [&](int32_t kb0) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sa_next[j] = sa[min(kb0 + j, last) * prob.sa_blk];
@@ -481,41 +526,48 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
 #pragma unroll
             for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
             for (int32_t kb0 = 0; kb0 <= last; kb0 += 4) {
-                if ((kb0 & 31) == 0) sb_lane = sb_next;
-                float scales[4];
+                if ((kb0 & 31) == 0) {
+                    sb_lane[0] = sb_next[0];
+                    sb_lane[1] = sb_next[1];
+                }
+                float sa_now[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    scales[j] = sa_next[j] *
-                                __shfl_sync(0xffffffffu, sb_lane, (kb0 & 31) + j);
+                for (int j = 0; j < 4; ++j) sa_now[j] = sa_next[j];
                 fetch(kb0 + 4);
-                if ((kb0 & 31) == 0) sb_next = sb[min(kb0 + 32 + lane, last)];
+                if ((kb0 & 31) == 0) fetch_sb(kb0 + 32);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (kb0 + j > last) break;
-                    const float scale = scales[j];
+                    float scale[2];
+                    scale[0] = sa_now[j] * __shfl_sync(0xffffffffu, sb_lane[0], (kb0 & 31) + j);
+                    if constexpr (C::kTwoBlocks)
+                        scale[1] =
+                            sa_now[j] * __shfl_sync(0xffffffffu, sb_lane[1], (kb0 & 31) + j);
                     if (!__all_sync(0xffffffffu,
                                     wait_many(full_at, parity, abort_flag, err,
                                                    kSiteEpiAccFull, limit_ns)))
                         goto stop;
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < C::kCols; c += 32 * C::kBatch) {
+                    for (int c0 = 0; c0 < C::kPieces; c0 += C::kBatch) {
                         uint32_t v[C::kBatch][32];
 #pragma unroll
-                        for (int b = 0; b < C::kBatch; ++b)
-                            tmem_ld_32x32b_x32(t_acc + c + 32 * b, v[b]);
+                        for (int c = 0; c < C::kBatch; ++c)
+                            tmem_ld_32x32b_x32(t_acc + 32 * (c0 + c), v[c]);
                         tmem_ld_wait();
-                        if (c + 32 * C::kBatch == C::kCols) {
+                        if (c0 + C::kBatch == C::kPieces) {
                             // All read (by every lane: the wait is collective):
                             // the accumulator goes back to the MMA warp.
                             tc_fence_before();
                             mbar_arrive_if(lane == 0, empty_at);
                         }
 #pragma unroll
-                        for (int b = 0; b < C::kBatch; ++b)
+                        for (int c = 0; c < C::kBatch; ++c) {
+                            const float f = C::kTwoBlocks && c0 + c >= second ? scale[1] : scale[0];
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                scale_add(acc[c + 32 * b + i], v[b][i], scale);
+                                scale_add(acc[32 * (c0 + c) + i], v[c][i], f);
+                        }
                     }
                     next_acc();
                 }
@@ -525,11 +577,9 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < C::kCols / 8; ++c) {
-                // Chunk c % 8 (8 columns, 16 bytes) of box c / 8; the 128-byte
-                // swizzle XORs the chunk with the row's low three bits.
-                const uint32_t at = buf + (c / 8) * C::kBoxBytes +
-                                    static_cast<uint32_t>(lane) * 128u +
-                                    (((c % 8) ^ (static_cast<uint32_t>(lane) & 7u)) << 4);
+                constexpr int kChunks = C::kBoxChunks;
+                const uint32_t at = buf + (c / kChunks) * C::kBoxBytes +
+                                    C::box_at(static_cast<uint32_t>(lane), c % kChunks);
                 uint32_t p[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -545,24 +595,25 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                 if (lane == 0 && left > 0) {
 #pragma unroll
                     for (int b = 0; b < C::kBoxes; ++b)
-                        if (x + 64 * b < prob.N &&
+                        if (x + C::kBoxCols * b < prob.N &&
                             check_ok((x & 7) == 0 && x >= 0 && y >= 0, err, kSiteCheckTma))
-                            tma_store_2d(&prob.tmD, buf + b * C::kBoxBytes, x + 64 * b, y);
+                            tma_store_2d(&prob.tmD, buf + b * C::kBoxBytes, x + C::kBoxCols * b,
+                                         y);
                     bulk_commit_group();
                 }
             } else {
                 // The group ends inside these 32 rows: plain stores of the rows
-                // that exist, eight lanes a row (the next rows are another
+                // that exist, a lane per 16-byte chunk (the next rows are another
                 // group's).
                 __syncwarp();
-                const int32_t chunk = lane & 7;
-                for (int32_t r = lane >> 3; r < left; r += 4) {
+                constexpr int32_t kLanes = C::kBoxChunks;   // lanes of a row
+                const int32_t chunk = lane % kLanes;
+                for (int32_t r = lane / kLanes; r < left; r += 32 / kLanes) {
 #pragma unroll
                     for (int b = 0; b < C::kBoxes; ++b) {
-                        const int32_t n = x + 64 * b + 8 * chunk;
+                        const int32_t n = x + C::kBoxCols * b + 8 * chunk;
                         const uint4 v = *reinterpret_cast<const uint4*>(
-                            smem + (buf - sbase) + b * C::kBoxBytes + r * 128 +
-                            ((chunk ^ (r & 7)) << 4));
+                            smem + (buf - sbase) + b * C::kBoxBytes + C::box_at(r, chunk));
                         if (n < prob.N && check_ok(y + r < prob.rows && n + 8 <= prob.N, err,
                                                    kSiteCheckBounds))
                             *reinterpret_cast<uint4*>(
@@ -595,21 +646,22 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
     }
 }
 
-// The tiles: 256 x 256 in CTA pairs for problems that fill the GPU with them,
-// 128 x 128 otherwise.
-template <bool G, bool T> using FpPair = Fp8Cfg<256, 128, 5, true, G, T>;
-template <bool G, bool T> using FpTile = Fp8Cfg<128, 64, 6, false, G, T>;
+// The tiles: 256 x 256 and 256 x 192 in CTA pairs, 128 x 128.
+template <bool G, bool T> using FpPair256 = Fp8Cfg<256, 128, 128, 5, true, G, T>;
+template <bool G, bool T> using FpPair192 = Fp8Cfg<192, 96, 96, 6, true, G, T>;
+template <bool G, bool T> using FpTile = Fp8Cfg<128, 128, 64, 6, false, G, T>;
 
-// D {N, rows} in store boxes of 64 columns x 32 rows.
+// D {N, rows} in store boxes of 64 or 32 columns x 32 rows.
 int encode_output(EncodeTiled encode, CUtensorMap* map, void* base, uint64_t N, uint64_t rows,
-                  bool bf16) {
+                  bool bf16, uint32_t box_cols) {
     cuuint64_t dims[2] = {N, rows};
     cuuint64_t strides[1] = {N * 2};
-    cuuint32_t box[2] = {64, 32};
+    cuuint32_t box[2] = {box_cols, 32};
     cuuint32_t estr[2] = {1, 1};
     return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                   2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? 0
                : -1;
@@ -621,7 +673,7 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
     const int64_t G = C::kGrouped ? g.groups : 1;
     if (encode_fp8_operand(dev.encode, &p.tmA, g.A, g.K, g.M, 0, C::kABoxRows) ||
         encode_fp8_operand(dev.encode, &p.tmB, g.B, g.K, g.N, G, C::kBBoxRows) ||
-        encode_output(dev.encode, &p.tmD, g.D, g.N, g.M, C::kBF16))
+        encode_output(dev.encode, &p.tmD, g.D, g.N, g.M, C::kBF16, C::kBoxCols))
         return cudaErrorInvalidValue;
     p.sa = g.SA;
     p.sa_row = g.sa_row;
@@ -652,17 +704,37 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
                          dev.err_word);
 }
 
+// Which pair tile: the one whose rounds of tiles over the pairs take less.  A
+// k-block of a 256 x 192 tile takes about 0.73 of one of 256 x 256 (8192^3: 319
+// against 435 ns), so 4096^3 (352 tiles in 5 rounds against 256 in 4) runs in
+// 57.5 against 61.2 us and 1024 x 4096 x 4096 (88 in 2 against 64 in 1) in 24.2
+// against 18.1 us.
+bool narrow_pairs(int64_t tile_rows, int64_t N, int pairs) {
+    const int64_t wide = ceil_div(tile_rows * ceil_div(N, 256), pairs) * 100;
+    const int64_t narrow = ceil_div(tile_rows * ceil_div(N, 192), pairs) * 73;
+    return narrow < wide;
+}
+
+template <bool G, bool T>
+cudaError_t launch_pairs(const Fp8Gemm& g, int64_t tile_rows, const Fp8Device& dev,
+                         cudaStream_t stream) {
+    return narrow_pairs(tile_rows, g.N, dev.pairs) ? launch_cfg<FpPair192<G, T>>(g, dev, stream)
+                                                   : launch_cfg<FpPair256<G, T>>(g, dev, stream);
+}
+
 template <bool T>
 cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
+    const int64_t rows256 = ceil_div(g.M, 256);
     if (g.offsets) {
-        // Whole 256-row tiles pay when the groups fill most of them.
+        // Whole 256-row tiles pay when the groups fill most of them.  (How the
+        // rows fall into groups is only known on the device: half a tile row is
+        // added for each group's last, partly filled one.)
         if (dev.pairs > 0 && g.M >= 192 * g.groups)
-            return launch_cfg<FpPair<true, T>>(g, dev, stream);
+            return launch_pairs<true, T>(g, rows256 + g.groups / 2, dev, stream);
         return launch_cfg<FpTile<true, T>>(g, dev, stream);
     }
-    const int64_t pair_tiles = ceil_div(g.M, 256) * ceil_div(g.N, FpPair<false, T>::BN);
-    if (dev.pairs > 0 && 2 * pair_tiles > dev.pairs)
-        return launch_cfg<FpPair<false, T>>(g, dev, stream);
+    if (dev.pairs > 0 && 2 * rows256 * ceil_div(g.N, 256) > dev.pairs)
+        return launch_pairs<false, T>(g, rows256, dev, stream);
     return launch_cfg<FpTile<false, T>>(g, dev, stream);
 }
 
