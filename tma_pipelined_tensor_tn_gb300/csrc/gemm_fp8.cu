@@ -525,6 +525,41 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
             float acc[C::kCols];
 #pragma unroll
             for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
+            // The pieces go through kBatch register buffers.  Where they take
+            // them all at once, a part is read whole and its accumulator goes back
+            // to the MMA warp before the first multiply-add.  Where a part takes
+            // more than one round of the buffers, a buffer is refilled as soon as
+            // its piece has been scaled, with a piece of the next round (of this
+            // part, or of the next k-block's): TMEM is read under the
+            // multiply-adds, and the accumulator goes back after its last round
+            // (at 8192^3 371 against 390 us; for one-round parts this order hands
+            // them back later and costs more than it hides, 444 against 396 us).
+            constexpr int kRounds = C::kPieces / C::kBatch;
+            uint32_t v[C::kBatch][32];
+            auto part_ready = [&]() {
+                const bool ready = __all_sync(
+                    0xffffffffu, wait_many(full_at, parity, abort_flag, err, kSiteEpiAccFull,
+                                           limit_ns));
+                tc_fence_after();
+                return ready;
+            };
+            // (Read by every lane: the wait is collective.)
+            auto round_read = [&](bool last_round) {
+                tmem_ld_wait();
+                if (last_round) {
+                    tc_fence_before();
+                    mbar_arrive_if(lane == 0, empty_at);
+                    next_acc();
+                }
+            };
+            auto first_round = [&]() {
+                if (!part_ready()) return false;
+#pragma unroll
+                for (int c = 0; c < C::kBatch; ++c) tmem_ld_32x32b_x32(t_acc + 32 * c, v[c]);
+                round_read(kRounds == 1);
+                return true;
+            };
+            if (kRounds > 1 && !first_round()) goto stop;
             for (int32_t kb0 = 0; kb0 <= last; kb0 += 4) {
                 if ((kb0 & 31) == 0) {
                     sb_lane[0] = sb_next[0];
@@ -543,33 +578,27 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                     if constexpr (C::kTwoBlocks)
                         scale[1] =
                             sa_now[j] * __shfl_sync(0xffffffffu, sb_lane[1], (kb0 & 31) + j);
-                    if (!__all_sync(0xffffffffu,
-                                    wait_many(full_at, parity, abort_flag, err,
-                                                   kSiteEpiAccFull, limit_ns)))
-                        goto stop;
-                    tc_fence_after();
+                    if (kRounds == 1 && !first_round()) goto stop;
 #pragma unroll
-                    for (int c0 = 0; c0 < C::kPieces; c0 += C::kBatch) {
-                        uint32_t v[C::kBatch][32];
-#pragma unroll
-                        for (int c = 0; c < C::kBatch; ++c)
-                            tmem_ld_32x32b_x32(t_acc + 32 * (c0 + c), v[c]);
-                        tmem_ld_wait();
-                        if (c0 + C::kBatch == C::kPieces) {
-                            // All read (by every lane: the wait is collective):
-                            // the accumulator goes back to the MMA warp.
-                            tc_fence_before();
-                            mbar_arrive_if(lane == 0, empty_at);
-                        }
+                    for (int r = 0; r < kRounds; ++r) {
+                        // The round to read after this one, if there is one.
+                        constexpr int kLast = kRounds - 1;
+                        const int next_r = r == kLast ? 0 : r + 1;
+                        const bool more = kRounds > 1 && (r < kLast || kb0 + j < last);
 #pragma unroll
                         for (int c = 0; c < C::kBatch; ++c) {
-                            const float f = C::kTwoBlocks && c0 + c >= second ? scale[1] : scale[0];
+                            const int piece = r * C::kBatch + c;
+                            const float f = C::kTwoBlocks && piece >= second ? scale[1] : scale[0];
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                scale_add(acc[32 * (c0 + c) + i], v[c][i], f);
+                                scale_add(acc[32 * piece + i], v[c][i], f);
+                            if (more) {
+                                if (c == 0 && next_r == 0 && !part_ready()) goto stop;
+                                tmem_ld_32x32b_x32(t_acc + 32 * (next_r * C::kBatch + c), v[c]);
+                            }
                         }
+                        if (more) round_read(next_r == kLast);
                     }
-                    next_acc();
                 }
             }
             // ---- round, stage in shared memory, store ----
@@ -705,13 +734,13 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
 }
 
 // Which pair tile: the one whose rounds of tiles over the pairs take less.  A
-// k-block of a 256 x 192 tile takes about 0.73 of one of 256 x 256 (8192^3: 319
-// against 435 ns), so 4096^3 (352 tiles in 5 rounds against 256 in 4) runs in
-// 57.5 against 61.2 us and 1024 x 4096 x 4096 (88 in 2 against 64 in 1) in 24.2
-// against 18.1 us.
+// k-block of a 256 x 192 tile takes about 0.8 of one of 256 x 256 (8192^3: 326
+// against 421 ns), so 1237 x 5000 x 2064 (135 tiles in 2 rounds against 100 in 2)
+// runs in 18.1 against 20.3 us and 2048 x 4096 x 4096 (176 in 3 against 128 in 2)
+// in 36.0 against 30.4 us.
 bool narrow_pairs(int64_t tile_rows, int64_t N, int pairs) {
     const int64_t wide = ceil_div(tile_rows * ceil_div(N, 256), pairs) * 100;
-    const int64_t narrow = ceil_div(tile_rows * ceil_div(N, 192), pairs) * 73;
+    const int64_t narrow = ceil_div(tile_rows * ceil_div(N, 192), pairs) * 80;
     return narrow < wide;
 }
 
