@@ -1,0 +1,141 @@
+"""Host-side tests of the 8-bit operators and the norms: refusals before any
+CUDA call, the binding's argument checks, the argument struct's layout."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import tma_pipelined_tensor_tn_gb300 as tg
+from tma_pipelined_tensor_tn_gb300 import _build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 1 << 20          # an aligned address that no refused call may touch
+OK, INVALID, ALIGN, UNSUPPORTED = (tg.TMAGEMM_OK, tg.TMAGEMM_ERR_INVALID, tg.TMAGEMM_ERR_ALIGN,
+                                   tg.TMAGEMM_ERR_UNSUPPORTED)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    _build.build()
+    return tg.lib()
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(M=-1), INVALID), (dict(K=0), INVALID), (dict(X=None), INVALID), (dict(Q=None), INVALID),
+    (dict(S=None), INVALID), (dict(block_rows=64), INVALID), (dict(s_row=0), INVALID),
+    (dict(s_blk=-1), INVALID), (dict(K=260), ALIGN), (dict(X=P + 2), ALIGN), (dict(Q=P + 8), ALIGN),
+    (dict(S=P + 2), ALIGN), (dict(M=1 << 31), UNSUPPORTED), (dict(M=0, X=None, Q=None, S=None), OK),
+])
+def test_quantize_refusals(change, expect):
+    a = dict(M=4, K=256, X=P, bf16=1, block_rows=1, Q=P, S=P, s_row=1, s_blk=4)
+    a.update(change)
+    assert tg.lib().quantize_fp8(*a.values(), None) == expect
+
+
+GEMM = dict(M=4, N=128, K=256, A=P, SA=P, sa_row=1, sa_blk=4, B=P, SB=P, D=P, bf16=1)
+GEMM_REFUSALS = [
+    (dict(M=-1), INVALID), (dict(N=0), INVALID), (dict(K=-8), INVALID), (dict(A=None), INVALID),
+    (dict(SA=None), INVALID), (dict(B=None), INVALID), (dict(SB=None), INVALID),
+    (dict(D=None), INVALID), (dict(sa_row=0), INVALID), (dict(sa_blk=0), INVALID),
+    (dict(K=264), ALIGN), (dict(N=100), ALIGN), (dict(A=P + 8), ALIGN), (dict(B=P + 4), ALIGN),
+    (dict(D=P + 2), ALIGN), (dict(SA=P + 1), ALIGN), (dict(SB=P + 2), ALIGN),
+    (dict(M=1 << 31), UNSUPPORTED), (dict(N=1 << 31), UNSUPPORTED),
+    (dict(M=0, A=None, SA=None, D=None), OK),
+]
+
+
+@pytest.mark.parametrize("change,expect", GEMM_REFUSALS)
+def test_gemm_refusals(change, expect):
+    assert tg.lib().gemm_fp8(*{**GEMM, **change}.values(), None) == expect
+
+
+@pytest.mark.parametrize("change,expect", GEMM_REFUSALS + [
+    (dict(G=0), INVALID), (dict(offsets=None), INVALID), (dict(G=385), UNSUPPORTED),
+    (dict(offsets=P + 2), ALIGN), (dict(G=300, N=1 << 23), UNSUPPORTED)])
+def test_grouped_refusals(change, expect):
+    a = {**dict(G=3, offsets=P), **GEMM, **change}
+    assert tg.lib().gemm_fp8_grouped(*a.values(), None) == expect
+
+
+def norm_struct(**fields):
+    p = tg.TmagemmNorm()
+    for k, v in {**dict(T=4, C=256, alpha=1.0, eps=1e-6, h=P), **fields}.items():
+        setattr(p, k, v)
+    return p
+
+
+FORWARD = dict(y=P, w_post=P, w_pre=P, h_out=P, x=P)
+
+
+@pytest.mark.parametrize("fields,expect", [
+    (dict(T=-1), INVALID), (dict(C=0), INVALID), (dict(h=None), INVALID), (dict(gate_mode=4), INVALID),
+    (dict(gate_mode=1), INVALID), (dict(gate_mode=-1), INVALID),
+    (dict(y=None, w_post=None, w_pre=None), INVALID), (dict(y=None), INVALID),
+    (dict(y=None, w_post=None, gate_mode=1, gate=P), INVALID), (dict(h_out=None), INVALID),
+    (dict(x=None), INVALID), (dict(x=None, q=P, scales=P), INVALID),
+    (dict(x=None, q=P, scales=P, s_row_stride=1), INVALID),
+    (dict(C=260), ALIGN), (dict(h=P + 2), ALIGN), (dict(y=P + 8), ALIGN), (dict(w_pre=P + 2), ALIGN),
+    (dict(gate_mode=1, gate=P + 2), ALIGN), (dict(gate_mode=2, gate=P + 1), ALIGN),
+    (dict(x=P + 8), ALIGN), (dict(rstd_pre=P + 2), ALIGN), (dict(C=16392), UNSUPPORTED),
+    (dict(T=1 << 31), UNSUPPORTED), (dict(T=0, h=None, h_out=None, x=None), OK),
+])
+def test_norm_forward_refusals(fields, expect):
+    p = norm_struct(**{**FORWARD, **fields})
+    assert tg.lib().norm_residual(ctypes.byref(p), None) == expect
+    assert tg.lib().norm_residual(None, None) == INVALID
+
+
+BACKWARD = dict(y=P, w_post=P, w_pre=P, rstd_post=P, rstd_pre=P, dh_out=P, dx=P, dh=P, dy=P,
+                dw_post=P, dw_pre=P)
+
+
+@pytest.mark.parametrize("fields,expect", [
+    (dict(dx=None), INVALID), (dict(w_pre=None), INVALID), (dict(dw_post=None), INVALID),
+    (dict(dw_pre=None), INVALID), (dict(dh=None), INVALID), (dict(dy=None), INVALID),
+    (dict(rstd_post=None), INVALID), (dict(rstd_pre=None), INVALID),
+    (dict(gate_mode=2, gate=P), INVALID), (dict(dh=P + 2), ALIGN), (dict(dw_pre=P + 2), ALIGN),
+    (dict(gate_mode=3, gate=P, dgate=P + 8), ALIGN), (dict(gate_mode=1, gate=P, dgate=P + 2), ALIGN),
+])
+def test_norm_backward_refusals(fields, expect):
+    p = norm_struct(**{**BACKWARD, **fields})
+    assert tg.lib().norm_residual_backward(ctypes.byref(p), P, 1 << 30, None) == expect
+
+
+def test_norm_workspace_refusals():
+    f = tg.lib().norm_residual_backward_workspace_size
+    assert f(-1, 256) == INVALID and f(4, 0) == INVALID and f(4, 16392) == UNSUPPORTED
+    assert f(0, 256) == 0
+
+
+def test_norm_struct_layout_matches_the_header(tmp_path):
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("gcc not available")
+    names = [n for n, _ in tg.TmagemmNorm._fields_]
+    body = "".join(f'printf("%zu\\n", offsetof(tmagemm_norm, {n}));' for n in names)
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "tmagemm.h"\n'
+                   f'int main(void) {{ {body} printf("%zu\\n", sizeof(tmagemm_norm)); return 0; }}\n')
+    exe = tmp_path / "layout"
+    subprocess.run([cc, "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    want = [getattr(tg.TmagemmNorm, n).offset for n in names] + [ctypes.sizeof(tg.TmagemmNorm)]
+    assert got == want
+
+
+def test_binding_refuses_host_tensors():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros((4, 256), dtype=torch.bfloat16)
+    q = torch.zeros((4, 256), dtype=torch.float8_e4m3fn)
+    s = torch.zeros((4, 2))
+    with pytest.raises(TypeError):
+        tg.quantize_fp8(x)
+    with pytest.raises(TypeError):
+        tg.gemm_fp8(q, s, q, s)
+    with pytest.raises(TypeError):
+        tg.gemm_fp8_grouped(q, s, q[None], s[None], torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        tg.norm_residual(x, x)

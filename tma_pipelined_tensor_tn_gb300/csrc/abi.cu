@@ -665,9 +665,11 @@ int gemm_fp8_impl(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
 int norm_args(const tmagemm_norm* p, NormArgs* a) {
     if (!p || p->T < 0 || p->C <= 0 || p->gate_mode < 0 || p->gate_mode > 3)
         return TMAGEMM_ERR_INVALID;
-    if ((!p->y && !p->w_pre) || (p->T > 0 && !p->h)) return TMAGEMM_ERR_INVALID;
-    if (!p->y && (p->w_post || p->gate_mode != kGateNone)) return TMAGEMM_ERR_INVALID;
-    if (p->T > 0 && p->gate_mode != kGateNone && !p->gate) return TMAGEMM_ERR_INVALID;
+    // (With no rows the T x C operands may be NULL: nothing is read.)
+    if (p->T > 0 &&
+        (!p->h || (!p->y && (!p->w_pre || p->w_post || p->gate_mode != kGateNone)) ||
+         (p->gate_mode != kGateNone && !p->gate)))
+        return TMAGEMM_ERR_INVALID;
     if (p->C > 16384 || p->T > (int64_t(1) << 31) - 1) return TMAGEMM_ERR_UNSUPPORTED;
     const void* aligned[] = {p->h, p->y, p->w_post, p->w_pre,
                              p->gate_mode == kGateToken ? nullptr : p->gate};
@@ -767,7 +769,7 @@ int norm_residual_backward(const tmagemm_norm* p, void* workspace, int64_t works
                            void* stream) {
     NormArgs a;
     if (int s = norm_args(p, &a)) return s;
-    if ((p->w_pre != nullptr) != (p->dx != nullptr)) return TMAGEMM_ERR_INVALID;
+    if (p->T > 0 && (p->w_pre != nullptr) != (p->dx != nullptr)) return TMAGEMM_ERR_INVALID;
     if ((p->w_post && !p->dw_post) || (p->w_pre && !p->dw_pre)) return TMAGEMM_ERR_INVALID;
     if (p->gate_mode != kGateNone && !p->dgate) return TMAGEMM_ERR_INVALID;
     if (p->T > 0 && (!p->dh || (p->y && !p->dy) || (p->w_post && !p->rstd_post) ||
