@@ -180,7 +180,7 @@ norm_forward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ 
     grid_launch_dependents();
     grid_dependency_wait();
     const int32_t C8 = p.C8;
-    const float inv_c = 1.0f / (8.0f * static_cast<float>(C8));
+    const float channels = 8.0f * static_cast<float>(C8);
     uint32_t slot = 0;
     RowPipe<V> pipe(in, ring, C8);
     pipe.issue(blockIdx.x, p.T, 0);
@@ -202,7 +202,7 @@ norm_forward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
             }
-            r = rsqrtf(cta_sum(ss, slots, slot) * inv_c + p.eps);
+            r = __frsqrt_rn(cta_sum(ss, slots, slot) / channels + p.eps);
             if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = r;
         }
         float ss = 0.0f;
@@ -231,7 +231,7 @@ norm_forward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ 
             for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
         }
         if (!p.w_pre) continue;
-        r = rsqrtf(cta_sum(ss, slots, slot) * inv_c + p.eps);
+        r = __frsqrt_rn(cta_sum(ss, slots, slot) / channels + p.eps);
         if (p.rstd_pre && threadIdx.x == 0) p.rstd_pre[row] = r;
 #pragma unroll
         for (int i = 0; i < V; ++i) {

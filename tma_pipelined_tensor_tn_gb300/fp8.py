@@ -23,6 +23,13 @@ FP8_BLOCK = 128
 _GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_ELEMENT = range(4)
 _F8, _F32 = torch.float8_e4m3fn, torch.float32
 _IS_BF16 = {torch.bfloat16: 1, torch.float16: 0}
+# These calls are as short as their launches: names are bound once, and the
+# current device and stream are asked for as numbers (a Stream object alone
+# costs as much as a launch).
+_Tensor, _empty, _empty_like, _empty_strided = (torch.Tensor, torch.empty, torch.empty_like,
+                                                torch.empty_strided)
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _blocks(n: int) -> int:
@@ -33,11 +40,11 @@ def _launch(device, stream, inputs, body):
     """body(handle) with `device` current and, for an explicit stream, that
     stream current too, so that the results body() allocates belong to it."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            # The raw handle: a Stream object costs as much as a launch.
-            return body(torch._C._cuda_getCurrentRawStream(device.index))
+        index = device.index
+        if index == _current_device():
+            return body(_current_stream(index))
         with torch.cuda.device(device):
-            return body(torch.cuda.current_stream(device).cuda_stream)
+            return body(_current_stream(index))
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     if stream != torch.cuda.current_stream(device):
@@ -49,10 +56,10 @@ def _launch(device, stream, inputs, body):
 
 
 def _check(name, t, dtype, shape, device, contiguous=True):
-    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device
             and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())):
         return
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -65,7 +72,7 @@ def _check(name, t, dtype, shape, device, contiguous=True):
 
 def _first(name, t, dims):
     """The device of a call's first operand: a CUDA tensor of `dims` dimensions."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
@@ -82,6 +89,19 @@ def _bf16(dtype) -> int:
 def _raise(status, what):
     if status != TMAGEMM_OK:
         raise TmaGemmError(status, what)
+
+
+class _Functions:
+    """The library's functions, each looked up once (loading the library at the
+    first use)."""
+
+    def __getattr__(self, name):
+        fn = getattr(lib(), name)
+        setattr(self, name, fn)
+        return fn
+
+
+_fn = _Functions()
 
 
 def quantize_fp8(X, block_rows: int = 1, stream=None):
@@ -102,14 +122,14 @@ def quantize_fp8(X, block_rows: int = 1, stream=None):
     blocks = _blocks(K)
 
     def body(handle):
-        Q = torch.empty_like(X, dtype=_F8)
+        Q = _empty_like(X, dtype=_F8)
         if block_rows == 1:
-            S = torch.empty_strided((M, blocks), (1, max(M, 1)), dtype=_F32, device=dev)
+            S = _empty_strided((M, blocks), (1, max(M, 1)), dtype=_F32, device=dev)
             strides = 1, max(M, 1)
         else:
-            S = torch.empty((_blocks(M), blocks), dtype=_F32, device=dev)
+            S = _empty((_blocks(M), blocks), dtype=_F32, device=dev)
             strides = max(blocks, 1), 1
-        _raise(lib().quantize_fp8(M, K, X.data_ptr(), bf16, block_rows, Q.data_ptr(),
+        _raise(_fn.quantize_fp8(M, K, X.data_ptr(), bf16, block_rows, Q.data_ptr(),
                                   S.data_ptr(), *strides, handle), "quantize_fp8")
         return Q, S
 
@@ -141,13 +161,16 @@ def _product(what, A, SA, B, SB, offsets, dtype, out, stream):
         sa_blk = 1
 
     def body(handle):
-        D = torch.empty((M, N), dtype=dtype, device=dev) if out is None else out
-        rest = (M, N, K, A.data_ptr(), SA.data_ptr(), sa_row, sa_blk, B.data_ptr(),
-                SB.data_ptr(), D.data_ptr(), bf16, handle)
+        D = _empty((M, N), dtype=dtype, device=dev) if out is None else out
         if offsets is None:
-            _raise(lib().gemm_fp8(*rest), what)
+            status = _fn.gemm_fp8(M, N, K, A.data_ptr(), SA.data_ptr(), sa_row, sa_blk,
+                                  B.data_ptr(), SB.data_ptr(), D.data_ptr(), bf16, handle)
         else:
-            _raise(lib().gemm_fp8_grouped(lead[0], offsets.data_ptr(), *rest), what)
+            status = _fn.gemm_fp8_grouped(lead[0], offsets.data_ptr(), M, N, K, A.data_ptr(),
+                                          SA.data_ptr(), sa_row, sa_blk, B.data_ptr(),
+                                          SB.data_ptr(), D.data_ptr(), bf16, handle)
+        if status:
+            _raise(status, what)
         return D
 
     return _launch(dev, stream, (A, SA, B, SB, offsets, out), body)
@@ -255,23 +278,23 @@ def norm_residual(h, y=None, gate=None, w_post=None, w_pre=None, alpha: float = 
     def body(handle):
         h_out, x, scales, r_post, r_pre = h, None, None, None, None
         if y is not None:
-            h_out = torch.empty_like(h)
+            h_out = _empty_like(h)
             p.h_out = h_out.data_ptr()
         if w_pre is not None and quantize:
-            x = torch.empty_like(h, dtype=_F8)
-            scales = torch.empty_strided((T, _blocks(C)), (1, max(T, 1)), dtype=_F32, device=dev)
+            x = _empty_like(h, dtype=_F8)
+            scales = _empty_strided((T, _blocks(C)), (1, max(T, 1)), dtype=_F32, device=dev)
             p.q, p.scales, p.s_row_stride, p.s_block_stride = (
                 x.data_ptr(), scales.data_ptr(), 1, max(T, 1))
         elif w_pre is not None:
-            x = torch.empty_like(h)
+            x = _empty_like(h)
             p.x = x.data_ptr()
         if save_rstd and w_post is not None:
-            r_post = torch.empty((T,), dtype=_F32, device=dev)
+            r_post = _empty((T,), dtype=_F32, device=dev)
             p.rstd_post = r_post.data_ptr()
         if save_rstd and w_pre is not None:
-            r_pre = torch.empty((T,), dtype=_F32, device=dev)
+            r_pre = _empty((T,), dtype=_F32, device=dev)
             p.rstd_pre = r_pre.data_ptr()
-        _raise(lib().norm_residual(ctypes.byref(p), handle), "norm_residual")
+        _raise(_fn.norm_residual(ctypes.byref(p), handle), "norm_residual")
         return NormOut(h_out, x, scales, r_post, r_pre)
 
     return _launch(dev, stream, (h, y, gate, w_post, w_pre), body)
@@ -303,26 +326,26 @@ def norm_residual_backward(h, y=None, dh=None, dx=None, gate=None, w_post=None, 
 
     def body(handle):
         dy = dgate = dw_post = dw_pre = None
-        need = lib().norm_residual_backward_workspace_size(T, C)
+        need = _fn.norm_residual_backward_workspace_size(T, C)
         if need < 0:
             raise TmaGemmError(int(need), "norm_residual_backward_workspace_size")
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        dh_in = torch.empty_like(h)
+        workspace = _empty((need,), dtype=torch.uint8, device=dev)
+        dh_in = _empty_like(h)
         p.dh = dh_in.data_ptr()
         if y is not None:
-            dy = torch.empty_like(h)
+            dy = _empty_like(h)
             p.dy = dy.data_ptr()
         if gate is not None:
-            dgate = torch.empty(gate.shape, device=dev,
+            dgate = _empty(gate.shape, device=dev,
                                 dtype=dt if p.gate_mode == _GATE_ELEMENT else _F32)
             p.dgate = dgate.data_ptr()
         if w_post is not None:
-            dw_post = torch.empty((C,), dtype=_F32, device=dev)
+            dw_post = _empty((C,), dtype=_F32, device=dev)
             p.dw_post = dw_post.data_ptr()
         if w_pre is not None:
-            dw_pre = torch.empty((C,), dtype=_F32, device=dev)
+            dw_pre = _empty((C,), dtype=_F32, device=dev)
             p.dw_pre = dw_pre.data_ptr()
-        _raise(lib().norm_residual_backward(ctypes.byref(p), workspace.data_ptr(), need, handle),
+        _raise(_fn.norm_residual_backward(ctypes.byref(p), workspace.data_ptr(), need, handle),
                "norm_residual_backward")
         return NormGrads(dh_in, dy, dgate, dw_post, dw_pre)
 
