@@ -2,7 +2,9 @@
 
 Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into a
 shared library with the CUDA runtime linked statically, so the library loads
-(and its symbols can be listed) on a machine without a GPU driver.
+(and its symbols can be listed) on a machine without a GPU driver.  The binding
+of the 8-bit operators (``csrc/torch_ops.cpp``, host code against torch's
+headers) is compiled beside them into ``_torch_ops.so``.
 """
 from __future__ import annotations
 
@@ -25,6 +27,10 @@ LIB = os.path.join(PKG, "libtmagemm.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libtmagemm_checked.so")
 
+# The native binding of the 8-bit operators for torch tensors.
+OPS = os.path.join(PKG, "_torch_ops.so")
+OPS_SOURCE = os.path.join(CSRC, "torch_ops.cpp")
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "--expt-relaxed-constexpr"]
@@ -44,6 +50,53 @@ def _sources():
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+
+
+def _ops_command(out: str):
+    """The compiler call for _torch_ops.so (this interpreter, this torch)."""
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+            "-I", sysconfig.get_paths()["include"], OPS_SOURCE, "-o", out,
+            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-ltorch"]
+
+
+def _ops_stamp() -> str:
+    import torch
+    h = hashlib.sha256(" ".join((platform.machine(), sys.version, torch.__version__,
+                                 " ".join(_ops_command(OPS)))).encode())
+    for d in (OPS_SOURCE, os.path.join(INCLUDE, "tmagemm.h"), os.path.abspath(__file__)):
+        with open(d, "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
+
+
+def _start_ops(force: bool):
+    """Starts compiling _torch_ops.so; None if it is up to date."""
+    if not force and os.path.exists(OPS) and os.path.exists(OPS + ".stamp"):
+        with open(OPS + ".stamp") as f:
+            if f.read().strip() == _ops_stamp():
+                return None
+    cmd = _ops_command(OPS + ".tmp")
+    return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish_ops(started) -> None:
+    if started is None:
+        return
+    cmd, p = started
+    out, _ = p.communicate()
+    if p.returncode != 0:
+        raise RuntimeError("compiling the torch binding failed:\n" + " ".join(cmd) + "\n"
+                           + out.decode(errors="replace"))
+    os.replace(OPS + ".tmp", OPS)
+    with open(OPS + ".stamp", "w") as f:
+        f.write(_ops_stamp() + "\n")
 
 
 def _stamp(flags) -> str:
@@ -74,7 +127,16 @@ def up_to_date(lib: str = LIB, flags=None) -> bool:
 def build(force: bool = False, verbose: bool = False, extra_flags=None,
           checked: bool = False) -> str:
     """Compile every CUDA source and link libtmagemm.so (or, with checked=True,
-    libtmagemm_checked.so); returns its path."""
+    libtmagemm_checked.so), and the torch binding beside it; returns the
+    library's path."""
+    ops = _start_ops(force)
+    try:
+        return _build_library(force, verbose, extra_flags, checked)
+    finally:
+        _finish_ops(ops)
+
+
+def _build_library(force: bool, verbose: bool, extra_flags, checked: bool) -> str:
     lib_path = LIB_CHECKED if checked else LIB
     build_dir = BUILD_CHECKED if checked else BUILD
     flags = ARCH + NVCC_FLAGS + (["-DTMAGEMM_CHECKED"] if checked else []) + list(extra_flags or [])
