@@ -478,13 +478,47 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
             empty_at = empty0 + 8u * slot;
             t_acc = t_base + slot * C::kAccCols;
         };
-        for (int32_t u = unit0; u < num_units; u += unit_step) {
+        // The tile that is being scaled, or about to be: this warp's 32 rows from
+        // y and kCols columns from x of D.
+        const int32_t last = prob.k_blocks - 1;
+        int32_t y = 0, x = 0, row_end = 0;
+        // Its scales: the row's for four k-blocks at a time, read while the four
+        // before them are used (loads issued one by one as they are used would
+        // make every use wait for the newest: a warp waits for all loads it has
+        // in flight), and the weights' for 32, one per lane.  Lanes past the
+        // last row read that row's (their sums are not stored), and blocks past
+        // the last read the last.  A warp's columns lie in two blocks of weight
+        // scales at most.
+        const float *sa = prob.sa, *sb = prob.sb, *sb2 = prob.sb;
+        float sa_next[4], sb_next[2] = {};
+        auto fetch = [&](int32_t kb0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sa_next[j] = sa[min(kb0 + j, last) * prob.sa_blk];
+        };
+        auto fetch_sb = [&](int32_t kb) {
+            sb_next[0] = sb[min(kb + lane, last)];
+            if constexpr (C::kTwoBlocks) sb_next[1] = sb2[min(kb + lane, last)];
+        };
+        // Moves on to tile u and starts on its first scales, which so travel while
+        // the tile before it is stored.
+        auto begin_tile = [&](int32_t u) {
+            if (u >= num_units) return;
             const Fp8Unit t = unit_of<C>(prob, start, u);
-            // This warp's 32 rows and kCols columns of D.
-            const int32_t y = t.row0 + static_cast<int32_t>(rank * C::BM + quarter * 32u);
-            const int32_t x = t.n0 + static_cast<int32_t>(col);
-            const int32_t last = prob.k_blocks - 1;
-            if (y >= t.row_end) {
+            y = t.row0 + static_cast<int32_t>(rank * C::BM + quarter * 32u);
+            x = t.n0 + static_cast<int32_t>(col);
+            row_end = t.row_end;
+            if (y >= row_end) return;
+            sa = prob.sa + min(y + lane, row_end - 1) * prob.sa_row;
+            const int32_t nb = min(x / kFp8Block, prob.n_blocks - 1);
+            sb = prob.sb +
+                 (static_cast<int64_t>(t.group) * prob.n_blocks + nb) * prob.k_blocks;
+            sb2 = nb + 1 < prob.n_blocks ? sb + prob.k_blocks : sb;
+            fetch_sb(0);
+            fetch(0);
+        };
+        begin_tile(unit0);
+        for (int32_t u = unit0; u < num_units; u += unit_step) {
+            if (y >= row_end) {
                 // No row of this warp exists: it only hands the accumulators back.
                 for (int32_t kb = 0; kb <= last; ++kb) {
                     if (!__all_sync(0xffffffffu,
@@ -494,34 +528,12 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                     mbar_arrive_if(lane == 0, empty_at);
                     next_acc();
                 }
+                begin_tile(u + unit_step);
                 continue;
             }
-            // Scales: the row's for four k-blocks at a time, read while the four
-            // before them are used (loads issued one by one as they are used
-            // would make every use wait for the newest: a warp waits for all
-            // loads it has in flight), and the weights' for 32, one per lane.
-            // Lanes past the last row read that row's (their sums are not
-            // stored), and blocks past the last read the last.
-            const float* sa = prob.sa + min(y + lane, t.row_end - 1) * prob.sa_row;
-            const int32_t nb = min(x / kFp8Block, prob.n_blocks - 1);
-            const int32_t nb2 = min(nb + 1, prob.n_blocks - 1);
-            const float* sb = prob.sb + static_cast<int64_t>(t.group) * prob.n_blocks *
-                                            prob.k_blocks;
             // The first piece in the second block of weight scales.
             const int32_t second = (kFp8Block - x % kFp8Block) / 32;
-            float sa_next[4], sb_lane[2] = {}, sb_next[2] = {};
-            auto fetch_sb = [&](int32_t kb) {
-                sb_next[0] = sb[static_cast<int64_t>(nb) * prob.k_blocks + min(kb + lane, last)];
-                if constexpr (C::kTwoBlocks)
-                    sb_next[1] =
-                        sb[static_cast<int64_t>(nb2) * prob.k_blocks + min(kb + lane, last)];
-            };
-            fetch_sb(0);
-            auto fetch = [&](int32_t kb0) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sa_next[j] = sa[min(kb0 + j, last) * prob.sa_blk];
-            };
-            fetch(0);
+            float sb_lane[2] = {};
             float acc[C::kCols];
 #pragma unroll
             for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
@@ -602,6 +614,9 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                 }
             }
             // ---- round, stage in shared memory, store ----
+            const int32_t y0 = y, x0 = x;
+            const int32_t left = row_end - y;   // rows of this warp that exist
+            begin_tile(u + unit_step);
             if (lane == 0) bulk_wait_group_read<0>();   // the last tile's stores have left
             __syncwarp();
 #pragma unroll
@@ -616,7 +631,6 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                                               __float_as_uint(acc[8 * c + 2 * i + 1]));
                 st_shared_v4(at, p[0], p[1], p[2], p[3]);
             }
-            const int32_t left = t.row_end - y;   // rows of this warp that exist
             const bool whole = !C::kGrouped || left >= 32;
             if (whole) {
                 fence_proxy_async_smem();
@@ -624,10 +638,10 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                 if (lane == 0 && left > 0) {
 #pragma unroll
                     for (int b = 0; b < C::kBoxes; ++b)
-                        if (x + C::kBoxCols * b < prob.N &&
-                            check_ok((x & 7) == 0 && x >= 0 && y >= 0, err, kSiteCheckTma))
-                            tma_store_2d(&prob.tmD, buf + b * C::kBoxBytes, x + C::kBoxCols * b,
-                                         y);
+                        if (x0 + C::kBoxCols * b < prob.N &&
+                            check_ok((x0 & 7) == 0 && x0 >= 0 && y0 >= 0, err, kSiteCheckTma))
+                            tma_store_2d(&prob.tmD, buf + b * C::kBoxBytes, x0 + C::kBoxCols * b,
+                                         y0);
                     bulk_commit_group();
                 }
             } else {
@@ -640,13 +654,13 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                 for (int32_t r = lane / kLanes; r < left; r += 32 / kLanes) {
 #pragma unroll
                     for (int b = 0; b < C::kBoxes; ++b) {
-                        const int32_t n = x + C::kBoxCols * b + 8 * chunk;
+                        const int32_t n = x0 + C::kBoxCols * b + 8 * chunk;
                         const uint4 v = *reinterpret_cast<const uint4*>(
                             smem + (buf - sbase) + b * C::kBoxBytes + C::box_at(r, chunk));
-                        if (n < prob.N && check_ok(y + r < prob.rows && n + 8 <= prob.N, err,
+                        if (n < prob.N && check_ok(y0 + r < prob.rows && n + 8 <= prob.N, err,
                                                    kSiteCheckBounds))
                             *reinterpret_cast<uint4*>(
-                                prob.d + static_cast<int64_t>(y + r) * prob.N + n) = v;
+                                prob.d + static_cast<int64_t>(y0 + r) * prob.N + n) = v;
                     }
                 }
                 __syncwarp();
