@@ -22,7 +22,8 @@
 // columns each): while one sets up or reduces, the other streams.
 //
 // Measured on GB300 (device time, weights colder than L2): 1 x 4096 x 14336
-// 11.4 us (5.1 TB/s of weights), 32 x 14336 x 4096 12.8 us.  A kernel that
+// 11.3 us (5.2 TB/s of weights), 32 x 14336 x 4096 12.5 us, 100 x 14336 x 4096
+// 18.1 us.  A kernel that
 // streamed the weights into mma.sync fragments, as the 16-bit few-row kernel
 // does, took 12.6 us at one token and 19.7 us at 16.
 #include <cuda.h>
@@ -60,20 +61,6 @@ struct FewCfg {
     static_assert(NP * kPartStride * 4 <= STAGES * kStageBytes, "partial tile over the ring");
     static_assert(kStageBytes % 1024 == 0, "swizzle atoms stay aligned");
 };
-
-constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {   // e4m3 operands, FP32 sums
-    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                         uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 
 struct FewProblem {
     CUtensorMap tmW;   // B {K, N}, box {128, 128}
@@ -192,8 +179,8 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
                 const uint64_t x_desc = x_desc0 + s * (C::kStageBytes / 16);
 #pragma unroll
                 for (int j = 0; j < C::BK / 32; ++j)   // 32 k = 32 bytes = 2 address units
-                    mma_e4m3(tmem_base + a * C::NP, w_desc + 2 * j, x_desc + 2 * j, kIdesc,
-                             j != 0 ? 1u : 0u);
+                    mma_e4m3<false>(tmem_base + a * C::NP, w_desc + 2 * j, x_desc + 2 * j, kIdesc,
+                                    j != 0 ? 1u : 0u);
                 mma_commit(empty_bar(s));
                 mma_commit(acc_full_bar(a));
             }
@@ -230,7 +217,7 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
                 next[j] = token && kb + j < kb1 ? sa[(kb + j) * prob.sa_blk] * sb[kb + j] : 0.0f;
         };
         fetch(kb0);
-        float acc[C::kCols] = {};
+        f32x2 acc[C::kCols / 2] = {};
         bool ok = true;
         uint32_t it = 0;
         for (int32_t kb = kb0; kb < kb1; kb += 4) {
@@ -268,12 +255,10 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
                     }
 #pragma unroll
                     for (int i = 0; i < kPart; i += 4) {
-                        const float4 f =
-                            *reinterpret_cast<const float4*>(sc + j * C::NP + col0 + c + i);
-                        scale_add(acc[c + i], v[i], f.x);
-                        scale_add(acc[c + i + 1], v[i + 1], f.y);
-                        scale_add(acc[c + i + 2], v[i + 2], f.z);
-                        scale_add(acc[c + i + 3], v[i + 3], f.w);
+                        const float4 f = *reinterpret_cast<const float4*>(
+                            sc + j * C::NP + col0 + c + i);
+                        scale_add(acc[(c + i) / 2], v[i], v[i + 1], pack_f32x2(f.x, f.y));
+                        scale_add(acc[(c + i) / 2 + 1], v[i + 2], v[i + 3], pack_f32x2(f.z, f.w));
                     }
                 }
             }
@@ -285,8 +270,12 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
             float* part = reinterpret_cast<float*>(smem);
             const uint32_t n = quarter * 32u + static_cast<uint32_t>(lane);
 #pragma unroll
-            for (int c = 0; c < C::kCols; ++c)
-                if (col0 + c < tokens) part[(col0 + c) * C::kPartStride + n] = acc[c];
+            for (int c = 0; c < C::kCols; c += 2) {
+                float lo, hi;
+                unpack_f32x2(acc[c / 2], lo, hi);
+                if (col0 + c < tokens) part[(col0 + c) * C::kPartStride + n] = lo;
+                if (col0 + c + 1 < tokens) part[(col0 + c + 1) * C::kPartStride + n] = hi;
+            }
         }
     }
 

@@ -78,12 +78,52 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
     return m;
 }
 
-// acc += t * s, with t from TMEM.  Volatile, so that it stays behind the wait
-// for the load that brought t.  (Multiply-adds of packed pairs are half as
-// many instructions for the same cycles, but each loaded register is then
-// copied to form its pair.)
-__device__ __forceinline__ void scale_add(float& acc, uint32_t t, float s) {
-    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(t)), "f"(s));
+// Instruction descriptor of kind::f8f6f4 with e4m3 operands and FP32 sums
+// (both K-major): the fields are those of kind::f16, with operand format 0 =
+// e4m3.
+constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Two packed floats: one multiply-add instruction for both.
+using f32x2 = uint64_t;
+
+__device__ __forceinline__ f32x2 pack_f32x2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack_f32x2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// acc += {t0, t1} * s, each half rounded once, with t0 and t1 from TMEM.  Volatile, so that it stays
+// behind the wait for the load that brought them.
+__device__ __forceinline__ void scale_add(f32x2& acc, uint32_t t0, uint32_t t1, f32x2 s) {
+    asm volatile(
+        "{\n\t.reg .b64 t;\n\t"
+        "mov.b64 t, {%1, %2};\n\t"
+        "fma.rn.f32x2 %0, t, %3, %0;\n\t}"
+        : "+l"(acc)
+        : "r"(t0), "r"(t1), "l"(s));
 }
 
 }  // namespace tmagemm

@@ -9,20 +9,28 @@
 // scalar per row and 128 columns) and add it to FP32 accumulators in their
 // registers, while the next block's MMAs fill another TMEM accumulator.
 //
-// Roles (one CTA per SM, three groups of four warps):
+// Roles (one CTA per SM):
 //   warp 0      TMA producer: A and B k-blocks (128 bytes a row, 128B swizzle)
 //               into a ring of stages;
-//   warps 1, 2  MMA issuers, one per 128-column part of the tile: per k-block four tcgen05.mma.kind::f8f6f4 into
-//               TMEM accumulator it % kAccs, then commits onto the stage's
-//               `empty` barrier and the accumulator's `acc_full` barrier;
+//   warps 1, 2  MMA issuers, one per part (half the columns of a pair's tile;
+//               a CTA's own tile is one part): per k-block four
+//               tcgen05.mma.kind::f8f6f4 into the part's next TMEM accumulator,
+//               then commits onto the stage's `empty` barrier and the
+//               accumulator's `acc_full` barrier;
 //   warps 4..11 scaling and epilogue: two warps per 32 rows, each half of the
-//               tile's columns.  Their accumulators (128 per thread for 256
-//               columns) take the registers that warps 0..3 (2 and 3 idle)
-//               give up.
-// What bounds it: per k-block of a 128 x 256 tile the MMAs take 512 cycles,
-// reading the accumulator 256 (32 lanes x 4 bytes per cycle and quarter) and
-// the scaling 128 packed multiply-adds in each of the two warps of a
-// scheduler, so the scaling fits under the MMAs.
+//               tile's columns.  Their FP32 sums (128 per thread for 256
+//               columns) take the registers that warps 0..3 (3, and 2 for one
+//               part, idle) give up.
+// What bounds it.  Per k-block of a pair's 256 x 256 tile each SM has 256 cycles
+// of MMAs, 256 of TMEM reads (128 lanes x 256 columns, at 32 lanes x 4 bytes per
+// cycle and quarter) and 128 packed multiply-adds in each of the two warps of a
+// scheduler (256 cycles more or less under the reads), and brings 64 KB per
+// pair from L2.  8192^3 runs in 368 to 376 us (2.9 to 3.0 PFLOP/s): without the multiply-adds
+// the same kernel takes 306 us, without the operand loads 343 and without both
+// 261, and with sums left to the tensor cores over all of K (no scales) 306, so
+// what is left is that these three share an SM's time, and L2 (about 14 TB/s
+// into the SMs) is next.  A CTA's own 128 x 128 tile needs 32 KB per k-block
+// and SM for half the work and is bound by L2 (13.4 TB/s).
 //
 // CTA pairs (PAIR): cta_group::2 MMAs on 256 x 256 tiles, each CTA holding 128
 // rows of A and half of B, as in the 16-bit kernel.
@@ -106,32 +114,6 @@ struct Fp8Cfg {
                   "whole parts, epilogue warps, pieces and swizzle atoms");
     static_assert(kStageBytes % 1024 == 0 && kBoxBytes % 1024 == 0, "atoms stay aligned");
 };
-
-// Instruction descriptor of kind::f8f6f4 with e4m3 operands and FP32 sums
-// (both K-major): the fields are those of kind::f16, with operand format 0 =
-// e4m3.
-constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
-    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-template <bool PAIR>
-__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
-    if constexpr (PAIR)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
-}
 
 // One arrival on an mbarrier at a shared::cluster address by the threads whose
 // `p` is not 0; predicated rather than branched around, and relaxed (what it
@@ -414,8 +396,8 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                         const uint32_t d_tmem = tmem_base + a * C::kAccCols;
 #pragma unroll
                         for (int j = 0; j < C::BK / 32; ++j)
-                            mma_e4m3_ss<C::kPair>(d_tmem, a_desc + 2 * j, b_desc + 2 * j, kIdesc,
-                                                  j != 0 ? 1u : 0u);
+                            mma_e4m3<C::kPair>(d_tmem, a_desc + 2 * j, b_desc + 2 * j, kIdesc,
+                                               j != 0 ? 1u : 0u);
                         // The accumulator is full, and this part done with stage
                         // s (in both CTAs of a pair), once these MMAs finish.
                         if constexpr (C::kPair) {
@@ -534,9 +516,9 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
             // The first piece in the second block of weight scales.
             const int32_t second = (kFp8Block - x % kFp8Block) / 32;
             float sb_lane[2] = {};
-            float acc[C::kCols];
+            f32x2 acc[C::kCols / 2];
 #pragma unroll
-            for (int i = 0; i < C::kCols; ++i) acc[i] = 0.0f;
+            for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
             // The pieces go through kBatch register buffers.  Where they take
             // them all at once, a part is read whole and its accumulator goes back
             // to the MMA warp before the first multiply-add.  Where a part takes
@@ -601,9 +583,10 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                         for (int c = 0; c < C::kBatch; ++c) {
                             const int piece = r * C::kBatch + c;
                             const float f = C::kTwoBlocks && piece >= second ? scale[1] : scale[0];
+                            const f32x2 f2 = pack_f32x2(f, f);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                scale_add(acc[32 * piece + i], v[c][i], f);
+                            for (int i = 0; i < 16; ++i)
+                                scale_add(acc[16 * piece + i], v[c][2 * i], v[c][2 * i + 1], f2);
                             if (more) {
                                 if (c == 0 && next_r == 0 && !part_ready()) goto stop;
                                 tmem_ld_32x32b_x32(t_acc + 32 * (next_r * C::kBatch + c), v[c]);
@@ -626,9 +609,11 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                                     C::box_at(static_cast<uint32_t>(lane), c % kChunks);
                 uint32_t p[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    p[i] = pack2_rn<C::kBF16>(__float_as_uint(acc[8 * c + 2 * i]),
-                                              __float_as_uint(acc[8 * c + 2 * i + 1]));
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi;
+                    unpack_f32x2(acc[4 * c + i], lo, hi);
+                    p[i] = pack2_rn<C::kBF16>(__float_as_uint(lo), __float_as_uint(hi));
+                }
                 st_shared_v4(at, p[0], p[1], p[2], p[3]);
             }
             const bool whole = !C::kGrouped || left >= 32;
@@ -748,13 +733,14 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
 }
 
 // Which pair tile: the one whose rounds of tiles over the pairs take less.  A
-// k-block of a 256 x 192 tile takes about 0.8 of one of 256 x 256 (8192^3: 326
-// against 421 ns), so 1237 x 5000 x 2064 (135 tiles in 2 rounds against 100 in 2)
-// runs in 18.1 against 20.3 us and 2048 x 4096 x 4096 (176 in 3 against 128 in 2)
-// in 36.0 against 30.4 us.
+// round of 256 x 192 tiles takes about 0.76 of one of 256 x 256 (4096^3: 10.3
+// against 13.8 us), so 1237 x 5000 x 2064 (135 tiles in 2 rounds against 100 in 2)
+// runs in 17.4 against 19.5 us and 4096^3 (352 in 5 against 256 in 4) in 51.7
+// against 55.1, but 2048 x 4096 x 4096 (176 in 3 against 128 in 2) in 31.8
+// against 29.4 us.  At 8192^3 (19 rounds against 14) both take 368 us.
 bool narrow_pairs(int64_t tile_rows, int64_t N, int pairs) {
     const int64_t wide = ceil_div(tile_rows * ceil_div(N, 256), pairs) * 100;
-    const int64_t narrow = ceil_div(tile_rows * ceil_div(N, 192), pairs) * 80;
+    const int64_t narrow = ceil_div(tile_rows * ceil_div(N, 192), pairs) * 76;
     return narrow < wide;
 }
 
