@@ -43,6 +43,34 @@ __device__ __forceinline__ uint32_t magnitude_bits(float v) {
     return __float_as_uint(v) & 0x7fffffffu;
 }
 
+// Two packed floats: one arithmetic instruction for both, each half rounded
+// once to nearest even.
+using f32x2 = uint64_t;
+
+__device__ __forceinline__ f32x2 pack_f32x2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack_f32x2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+    float lo, hi;
+    unpack_f32x2(v, lo, hi);
+    return lo + hi;
+}
+
 // Eight packed 16-bit values -> FP32.
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4& p, float (&v)[8]) {
@@ -69,6 +97,22 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     p.z = pack2_rn<BF16>(__float_as_uint(v[4]), __float_as_uint(v[5]));
     p.w = pack2_rn<BF16>(__float_as_uint(v[6]), __float_as_uint(v[7]));
     return p;
+}
+
+// The same, in pairs.
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& p, f32x2 (&v)[4]) {
+    float f[8];
+    unpack8<BF16>(p, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack_f32x2(f[2 * i], f[2 * i + 1]);
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const f32x2 (&v)[4]) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack_f32x2(v[i], f[2 * i], f[2 * i + 1]);
+    return pack8<BF16>(f);
 }
 
 // Largest magnitude bits over the 16 lanes of a half warp (all 32 lanes active).
@@ -104,17 +148,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
             : "memory");
 }
 
-// Two packed floats: one multiply-add instruction for both.
-using f32x2 = uint64_t;
-
-__device__ __forceinline__ f32x2 pack_f32x2(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack_f32x2(f32x2 v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
 // acc += {t0, t1} * s, each half rounded once, with t0 and t1 from TMEM.  Volatile, so that it stays
 // behind the wait for the load that brought them.
 __device__ __forceinline__ void scale_add(f32x2& acc, uint32_t t0, uint32_t t1, f32x2 s) {

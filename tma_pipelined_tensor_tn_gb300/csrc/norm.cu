@@ -8,10 +8,22 @@
 //
 // Bound by memory, each operand read once and each result written once.  A CTA
 // walks rows blockIdx.x, + gridDim.x, ...; thread t owns the 8-channel vectors
-// t + i * blockDim.x of every row, so weights and column sums stay in its
-// registers, and it copies its own vectors of the next row into shared memory
-// (cp.async) while the CTA works on this one: no thread reads another's copy,
-// so only the two row sums need a barrier.
+// t + i * blockDim.x of every row, so column sums stay in its registers, and it
+// copies its own vectors of the next rows into shared memory (cp.async) while
+// the CTA works on this one: no thread reads another's copy, so only the row
+// sums need a barrier.  The per-channel weights and gate lie in shared memory
+// too (in registers they made the compiler spill, and a spilled value's load
+// waits behind the row copies in flight: the backward at 4096 x 8192 took 95
+// us, and takes 69).  Vectors past the last channel are zeros, so that a
+// thread's vectors are worked on together, without branches between them.
+// Arithmetic is on packed pairs, half the instructions of scalar FP32.
+//
+// Measured on GB300 (device time, operands colder than L2), h and y 16-bit:
+// forward 8192 x 4096 with a (T, C) gate 53 us (6.3 TB/s), 4096 x 8192 into
+// codes 41 us (5.7 TB/s); backward 8192 x 4096 with both weights 68 us without a
+// gate (5.9 TB/s) and 100 us with a (T, C) gate (5.3 TB/s, where a kernel that
+// only copies the same five operands to three takes 91); one row of 4096
+// channels 3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -27,23 +39,38 @@ namespace {
 
 constexpr int kMaxWarps = 32;
 
-// Sum over the CTA, the same in every thread: each warp by shuffles, then
+// N sums over the CTA, the same in every thread: each warp by shuffles, then
 // every warp adds the warps' sums in the same order.  `slot` alternates, so
 // one barrier separates the uses of a slot.
-__device__ __forceinline__ float cta_sum(float v, float (*slots)[kMaxWarps], uint32_t& slot) {
+template <int N>
+using SumSlots = float[2][N][kMaxWarps];
+
+template <int N>
+__device__ __forceinline__ void cta_sums(float (&v)[N], SumSlots<N>& slots, uint32_t& slot) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
     const int warps = static_cast<int>(blockDim.x) >> 5;
-    if (warps == 1) return v;
+    if (warps == 1) return;
     const int lane = static_cast<int>(threadIdx.x) & 31;
-    float* s = slots[slot];
+    auto& s = slots[slot];
     slot ^= 1u;
-    if (lane == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = lane < warps ? s[lane] : 0.0f;
+    if (lane == 0)
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-    return t;
+        for (int k = 0; k < N; ++k) s[k][threadIdx.x >> 5] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = lane < warps ? s[k][lane] : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], d);
+}
+__device__ __forceinline__ float cta_sum(float v, SumSlots<1>& slots, uint32_t& slot) {
+    float s[1] = {v};
+    cta_sums<1>(s, slots, slot);
+    return s[0];
 }
 
 template <bool BF16>
@@ -57,6 +84,10 @@ __device__ __forceinline__ float to_float(uint16_t v) {
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// The same through L1, for what the CTAs of an SM share.
+__device__ __forceinline__ void cp_async_16_shared(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -66,100 +97,116 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-constexpr int kMaxRowInputs = 5;
+constexpr int kMaxRowInputs = 5, kMaxChannelInputs = 3;
 
-// The T x C operands of a row: their order in a stage, -1 where absent.
+// Where the operands lie in shared memory.  An operand takes V * threads
+// 16-byte slots, vector i of thread t in slot i * threads + t; a stage holds
+// the T x C operands of one row, and the per-channel ones come after the
+// stages.  Offsets are in bytes from a stage (h to dx) or from the start
+// (w_post to gate_c), -1 where absent.
 struct RowInputs {
-    const uint4* base[kMaxRowInputs];
-    int n;
+    const uint4* row[kMaxRowInputs];
+    const uint4* channel[kMaxChannelInputs];
+    int rows, channels;
     int h, y, gate, dh, dx;
-    int stages;   // rows in shared memory: 2, or 1 where two do not fit
+    int w_post, w_pre, gate_c;
+    int step, stage_bytes;   // from a thread's vector to its next, from a stage to the next
+    int stages;              // 1 to 3
 };
 
-// This thread's vectors of the rows of its CTA, in shared memory one row ahead
-// (with one stage, the next row's are fetched when this one is done):
-// vector i of operand a at ring[(stage * n + a) * V + i][thread].
+// This thread's vectors of the rows of its CTA, copied to shared memory up to
+// two rows ahead (with one stage, the next row's are fetched when this one is
+// done).  Vectors past the last channel are zeros.
 template <int V>
 struct RowPipe {
     const RowInputs& in;
-    uint32_t base;    // shared-memory address of this thread's column
-    uint32_t step;    // bytes between consecutive vectors of a thread
+    const uint8_t* mine;   // this thread's first slot
+    uint32_t base;         // its shared-memory address
     int32_t C8;
-    uint32_t stage = 0;
+    uint32_t at, to;  // offsets of the stages read now and filled next
 
     __device__ __forceinline__ RowPipe(const RowInputs& inputs, uint4* ring, int32_t c8)
-        : in(inputs), base(smem_u32(ring) + threadIdx.x * 16u), step(blockDim.x * 16u), C8(c8) {}
-    __device__ __forceinline__ uint32_t at(uint32_t st, int a, int i) const {
-        return base + ((st * in.n + a) * V + i) * step;
+        : in(inputs), mine(reinterpret_cast<const uint8_t*>(ring + threadIdx.x)),
+          base(smem_u32(ring + threadIdx.x)), C8(c8), at(0), to(0) {}
+    __device__ __forceinline__ bool exists(int i) const {
+        return static_cast<int32_t>(threadIdx.x + i * blockDim.x) < C8;
     }
-    __device__ __forceinline__ void issue(int64_t row, int64_t T, uint32_t st) {
+    __device__ __forceinline__ void next(uint32_t& stage) const {
+        stage += in.stage_bytes;
+        if (stage == static_cast<uint32_t>(in.stages * in.stage_bytes)) stage = 0;
+    }
+    __device__ __forceinline__ void issue(int64_t row, int64_t T) {
         if (row < T) {
-            for (int a = 0; a < in.n; ++a)
+            const int64_t first = row * C8 + threadIdx.x;
+            uint32_t dst = base + to;
+            for (int a = 0; a < in.rows; ++a)
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-                    if (c < C8) cp_async_16(at(st, a, i), in.base[a] + row * C8 + c);
-                }
+                for (int i = 0; i < V; ++i, dst += in.step)
+                    if (exists(i)) cp_async_16(dst, in.row[a] + first + i * blockDim.x);
         }
         cp_async_commit();
+        next(to);
     }
-    // Before a row: starts on the copies of row `next`, waits for this row's.
-    __device__ __forceinline__ void begin(int64_t next, int64_t T) {
-        if (in.stages == 2) {
-            issue(next, T, stage ^ 1u);
+    __device__ __forceinline__ void start(int64_t row, int64_t T) {
+        const int32_t all = in.stages * in.rows + in.channels;
+        for (int i = 0; i < V; ++i)
+            if (!exists(i))
+                for (int a = 0; a < all; ++a)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
+                                 ::"r"(base + (a * V + i) * in.step), "r"(0u)
+                                 : "memory");
+        uint32_t dst = base + in.stages * in.stage_bytes;
+        for (int a = 0; a < in.channels; ++a)
+#pragma unroll
+            for (int i = 0; i < V; ++i, dst += in.step)
+                if (exists(i))
+                    cp_async_16_shared(dst, in.channel[a] + threadIdx.x + i * blockDim.x);
+        issue(row, T);
+        if (in.stages == 3) issue(row + gridDim.x, T);
+    }
+    // Before a row: starts on a later one's copies, waits for this one's.
+    __device__ __forceinline__ void begin(int64_t row, int64_t T) {
+        if (in.stages == 3) {
+            issue(row + 2 * gridDim.x, T);
+            cp_async_wait<2>();
+        } else if (in.stages == 2) {
+            issue(row + gridDim.x, T);
             cp_async_wait<1>();
         } else {
             cp_async_wait<0>();
         }
     }
     // After a row (its vectors have been read).
-    __device__ __forceinline__ void end(int64_t next, int64_t T) {
-        if (in.stages == 2)
-            stage ^= 1u;
-        else
-            issue(next, T, 0);
+    __device__ __forceinline__ void end(int64_t row, int64_t T) {
+        next(at);
+        if (in.stages == 1) issue(row + gridDim.x, T);
     }
     template <bool BF16>
-    __device__ __forceinline__ void read(int a, int i, float (&v)[8]) const {
-        uint4 p;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(p.x), "=r"(p.y), "=r"(p.z), "=r"(p.w)
-                     : "r"(at(stage, a, i))
-                     : "memory");
-        unpack8<BF16>(p, v);
+    __device__ __forceinline__ void load(uint32_t from, f32x2 (&v)[4]) const {
+        unpack8<BF16>(*reinterpret_cast<const uint4*>(mine + from), v);
     }
-};
-
-// This thread's vectors of the per-channel operands, kept packed.
-template <int V>
-struct Channels {
-    uint4 w_post[V], w_pre[V], gate[V];
-    __device__ __forceinline__ explicit Channels(const NormArgs& p) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            w_post[i] = p.w_post && c < p.C8 ? p.w_post[c] : z;
-            w_pre[i] = p.w_pre && c < p.C8 ? p.w_pre[c] : z;
-            gate[i] = p.gate_mode == kGateChannel && c < p.C8
-                          ? static_cast<const uint4*>(p.gate)[c]
-                          : z;
-        }
+    // Vector i of a row's operand, and of a per-channel one.
+    template <bool BF16>
+    __device__ __forceinline__ void read(int operand, int i, f32x2 (&v)[4]) const {
+        load<BF16>(at + operand + i * in.step, v);
+    }
+    template <bool BF16>
+    __device__ __forceinline__ void channels(int operand, int i, f32x2 (&v)[4]) const {
+        load<BF16>(operand + i * in.step, v);
     }
 };
 
 // The gate of vector i of the current row; `token` is a per-token gate (or 1).
 template <bool BF16, int V>
-__device__ __forceinline__ void gate8(const NormArgs& p, const Channels<V>& ch,
-                                      const RowPipe<V>& pipe, float token, int i,
-                                      float (&g)[8]) {
+__device__ __forceinline__ void gate8(const NormArgs& p, const RowPipe<V>& pipe, float token,
+                                      int i, f32x2 (&g)[4]) {
     if (p.gate_mode == kGateChannel) {
-        unpack8<BF16>(ch.gate[i], g);
+        pipe.template channels<BF16>(pipe.in.gate_c, i, g);
     } else if (p.gate_mode == kGateElement) {
         pipe.template read<BF16>(pipe.in.gate, i, g);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = token;
+        for (int e = 0; e < 4; ++e) g[e] = pack_f32x2(token, token);
     }
 }
 
@@ -176,83 +223,84 @@ template <bool BF16, int V, int MAX_THREADS, int MIN_CTAS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS)
 norm_forward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ RowInputs in) {
     extern __shared__ uint4 ring[];
-    __shared__ float slots[2][kMaxWarps];
+    __shared__ SumSlots<1> slots;
     grid_launch_dependents();
     grid_dependency_wait();
     const int32_t C8 = p.C8;
     const float channels = 8.0f * static_cast<float>(C8);
+    const f32x2 alpha = pack_f32x2(p.alpha, p.alpha);
     uint32_t slot = 0;
     RowPipe<V> pipe(in, ring, C8);
-    pipe.issue(blockIdx.x, p.T, 0);
+    pipe.start(blockIdx.x, p.T);
     float token_next = token_gate<BF16>(p, blockIdx.x);
-    const Channels<V> ch(p);
-    for (int64_t row = blockIdx.x; row < p.T; pipe.end(row + gridDim.x, p.T), row += gridDim.x) {
-        pipe.begin(row + gridDim.x, p.T);
+    for (int64_t row = blockIdx.x; row < p.T; pipe.end(row, p.T), row += gridDim.x) {
+        pipe.begin(row, p.T);
         const float token = token_next;
         token_next = token_gate<BF16>(p, row + gridDim.x);
-        float h[V][8];
+        f32x2 h[V][4];
         float r = 1.0f;
         if (p.w_post) {
-            float ss = 0.0f;
+            f32x2 ss = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (static_cast<int32_t>(threadIdx.x + i * blockDim.x) >= C8) continue;
-                float y[8];
+                f32x2 y[4];
                 pipe.template read<BF16>(in.y, i, y);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+                for (int e = 0; e < 4; ++e) ss = fma2(y[e], y[e], ss);
             }
-            r = __frsqrt_rn(cta_sum(ss, slots, slot) / channels + p.eps);
+            r = __frsqrt_rn(cta_sum(sum2(ss), slots, slot) / channels + p.eps);
             if (p.rstd_post && threadIdx.x == 0) p.rstd_post[row] = r;
         }
-        float ss = 0.0f;
+        f32x2 ss = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = 0.0f;
-            if (c >= C8) continue;
             pipe.template read<BF16>(in.h, i, h[i]);
             if (p.y) {
-                float y[8], g[8];
+                f32x2 y[4], g[4];
                 pipe.template read<BF16>(in.y, i, y);
-                gate8<BF16>(p, ch, pipe, token, i, g);
+                gate8<BF16>(p, pipe, token, i, g);
                 if (p.w_post) {
-                    float w[8];
-                    unpack8<BF16>(ch.w_post[i], w);
+                    f32x2 w[4];
+                    pipe.template channels<BF16>(in.w_post, i, w);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
+                    for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], pack_f32x2(r, r)), w[e]);
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[i][e] = fmaf(p.alpha, g[e] * y[e], h[i][e]);
-                p.h_out[row * C8 + c] = pack8<BF16>(h[i]);
+                for (int e = 0; e < 4; ++e) h[i][e] = fma2(alpha, mul2(g[e], y[e]), h[i][e]);
+                if (c < C8) p.h_out[row * C8 + c] = pack8<BF16>(h[i]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+            for (int e = 0; e < 4; ++e) ss = fma2(h[i][e], h[i][e], ss);
         }
         if (!p.w_pre) continue;
-        r = __frsqrt_rn(cta_sum(ss, slots, slot) / channels + p.eps);
+        r = __frsqrt_rn(cta_sum(sum2(ss), slots, slot) / channels + p.eps);
         if (p.rstd_pre && threadIdx.x == 0) p.rstd_pre[row] = r;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-            float x[8], w[8];
-            unpack8<BF16>(ch.w_pre[i], w);   // zeros past the last channel
+            f32x2 x[4], w[4];
+            pipe.template channels<BF16>(in.w_pre, i, w);   // zeros past the last channel
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = h[i][e] * r * w[e];
+            for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(h[i][e], pack_f32x2(r, r)), w[e]);
             if (p.x) {
                 if (c < C8) p.x[row * C8 + c] = pack8<BF16>(x);
                 continue;
             }
+            float v[8];
             uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, c < C8 ? magnitude_bits(x[e]) : 0u);
-            const BlockScale b = block_scale(__uint_as_float(half_warp_max(m)));
+            for (int e = 0; e < 4; ++e) {
+                unpack_f32x2(x[e], v[2 * e], v[2 * e + 1]);
+                m = max(m, max(magnitude_bits(v[2 * e]), magnitude_bits(v[2 * e + 1])));
+            }
+            // (A lane past the last channel takes no part.)
+            const BlockScale b = block_scale(__uint_as_float(half_warp_max(c < C8 ? m : 0u)));
             if (c < C8) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], b.inverse);
-                p.q[row * C8 + c] = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]),
-                                               e4m3x4(x[4], x[5], x[6], x[7]));
+                for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], b.inverse);
+                p.q[row * C8 + c] = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]),
+                                               e4m3x4(v[4], v[5], v[6], v[7]));
                 if ((threadIdx.x & 15) == 0) p.scales[row * p.s_row + (c >> 4) * p.s_blk] = b.scale;
             }
         }
@@ -268,6 +316,10 @@ norm_forward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ 
 // g; and with a per-channel gate both dw_post = g S and dgate = w_post S come
 // from the one column sum S = sum alpha t m.  So a row needs two sums and a
 // column two accumulators.  h' is recomputed from h and y, unrounded.
+// The second sum waits for t, and t for the first; but with t0 = dh' + rh p,
+//   sum(t g u) = sum(t0 g u) - rh mean(p n) sum(n g u),
+// so three sums of what is known at once replace them, with one barrier per row
+// (8192 x 4096, both weights: 85 against 90 us with two).
 // The column accumulators are left in `partial` [CTA][2][C]; the second kernel
 // adds them in CTA order, so the sums are the same from run to run.
 // POST (w_post given) and GATE are fixed at compile time: read at run time they
@@ -278,124 +330,139 @@ norm_backward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__
     constexpr int V = 2;
     constexpr bool kTokenLike = GATE == kGateNone || GATE == kGateToken;   // one gate per row
     extern __shared__ uint4 ring[];
-    __shared__ float slots[2][kMaxWarps];
+    // Whether sum(t g u) is wanted.
+    constexpr bool kSecond = POST || GATE == kGateToken;
+    constexpr int kSums = kSecond ? 3 : 1;
+    __shared__ SumSlots<kSums> slots;
     grid_launch_dependents();
     grid_dependency_wait();
     const int32_t C8 = p.C8;
     const float inv_c = 1.0f / (8.0f * static_cast<float>(C8));
     uint32_t slot = 0;
     RowPipe<V> pipe(in, ring, C8);
-    pipe.issue(blockIdx.x, p.T, 0);
-    // The row's two factors and its gate, one row ahead like its operands.
-    float token_next = 1.0f, ry_next = 1.0f, rh_next = 1.0f;
-    auto fetch = [&](int64_t row) {
-        if (row >= p.T) return;
-        if constexpr (GATE == kGateToken) token_next = token_gate<BF16>(p, row);
-        if constexpr (POST) ry_next = p.rstd_post[row];
-        if (p.w_pre) rh_next = p.rstd_pre[row];
-    };
-    fetch(blockIdx.x);
-    const Channels<V> ch(p);
-    float col_a[V][8] = {}, col_b[V][8] = {};
-    for (int64_t row = blockIdx.x; row < p.T; pipe.end(row + gridDim.x, p.T), row += gridDim.x) {
-        pipe.begin(row + gridDim.x, p.T);
-        // alpha times the row's gate where that is one number
-        const float ry = ry_next, rh = rh_next, ag = p.alpha * token_next;
-        fetch(row + gridDim.x);
-        // alpha g of vector i
-        auto scaled_gate = [&](int i, float (&g)[8]) {
-            if constexpr (GATE == kGateChannel) unpack8<BF16>(ch.gate[i], g);
+    pipe.start(blockIdx.x, p.T);
+    // The factors and gates of the CTA's next 32 rows, one row per lane.
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    float ry_lane = 1.0f, rh_lane = 1.0f, token_lane = 1.0f;
+    int at = 0;
+    f32x2 col_a[V][4] = {}, col_b[V][4] = {};
+    for (int64_t row = blockIdx.x; row < p.T; pipe.end(row, p.T), row += gridDim.x) {
+        pipe.begin(row, p.T);
+        if (at == 0) {
+            const int64_t r = row + static_cast<int64_t>(lane) * gridDim.x;
+            if (r < p.T) {
+                if constexpr (GATE == kGateToken) token_lane = token_gate<BF16>(p, r);
+                if constexpr (POST) ry_lane = p.rstd_post[r];
+                if (p.w_pre) rh_lane = p.rstd_pre[r];
+            }
+        }
+        // alpha, times the row's gate where that is one number
+        const float ry = POST ? __shfl_sync(0xffffffffu, ry_lane, at) : 1.0f;
+        const float rh = __shfl_sync(0xffffffffu, rh_lane, at);
+        const float ag = GATE == kGateToken
+                             ? p.alpha * __shfl_sync(0xffffffffu, token_lane, at) : p.alpha;
+        at = (at + 1) & 31;
+        const f32x2 ry2 = pack_f32x2(ry, ry), rh2 = pack_f32x2(rh, rh), ag2 = pack_f32x2(ag, ag);
+        auto vector_gate = [&](int i, f32x2 (&g)[4]) {   // of vector i
+            if constexpr (GATE == kGateChannel)
+                pipe.template channels<BF16>(in.gate_c, i, g);
             if constexpr (GATE == kGateElement) pipe.template read<BF16>(in.gate, i, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = kTokenLike ? ag : p.alpha * g[e];
         };
-        float u[V][8] = {}, t[V][8] = {}, n[V][8];
-        float sum = 0.0f;
+        // gu: u, times the gate where that differs within the row
+        f32x2 gu[V][4] = {}, t[V][4] = {}, n[V][4];
+        f32x2 pn = 0, tu = 0, nu = 0;   // sums of p n, t gu (without n's part) and n gu
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (static_cast<int32_t>(threadIdx.x + i * blockDim.x) >= C8) continue;
-            float w[8];
-            if (POST || in.y >= 0) pipe.template read<BF16>(in.y, i, u[i]);
+            f32x2 w[4];
+            if (POST || in.y >= 0) pipe.template read<BF16>(in.y, i, gu[i]);
             if constexpr (POST) {
-                unpack8<BF16>(ch.w_post[i], w);
+                pipe.template channels<BF16>(in.w_post, i, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[i][e] *= ry * w[e];
+                for (int e = 0; e < 4; ++e) gu[i][e] = mul2(mul2(gu[i][e], ry2), w[e]);
+            }
+            if constexpr (!kTokenLike) {
+                f32x2 g[4];
+                vector_gate(i, g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) gu[i][e] = mul2(gu[i][e], g[e]);
             }
             if (in.dh >= 0) pipe.template read<BF16>(in.dh, i, t[i]);
             if (p.w_pre) {
-                float dx[8], g[8];
+                f32x2 dx[4];
                 pipe.template read<BF16>(in.h, i, n[i]);
-                scaled_gate(i, g);
                 pipe.template read<BF16>(in.dx, i, dx);
-                unpack8<BF16>(ch.w_pre[i], w);
+                pipe.template channels<BF16>(in.w_pre, i, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    n[i][e] = fmaf(g[e], u[i][e], n[i][e]) * rh;
-                    col_b[i][e] = fmaf(dx[e], n[i][e], col_b[i][e]);
-                    dx[e] *= w[e];
-                    sum = fmaf(dx[e], n[i][e], sum);
-                    t[i][e] = fmaf(rh, dx[e], t[i][e]);
+                for (int e = 0; e < 4; ++e) {
+                    n[i][e] = mul2(fma2(ag2, gu[i][e], n[i][e]), rh2);
+                    col_b[i][e] = fma2(dx[e], n[i][e], col_b[i][e]);
+                    dx[e] = mul2(dx[e], w[e]);
+                    pn = fma2(dx[e], n[i][e], pn);
+                    t[i][e] = fma2(rh2, dx[e], t[i][e]);
+                    if constexpr (kSecond) nu = fma2(n[i][e], gu[i][e], nu);
                 }
             }
+            if constexpr (kSecond) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tu = fma2(t[i][e], gu[i][e], tu);
+            }
         }
-        float c1 = 0.0f;
-        if (p.w_pre) c1 = -rh * (cta_sum(sum, slots, slot) * inv_c);
-        // t, and the sum of t u (times alpha g where g differs within the row)
-        sum = 0.0f;
+        float sums[kSums];
+        sums[0] = sum2(pn);
+        if constexpr (kSecond) {
+            sums[1] = sum2(tu);
+            sums[2] = sum2(nu);
+        }
+        if (kSecond || p.w_pre) cta_sums<kSums>(sums, slots, slot);
+        const float c1 = -rh * (sums[0] * inv_c);   // (0 without w_pre)
+        const f32x2 c1_2 = pack_f32x2(c1, c1);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-            if (c >= C8) continue;
             if (p.w_pre) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t[i][e] = fmaf(c1, n[i][e], t[i][e]);
+                for (int e = 0; e < 4; ++e) t[i][e] = fma2(c1_2, n[i][e], t[i][e]);
             }
-            p.dh_in[row * C8 + c] = pack8<BF16>(t[i]);
-            if constexpr (kTokenLike) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e], u[i][e], sum);
-            } else if constexpr (POST) {
-                float g[8];
-                scaled_gate(i, g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fmaf(t[i][e] * g[e], u[i][e], sum);
-            }
+            if (c < C8) p.dh_in[row * C8 + c] = pack8<BF16>(t[i]);
         }
         if (!POST && in.y < 0) continue;
         float c2 = 0.0f;
-        if constexpr (POST || GATE == kGateToken) {
-            c2 = cta_sum(sum, slots, slot);
+        if constexpr (kSecond) {
+            c2 = fmaf(c1, sums[2], sums[1]);
             if (GATE == kGateToken && threadIdx.x == 0)
                 static_cast<float*>(p.dgate)[row] = p.alpha * c2;
-            c2 *= -inv_c * ry * ry * (kTokenLike ? ag : 1.0f);
+            c2 *= -inv_c * ag;   // - mean(q m)
         }
-        // dy = ry (du w_post - (y ry) mean(q m)), the last product through c2
+        const f32x2 c2_2 = pack_f32x2(c2, c2);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
-            if (c >= C8) continue;
-            float g[8], w[8], y[8], out[8];
-            scaled_gate(i, g);
+            f32x2 m[4], w[4], g[4], out[4];
+            pipe.template read<BF16>(in.y, i, m);
+            vector_gate(i, g);
+            if constexpr (POST) pipe.template channels<BF16>(in.w_post, i, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (POST) m[e] = mul2(m[e], ry2);
+                t[i][e] = mul2(t[i][e], ag2);
+            }
             if constexpr (GATE == kGateElement) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) out[e] = p.alpha * t[i][e] * u[i][e];
-                static_cast<uint4*>(p.dgate)[row * C8 + c] = pack8<BF16>(out);
+                for (int e = 0; e < 4; ++e)
+                    out[e] = mul2(t[i][e], POST ? mul2(m[e], w[e]) : m[e]);
+                if (c < C8) static_cast<uint4*>(p.dgate)[row * C8 + c] = pack8<BF16>(out);
             }
-            if constexpr (POST) unpack8<BF16>(ch.w_post[i], w);
-            pipe.template read<BF16>(in.y, i, y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                out[e] = t[i][e] * g[e];   // du
-                // (a column of a per-channel gate's du m, without the gate)
-                const float s = GATE == kGateChannel ? p.alpha * t[i][e] : out[e];
-                if constexpr (POST) {
-                    col_a[i][e] = fmaf(s * ry, y[e], col_a[i][e]);
-                    out[e] = fmaf(out[e] * ry, w[e], c2 * y[e]);
-                } else if constexpr (GATE == kGateChannel) {
-                    col_a[i][e] = fmaf(s, y[e], col_a[i][e]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                out[e] = kTokenLike ? t[i][e] : mul2(t[i][e], g[e]);   // du
+                if constexpr (GATE == kGateChannel)
+                    col_a[i][e] = fma2(t[i][e], m[e], col_a[i][e]);
+                else if constexpr (POST)
+                    col_a[i][e] = fma2(out[e], m[e], col_a[i][e]);
+                if constexpr (POST)
+                    out[e] = mul2(fma2(out[e], w[e], mul2(c2_2, m[e])), ry2);
             }
-            p.dy[row * C8 + c] = pack8<BF16>(out);
+            if (c < C8) p.dy[row * C8 + c] = pack8<BF16>(out);
         }
     }
     float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 16 * C8;
@@ -404,11 +471,11 @@ norm_backward_kernel(const __grid_constant__ NormArgs p, const __grid_constant__
         const int32_t c = static_cast<int32_t>(threadIdx.x + i * blockDim.x);
         if (c >= C8) continue;
 #pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            *reinterpret_cast<float4*>(part + 8 * c + e) =
-                make_float4(col_a[i][e], col_a[i][e + 1], col_a[i][e + 2], col_a[i][e + 3]);
-            *reinterpret_cast<float4*>(part + 8 * (C8 + c) + e) =
-                make_float4(col_b[i][e], col_b[i][e + 1], col_b[i][e + 2], col_b[i][e + 3]);
+        for (int e = 0; e < 4; e += 2) {   // (16-byte aligned)
+            *reinterpret_cast<ulonglong2*>(part + 8 * c + 2 * e) =
+                make_ulonglong2(col_a[i][e], col_a[i][e + 1]);
+            *reinterpret_cast<ulonglong2*>(part + 8 * (C8 + c) + 2 * e) =
+                make_ulonglong2(col_b[i][e], col_b[i][e + 1]);
         }
     }
 }
@@ -463,68 +530,93 @@ int row_threads(int64_t C8, int V) {
     return static_cast<int>(((C8 + V - 1) / V + 31) / 32 * 32);
 }
 
-RowInputs row_inputs(const NormArgs& p, bool backward) {
+// The operands' places for CTAs of `threads` with V vectors each, `per_sm` of
+// them sharing an SM's shared memory.
+RowInputs row_inputs(const NormArgs& p, bool backward, int threads, int V, int per_sm) {
+    constexpr int kMost = 227 * 1024, kEach = 2048;   // (static and reserved, per CTA)
     RowInputs in{};
+    in.step = threads * 16;
+    const int operand = V * in.step;
     auto add = [&](const void* q) {
         if (!q) return -1;
-        in.base[in.n] = static_cast<const uint4*>(q);
-        return in.n++;
+        in.row[in.rows] = static_cast<const uint4*>(q);
+        return operand * in.rows++;
     };
     in.h = add(!backward || p.w_pre ? p.h : nullptr);   // dh' alone needs no h
     in.y = add(p.y);
     in.gate = add(p.gate_mode == kGateElement ? p.gate : nullptr);
     in.dh = add(backward ? p.dh : nullptr);
     in.dx = add(backward ? p.dx : nullptr);
+    in.stage_bytes = operand * in.rows;
+    const void* channel[kMaxChannelInputs] = {
+        p.w_post, p.w_pre, p.gate_mode == kGateChannel ? p.gate : nullptr};
+    for (const void* c : channel) in.channels += c != nullptr;
+    // (One stage always fits: at 16384 channels at most seven operands of 32 KB.)
+    // A third stage pays in the forward (8192 x 2048 into codes 26.6 against 28.5
+    // us, 8192 x 4096 without a gate 10 us of 50), not in the backward (8192 x 4096
+    // without w_post 75.2 against 70.4 us).
+    const int room = kMost / per_sm - kEach - operand * in.channels;
+    in.stages = !backward && 3 * in.stage_bytes <= room ? 3 : 2 * in.stage_bytes <= room ? 2 : 1;
+    int at = in.stages * in.stage_bytes, k = 0;
+    auto place = [&](const void* q) {
+        if (!q) return -1;
+        in.channel[k++] = static_cast<const uint4*>(q);
+        at += operand;
+        return at - operand;
+    };
+    in.w_post = place(channel[0]);
+    in.w_pre = place(channel[1]);
+    in.gate_c = place(channel[2]);
     return in;
 }
 
 template <class K>
-cudaError_t launch_rows(K kernel, ContextMarks& done, const NormArgs& p, RowInputs in,
-                        int64_t ctas, int threads, int V, bool pdl, cudaStream_t stream) {
-    constexpr int kMost = 227 * 1024 - 1024;   // dynamic shared memory, beside the static
-    const int row = in.n * V * threads * 16;   // at most 160 KB (five operands, 16384 channels)
-    in.stages = 2 * row <= kMost ? 2 : 1;
-    const size_t smem = static_cast<size_t>(in.stages) * row;
-    if (cudaError_t e = smem_opt_in(kernel, kMost, done, false)) return e;
+cudaError_t launch_rows(K kernel, ContextMarks& done, const NormArgs& p, bool backward,
+                        int64_t ctas, int threads, int V, int per_sm, bool pdl,
+                        cudaStream_t stream) {
+    const RowInputs in = row_inputs(p, backward, threads, V, per_sm);
+    const int smem = in.stages * in.stage_bytes + in.channels * V * in.step;
+    if (cudaError_t e = smem_opt_in(kernel, 225 * 1024, done, false)) return e;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(ctas)),
                          dim3(static_cast<unsigned>(threads)), smem, stream, 1, pdl, p, in);
 }
 
 template <bool BF16>
 cudaError_t forward_typed(const NormArgs& p, int sms, bool pdl, cudaStream_t stream) {
-    const RowInputs in = row_inputs(p, false);
     // Few rows: a vector per thread, the shortest time for one row.
     static ContextMarks done1, done256, done512, done1024;
     if (p.C8 <= 1024 && (p.C8 <= 32 || p.T <= sms))
-        return launch_rows(norm_forward_kernel<BF16, 1, 1024, 1>, done1, p, in,
-                           p.T < 8 * sms ? p.T : 8 * sms, row_threads(p.C8, 1), 1, pdl, stream);
-    // Two CTAs of 256 threads with 128 registers, or two of 512 with 64: at 8192
-    // x 4096 55 us against 66 us for four of 256 with 64 registers, at 4096 x
-    // 8192 43 us against 50 us for one of 512 with 128.
+        return launch_rows(norm_forward_kernel<BF16, 1, 1024, 1>, done1, p, false,
+                           p.T < 8 * sms ? p.T : 8 * sms, row_threads(p.C8, 1), 1,
+                           p.T <= sms ? 1 : 8, pdl, stream);
+    // How many CTAs share an SM: 1024 threads of narrow CTAs, 768 of 160 to 256
+    // threads, two wider ones.  8192 x 2048 into codes 25.2 us with 1024 threads, 26.1
+    // with 768 and 35.0 with 512; 8192 x 4096 with a (T, C) gate 52.9 us with 768, 56.4
+    // with 512, and 56.8 with 1024, whose rings hold a row less.
     const int threads = row_threads(p.C8, 2);
-    const int64_t most = static_cast<int64_t>(sms) * (threads < 256 ? 512 / threads
-                                                      : threads <= 512 ? 2 : 1);
+    const int per_sm = threads <= 128 ? 1024 / threads : threads <= 256 ? 768 / threads
+                       : threads <= 512 ? 2 : 1;
+    const int64_t most = static_cast<int64_t>(sms) * per_sm;
     const int64_t ctas = p.T < most ? p.T : most;
     if (threads <= 256)
-        return launch_rows(norm_forward_kernel<BF16, 2, 256, 2>, done256, p, in, ctas, threads, 2,
-                           pdl, stream);
+        return launch_rows(norm_forward_kernel<BF16, 2, 256, 4>, done256, p, false, ctas, threads,
+                           2, per_sm, pdl, stream);
     if (threads <= 512)
-        return launch_rows(norm_forward_kernel<BF16, 2, 512, 2>, done512, p, in, ctas, threads, 2,
-                           pdl, stream);
-    return launch_rows(norm_forward_kernel<BF16, 2, 1024, 1>, done1024, p, in, ctas, threads, 2,
-                       pdl, stream);
+        return launch_rows(norm_forward_kernel<BF16, 2, 512, 2>, done512, p, false, ctas, threads,
+                           2, per_sm, pdl, stream);
+    return launch_rows(norm_forward_kernel<BF16, 2, 1024, 1>, done1024, p, false, ctas, threads,
+                       2, per_sm, pdl, stream);
 }
 
 template <bool BF16, bool POST, int GATE>
 cudaError_t backward_rows(const NormArgs& p, int64_t ctas, int threads, bool pdl,
                           cudaStream_t stream) {
-    const RowInputs in = row_inputs(p, true);
     static ContextMarks done512, done1024;
     if (threads <= 512)
-        return launch_rows(norm_backward_kernel<BF16, POST, GATE, 512>, done512, p, in, ctas,
-                           threads, 2, pdl, stream);
-    return launch_rows(norm_backward_kernel<BF16, POST, GATE, 1024>, done1024, p, in, ctas,
-                       threads, 2, pdl, stream);
+        return launch_rows(norm_backward_kernel<BF16, POST, GATE, 512>, done512, p, true, ctas,
+                           threads, 2, 512 / threads, pdl, stream);
+    return launch_rows(norm_backward_kernel<BF16, POST, GATE, 1024>, done1024, p, true, ctas,
+                       threads, 2, 1, pdl, stream);
 }
 
 template <bool BF16, bool POST>
