@@ -63,7 +63,7 @@ def _ops_command(out: str):
             "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
             "-I", sysconfig.get_paths()["include"], OPS_SOURCE, "-o", out,
             "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
-            "-lc10_cuda", "-ltorch"]
+            "-lc10_cuda", "-ltorch_cuda", "-ltorch"]
 
 
 def _ops_stamp() -> str:

@@ -6,9 +6,8 @@
 //
 // The library's functions come in as addresses (bind), so that the module works
 // with either build of the library and links to neither.
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
-#include <ATen/ops/empty_strided.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -91,10 +90,18 @@ void* stream_of(const at::Device& device) {
 
 void* ptr(const MaybeTensor& t) { return t ? t->data_ptr() : nullptr; }
 
+// New tensors on the device of `like`, past the dispatcher (a call makes up to
+// seven).
+Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+Tensor same(const Tensor& like) { return empty(like.sizes(), like.scalar_type(), like); }
+
 // Row scales, consecutive rows next to each other.
 Tensor row_scales(int64_t rows, int64_t cols, const Tensor& like) {
-    return at::empty_strided({rows, blocks(cols)}, {1, std::max<int64_t>(rows, 1)},
-                             like.options().dtype(at::kFloat));
+    return Tensor(at::detail::empty_strided_cuda({rows, blocks(cols)},
+                                                 {1, std::max<int64_t>(rows, 1)}, at::kFloat,
+                                                 like.device()));
 }
 
 std::tuple<Tensor, Tensor> quantize(const Tensor& X, int block_rows) {
@@ -105,10 +112,9 @@ std::tuple<Tensor, Tensor> quantize(const Tensor& X, int block_rows) {
         throw py::value_error("block_rows must be 1 or 128");
     const c10::cuda::CUDAGuard guard(X.device());
     const int64_t M = X.size(0), K = X.size(1);
-    Tensor Q = at::empty_like(X, X.options().dtype(at::kFloat8_e4m3fn));
-    Tensor S = block_rows == 1
-                   ? row_scales(M, K, X)
-                   : at::empty({blocks(M), blocks(K)}, X.options().dtype(at::kFloat));
+    Tensor Q = empty({M, K}, at::kFloat8_e4m3fn, X);
+    Tensor S = block_rows == 1 ? row_scales(M, K, X)
+                               : empty({blocks(M), blocks(K)}, at::kFloat, X);
     require(lib.quantize(M, K, X.data_ptr(), bf16, block_rows, Q.data_ptr(),
                          static_cast<float*>(S.data_ptr()),
                          block_rows == 1 ? 1 : std::max<int64_t>(blocks(K), 1),
@@ -139,7 +145,7 @@ Tensor product(const Tensor& A, const Tensor& SA, const Tensor& B, const Tensor&
     const at::ScalarType type = bf16 ? at::kBFloat16 : at::kHalf;
     if (out) check("out", *out, type, {M, N}, device);
     const c10::cuda::CUDAGuard guard(device);
-    Tensor D = out ? *out : at::empty({M, N}, A.options().dtype(type));
+    Tensor D = out ? *out : empty({M, N}, type, A);
     // A stride that is never stepped (a dimension of one) counts as 1.
     // Broadcast (zero) strides are refused by the library.
     const int64_t row = M > 1 ? SA.stride(0) : 1, block = kb > 1 ? SA.stride(1) : 1;
@@ -201,7 +207,7 @@ tmagemm_norm norm_operands(const Tensor& h, const MaybeTensor& y, const MaybeTen
 }
 
 float* floats(MaybeTensor& t, at::IntArrayRef shape, const Tensor& like) {
-    t = at::empty(shape, like.options().dtype(at::kFloat));
+    t = empty(shape, at::kFloat, like);
     return static_cast<float*>(t->data_ptr());
 }
 
@@ -214,18 +220,18 @@ std::tuple<Tensor, MaybeTensor, MaybeTensor, MaybeTensor, MaybeTensor> norm(
     Tensor h_out = h;
     MaybeTensor x, scales, rstd_post, rstd_pre;
     if (y) {
-        h_out = at::empty_like(h);
+        h_out = same(h);
         p.h_out = h_out.data_ptr();
     }
     if (w_pre && quantize) {
-        x = at::empty_like(h, h.options().dtype(at::kFloat8_e4m3fn));
+        x = empty(h.sizes(), at::kFloat8_e4m3fn, h);
         scales = row_scales(p.T, p.C, h);
         p.q = x->data_ptr();
         p.scales = static_cast<float*>(scales->data_ptr());
         p.s_row_stride = 1;
         p.s_block_stride = std::max<int64_t>(p.T, 1);
     } else if (w_pre) {
-        x = at::empty_like(h);
+        x = same(h);
         p.x = x->data_ptr();
     }
     if (save_rstd && w_post) p.rstd_post = floats(rstd_post, {p.T}, h);
@@ -255,16 +261,16 @@ std::tuple<Tensor, MaybeTensor, MaybeTensor, MaybeTensor, MaybeTensor> norm_back
     const c10::cuda::CUDAGuard guard(device);
     const int64_t need = lib.norm_workspace(p.T, p.C);
     if (need < 0) require(static_cast<int>(need), "norm_residual_backward_workspace_size");
-    Tensor workspace = at::empty({need}, h.options().dtype(at::kByte));
-    Tensor dh_in = at::empty_like(h);
+    Tensor workspace = empty({need}, at::kByte, h);
+    Tensor dh_in = same(h);
     MaybeTensor dy, dgate, dw_post, dw_pre;
     p.dh = dh_in.data_ptr();
     if (y) {
-        dy = at::empty_like(h);
+        dy = same(h);
         p.dy = dy->data_ptr();
     }
     if (gate && p.gate_mode == kElement) {
-        dgate = at::empty_like(h);
+        dgate = same(h);
         p.dgate = dgate->data_ptr();
     } else if (gate) {
         p.dgate = floats(dgate, gate->sizes(), h);
