@@ -69,8 +69,55 @@ struct FewProblem {
     const float *sa, *sb;
     int64_t sa_row, sa_blk;
     uint16_t* d;
-    int32_t M, N, k_blocks, n_tiles, splits, slice;   // slice: k-blocks per CTA of a cluster
+    int32_t M, N, k_blocks, n_tiles, splits;   // splits: CTAs of a cluster
 };
+
+// Tokens first, first + warps, ... below `end` of the tile at (m0, n0): the
+// partial sums of the cluster's CTAs (at most MOST), in slice order, rounded
+// once and stored.  ROWS tokens at a time, whose loads are in flight together (one
+// by one, the store of a 128 x 128 tile took 2 us).
+template <class C, int ROWS, int MOST>
+__device__ __forceinline__ void add_and_store(const FewProblem& prob, const float* part,
+                                              int32_t m0, int32_t n0, int first, int end,
+                                              uint32_t* err) {
+    constexpr int kWarps = C::kThreads / 32;
+    const int n = n0 + 4 * (static_cast<int>(threadIdx.x) % 32);
+    if (n >= prob.N) return;
+    for (int m = first; m < end; m += ROWS * kWarps) {
+        float v[ROWS][MOST][4];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int row = m + r * kWarps;
+            if (row >= end) break;
+            const uint32_t at = smem_u32(part) + (row * C::kPartStride + (n - n0)) * 4u;
+#pragma unroll
+            for (int q = 0; q < MOST; ++q) {
+                if constexpr (MOST == 1)
+                    *reinterpret_cast<float4*>(v[r][0]) = *reinterpret_cast<const float4*>(
+                        part + row * C::kPartStride + (n - n0));
+                else if (q < prob.splits)
+                    ld_shared_cluster_v4(map_to_rank(at, q), v[r][q]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int row = m + r * kWarps;
+            if (row >= end) break;
+            float s[4] = {v[r][0][0], v[r][0][1], v[r][0][2], v[r][0][3]};
+#pragma unroll
+            for (int q = 1; q < MOST; ++q)
+                if (q < prob.splits)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] += v[r][q][e];
+            uint2 out;
+            out.x = pack2_rn<C::kBF16>(__float_as_uint(s[0]), __float_as_uint(s[1]));
+            out.y = pack2_rn<C::kBF16>(__float_as_uint(s[2]), __float_as_uint(s[3]));
+            if (check_ok(m0 + row < prob.M && n + 4 <= prob.N, err, kSiteCheckBounds))
+                *reinterpret_cast<uint2*>(prob.d + static_cast<int64_t>(m0 + row) * prob.N + n) =
+                    out;
+        }
+    }
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm)
@@ -95,8 +142,9 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
     const int32_t tile = static_cast<int32_t>(blockIdx.x) / prob.splits;
     const int32_t n0 = tile % prob.n_tiles * C::BN, m0 = tile / prob.n_tiles * C::NP;
     const int32_t tokens = min(C::NP, prob.M - m0);
-    const int32_t kb0 = static_cast<int32_t>(rank) * prob.slice;
-    const int32_t kb1 = min(prob.k_blocks, kb0 + prob.slice);   // may be <= kb0: no blocks
+    // This CTA's k-blocks [kb0, kb1); may be none.
+    const int32_t kb0 = static_cast<int32_t>(rank) * prob.k_blocks / prob.splits;
+    const int32_t kb1 = (static_cast<int32_t>(rank) + 1) * prob.k_blocks / prob.splits;
 
     grid_launch_dependents();
     if (warp == 0) {
@@ -285,36 +333,40 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
         tc_fence_after();
         tmem_dealloc(tmem_base, C::kTmemCols);
     }
-    // Groups of four outputs of a token, dealt out evenly over the cluster's
-    // CTAs (N is a multiple of 8: a group is either whole or outside).
-    const int cols = min(C::BN, prob.N - n0) / 4;
-    const int total = tokens * cols;
-    const int end = (static_cast<int>(rank) + 1) * total / prob.splits;
-    for (int o = static_cast<int>(rank) * total / prob.splits + static_cast<int>(threadIdx.x);
-         o < end; o += C::kThreads) {
-        const int m = o / cols, n = 4 * (o % cols);
-        const uint32_t local = sbase + (m * C::kPartStride + n) * 4u;
-        float v[8][4];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q < prob.splits) ld_shared_cluster_v4(map_to_rank(local, q), v[q]);
-        float s[4] = {v[0][0], v[0][1], v[0][2], v[0][3]};
-#pragma unroll
-        for (int q = 1; q < 8; ++q)
-            if (q < prob.splits)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] += v[q][e];
-        uint2 out;
-        out.x = pack2_rn<C::kBF16>(__float_as_uint(s[0]), __float_as_uint(s[1]));
-        out.y = pack2_rn<C::kBF16>(__float_as_uint(s[2]), __float_as_uint(s[3]));
-        if (check_ok(m0 + m < prob.M && n0 + n + 4 <= prob.N, err, kSiteCheckBounds))
-            *reinterpret_cast<uint2*>(prob.d + static_cast<int64_t>(m0 + m) * prob.N + n0 + n) =
-                out;
-    }
+    // Each CTA of the cluster adds and stores a share of the tokens, a warp a
+    // token and a lane four outputs (N is a multiple of 8: they are all inside
+    // or all outside).
+    const int first = static_cast<int>(rank) * tokens / prob.splits + warp;
+    const int end = (static_cast<int>(rank) + 1) * tokens / prob.splits;
+    const float* part = reinterpret_cast<const float*>(smem);
+    if (prob.splits == 1)
+        add_and_store<C, 4, 1>(prob, part, m0, n0, first, end, err);
+    else if (prob.splits <= 4)
+        add_and_store<C, 4, 4>(prob, part, m0, n0, first, end, err);
+    else
+        add_and_store<C, 2, 8>(prob, part, m0, n0, first, end, err);
     if (threadIdx.x == 0 && !*abort_flag)
         check_count_unit(err, static_cast<int32_t>(blockIdx.x));
     // Peers' shared memory stays alive until every CTA has read it.
     if (prob.splits > 1) cluster_sync();
+}
+
+// K slices (CTAs of a cluster): the most with which all clusters are resident at
+// once and each CTA has `least` k-blocks (one for 128 tokens, whose store is long
+// enough to be worth sharing: 134 x 1920 x 272 5.5 against 6.6 us undivided; else
+// two).  A cluster lies within a GPC, so clusters of more than two leave some
+// slots empty: kFill is the share, in percent, that clusters of each size fill.
+// 12 x 9728 x 5632 (76 tiles): 11.7 us with 3 slices (228 CTAs), 15.1 with 4 (304);
+// 1 x 4864 x 14336 (38): 13.0 with 7, 17.0 with 8; 5 x 5088 x 2656 (40): 5.6 with 6,
+// 8.6 with 7; 1 x 4096 x 14336 (32): 11.4 with 8, 12.1 with 6.
+int split_count(int64_t tiles, int32_t k_blocks, int sms, int per_sm, int least) {
+    constexpr int kFill[2][9] = {{0, 100, 100, 90, 94, 92, 90, 69, 79},    // one CTA per SM
+                                 {0, 100, 100, 90, 94, 92, 90, 87, 92}};   // two
+    for (int splits = 8; splits > 1; --splits)
+        if (tiles * splits * 100 <= static_cast<int64_t>(sms) * per_sm * kFill[per_sm - 1][splits] &&
+            k_blocks >= least * splits)
+            return splits;
+    return 1;
 }
 
 template <class C>
@@ -331,14 +383,10 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
     p.M = static_cast<int32_t>(g.M);
     p.N = static_cast<int32_t>(g.N);
     p.k_blocks = static_cast<int32_t>(ceil_div(g.K, C::BK));
-    // As many K slices as keep all CTAs resident, each with at least two blocks.
     p.n_tiles = static_cast<int32_t>(ceil_div(g.N, C::BN));
     const int64_t tiles = p.n_tiles * ceil_div(g.M, C::NP);
-    const int64_t slots = static_cast<int64_t>(dev.sms) * C::kCtasPerSm;
-    int splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= slots && p.k_blocks >= 4 * splits) splits *= 2;
-    p.splits = splits;
-    p.slice = static_cast<int32_t>(ceil_div(p.k_blocks, splits));
+    p.splits = split_count(tiles, p.k_blocks, dev.sms, C::kCtasPerSm, C::NP < 128 ? 3 : 1);
+    const int splits = p.splits;
     static ContextMarks attr_done;
     auto kernel = few_rows_fp8_kernel<C>;
     if (cudaError_t e = smem_opt_in(kernel, static_cast<int>(C::kSmemBytes), attr_done)) return e;
