@@ -1,10 +1,14 @@
 /*
- * tmagemm — FP16 "TN" GEMM D = A * B^T and M = 1 GEMV for sm_103a (GB300).
+ * tmagemm — FP16 and BF16 "TN" GEMM D = A * B^T and M = 1 GEMV for sm_103a
+ * (GB300), block-scaled 8-bit linear layers, and the norms between them.
  *
- * C ABI of libtmagemm.so.  Plain pointers and sizes only.  All matrices are
- * dense row-major binary16 (IEEE fp16) with no padding between rows.
+ * C ABI of libtmagemm.so.  Plain pointers and sizes only.  Matrices are dense
+ * row-major with no padding between rows: binary16 (IEEE fp16) for gemm_f16
+ * and gemv_f16, described here; bfloat16 for the gemm_bf16 and gemv_bf16; e4m3
+ * codes with FP32 scales for the 8-bit entry points, which have a section of
+ * their own below.
  *
- * Operation (both entry points): FP32 accumulation inside the kernel and one
+ * Operation (gemm_f16 and gemv_f16): FP32 accumulation inside the kernel and one
  * round-to-nearest-even conversion to fp16 per output element.
  *   - GEMM and its operand layout: "使用 TMA 为 GEMM 建立 Pipeline" (Modern GPU
  *     programming for MLSys), step 4 "完整 Kernel": A (M, K), B (N, K),
@@ -20,8 +24,9 @@
  * Ownership: the caller owns every buffer.  The library allocates no device
  * memory in any call.  A, B and D must not overlap.
  *
- * Execution: gemm_f16 / gemv_f16 validate their arguments on the host, enqueue
- * one kernel on `stream` and return without synchronising.  A CUDA launch
+ * Execution: every call validates its arguments on the host, enqueues its
+ * kernels (one, unless its description says otherwise) on `stream` and returns
+ * without synchronising.  A CUDA launch
  * error is reported as TMAGEMM_ERR_CUDA.  A device-side wait that exceeds its
  * time limit (a pipeline handshake that never completes) makes the kernel stop
  * early and record a sticky error; tmagemm_check() reports it.

@@ -1,4 +1,5 @@
-"""FP16 TN GEMM (D = A @ B.T) and M=1 GEMV for GB300 (sm_103a).
+"""FP16/BF16 TN GEMM (D = A @ B.T), M=1 GEMV and block-scaled 8-bit linear layers
+with the norms between them, for GB300 (sm_103a).
 
 The compute path is the CUDA library ``libtmagemm.so`` built from ``csrc/``;
 this package only marshals arguments to its C ABI (``include/tmagemm.h``).

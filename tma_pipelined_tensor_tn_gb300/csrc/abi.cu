@@ -656,8 +656,8 @@ int gemm_fp8_impl(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
     const Tuning t = process_tuning();
     const Fp8Device dev{g_encode, d->sms, d->pairs, wait_limit_ns(), d->err_word, t.pdl()};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = !offsets && few_rows_fp8(M, N, d->sms) ? launch_few_rows_fp8(g, dev, st)
-                                                                 : launch_gemm_fp8(g, dev, st);
+    const bool few = !offsets && few_rows_fp8(M, N, K, d->sms);
+    const cudaError_t e = few ? launch_few_rows_fp8(g, dev, st) : launch_gemm_fp8(g, dev, st);
     return e == cudaSuccess ? TMAGEMM_OK : TMAGEMM_ERR_CUDA;
 }
 

@@ -1,16 +1,18 @@
-// gemm_fp8 for few rows of activations on tcgen05, with the operands' roles
-// swapped: the weights are the 128-row MMA operand and the activations the
-// narrow one, in blocks of NP = 16, 32, 64 or 128 tokens (rows past M zero), so
-// the work follows the number of tokens and all 128 accumulator lanes hold
-// weight rows.  Bound by streaming the weights; K is split over the CTAs of a
-// cluster so that enough of them stream at once.
+// gemm_fp8 for few rows of activations on tcgen05.  Up to 64 tokens the operands'
+// roles are swapped: the weights are the 128-row MMA operand and the activations
+// the narrow one, in blocks of NP = 16, 32 or 64 tokens (rows past M zero), so the
+// work follows the number of tokens and all 128 accumulator lanes hold weight rows.
+// Blocks of NP = 128 tokens keep the rows themselves.  Bound by streaming the
+// weights; K is split over the CTAs of a cluster so that enough of them stream at
+// once.
 //
-// As in the tile kernel each 128-k block's product has a TMEM accumulator of
-// its own (four of them).  Here a lane is a weight row and a column a token,
-// so a block's scale varies along the columns: the epilogue threads keep
-// SA[token] * SB (the tile's 128 weight rows share one SB per block) of four
-// blocks in shared memory, read as broadcasts, and add
-//   acc[token] += t[token] * scale[token].
+// As in the tile kernel each 128-k block's product has a TMEM accumulator of its
+// own (four of them), added as acc += t * scale.  Swapped, a lane is a weight row
+// and a column a token, so a block's scale varies along the columns: the epilogue
+// threads keep SA[token] * SB (the tile's 128 weight rows share one SB per block) of
+// four blocks in shared memory, read as broadcasts.  Otherwise a lane is a token
+// and its scale one register (100 x 14336 x 4096 15.1 us, swapped 16.4: the
+// broadcast reads of 128 columns took longer than their MMAs).
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, then four scaling warps (eight
 // for 128 tokens, half of the columns each).  The CTAs of a cluster leave their
@@ -22,10 +24,11 @@
 // columns each): while one sets up or reduces, the other streams.
 //
 // Measured on GB300 (device time, weights colder than L2): 1 x 4096 x 14336
-// 11.3 us (5.2 TB/s of weights), 32 x 14336 x 4096 12.5 us, 100 x 14336 x 4096
-// 18.1 us.  A kernel that
-// streamed the weights into mma.sync fragments, as the 16-bit few-row kernel
-// does, took 12.6 us at one token and 19.7 us at 16.
+// 11.4 us (5.1 TB/s of weights), 32 x 14336 x 4096 12.3 us, 12 x 9664 x 5584
+// 12.5 us; 100 x 14336 x 4096, 112 tiles undivided, 15.1 us (two CTAs an SM, with
+// half the accumulators and registers each: 22.3).  A kernel that streamed the
+// weights into mma.sync fragments, as the 16-bit few-row kernel does, took 12.6 us
+// at one token and 19.7 us at 16.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -46,13 +49,16 @@ struct FewCfg {
     static constexpr bool kBF16 = BF16_;
     static constexpr int kEpiThreads = 32 * EPI_WARPS_;
     static constexpr int kThreads = 64 + kEpiThreads, kAccs = 4;
-    static constexpr int kCols = NP_ / (EPI_WARPS_ / 4);   // tokens of one epilogue warp
+    // 128 tokens are as good an MMA operand as 128 weight rows: they keep their role,
+    // so that a lane is a token and its scale one register.
+    static constexpr bool kSwap = NP_ < 128;
+    static constexpr int kCols = NP_ / (EPI_WARPS_ / 4);   // columns of one epilogue warp
     static constexpr uint32_t kTmemCols = kAccs * NP;
     static constexpr uint32_t kWBytes = BN * BK, kXBytes = NP * BK;
     static constexpr uint32_t kStageBytes = kWBytes + kXBytes;
     static constexpr uint32_t kPartStride = BN + 4;   // floats; rows stay 16-byte aligned
-    static constexpr uint32_t kOffScale = STAGES * kStageBytes;   // [2][4][NP] floats
-    static constexpr uint32_t kOffBar = kOffScale + 2 * 4 * NP * 4;
+    static constexpr uint32_t kOffScale = STAGES * kStageBytes;   // [2][4][NP] floats (kSwap)
+    static constexpr uint32_t kOffBar = kOffScale + (kSwap ? 2 * 4 * NP * 4 : 0);
     static constexpr uint32_t kNumBars = 2 * STAGES + 2 * kAccs + 1;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
     static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;
@@ -227,7 +233,8 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
                 const uint64_t x_desc = x_desc0 + s * (C::kStageBytes / 16);
 #pragma unroll
                 for (int j = 0; j < C::BK / 32; ++j)   // 32 k = 32 bytes = 2 address units
-                    mma_e4m3<false>(tmem_base + a * C::NP, w_desc + 2 * j, x_desc + 2 * j, kIdesc,
+                    mma_e4m3<false>(tmem_base + a * C::NP, (C::kSwap ? w_desc : x_desc) + 2 * j,
+                                    (C::kSwap ? x_desc : w_desc) + 2 * j, kIdesc,
                                     j != 0 ? 1u : 0u);
                 mma_commit(empty_bar(s));
                 mma_commit(acc_full_bar(a));
@@ -250,13 +257,16 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
     } else {
         const uint32_t quarter = static_cast<uint32_t>(warp) & 3u;
         const int tid = static_cast<int>(threadIdx.x) - 64;
-        const int col0 = ((warp - 2) >> 2) * C::kCols;   // this warp's first token
+        const int col0 = ((warp - 2) >> 2) * C::kCols;   // this warp's first column
         const uint32_t t_base = tmem_base + ((quarter * 32u) << 16) + col0;
+        const int row = static_cast<int>(quarter) * 32 + lane;   // this lane's accumulator row
         float* scale = reinterpret_cast<float*>(smem + C::kOffScale);
-        // Token `tid`'s scales (and the tile's weight scales) of four blocks at
-        // a time, read while the four before them are used.
-        const bool token = tid < tokens;
-        const float* sa = prob.sa + (token ? (m0 + tid) * prob.sa_row : 0);
+        // A token's scales (times the tile's weight scales) of four blocks at a time,
+        // read while the four before them are used: of the lane's token, or of token
+        // `tid`, which every lane then reads from shared memory.
+        const int mine = C::kSwap ? tid : row;
+        const bool token = mine < tokens;
+        const float* sa = prob.sa + (token ? (m0 + mine) * prob.sa_row : 0);
         const float* sb = prob.sb + static_cast<int64_t>(n0 / kFp8Block) * prob.k_blocks;
         float next[4];
         auto fetch = [&](int32_t kb) {
@@ -270,12 +280,19 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
         uint32_t it = 0;
         for (int32_t kb = kb0; kb < kb1; kb += 4) {
             float* sc = scale + ((kb - kb0) & 4) * C::NP;   // the two buffers in turn
-            if (tid < C::NP) {
+            float now[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sc[j * C::NP + tid] = next[j];
+            for (int j = 0; j < 4; ++j) now[j] = next[j];
+            if constexpr (C::kSwap) {
+                if (tid < C::NP) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sc[j * C::NP + tid] = now[j];
+                }
+                // Also ends the loop in every warp once a wait has failed in one.
+                if (!named_bar_and(1, C::kEpiThreads, ok)) break;
+            } else if (!ok) {
+                break;
             }
-            // Also ends the loop in every warp once a wait has failed in one.
-            if (!named_bar_and(1, C::kEpiThreads, ok)) break;
             fetch(kb + 4);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -303,8 +320,9 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
                     }
 #pragma unroll
                     for (int i = 0; i < kPart; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(
-                            sc + j * C::NP + col0 + c + i);
+                        float4 f = make_float4(now[j], now[j], now[j], now[j]);
+                        if constexpr (C::kSwap)
+                            f = *reinterpret_cast<const float4*>(sc + j * C::NP + col0 + c + i);
                         scale_add(acc[(c + i) / 2], v[i], v[i + 1], pack_f32x2(f.x, f.y));
                         scale_add(acc[(c + i) / 2 + 1], v[i + 2], v[i + 3], pack_f32x2(f.z, f.w));
                     }
@@ -316,13 +334,20 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
         // (After a failed wait stages may still be written: leave them alone.)
         if (named_bar_and(1, C::kEpiThreads, ok)) {
             float* part = reinterpret_cast<float*>(smem);
-            const uint32_t n = quarter * 32u + static_cast<uint32_t>(lane);
 #pragma unroll
-            for (int c = 0; c < C::kCols; c += 2) {
-                float lo, hi;
-                unpack_f32x2(acc[c / 2], lo, hi);
-                if (col0 + c < tokens) part[(col0 + c) * C::kPartStride + n] = lo;
-                if (col0 + c + 1 < tokens) part[(col0 + c + 1) * C::kPartStride + n] = hi;
+            for (int c = 0; c < C::kCols; c += 4) {
+                float v[4];
+                unpack_f32x2(acc[c / 2], v[0], v[1]);
+                unpack_f32x2(acc[c / 2 + 1], v[2], v[3]);
+                if constexpr (C::kSwap) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (col0 + c + i < tokens)
+                            part[(col0 + c + i) * C::kPartStride + row] = v[i];
+                } else if (token) {
+                    *reinterpret_cast<float4*>(part + row * C::kPartStride + col0 + c) =
+                        make_float4(v[0], v[1], v[2], v[3]);
+                }
             }
         }
     }
@@ -352,19 +377,19 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
 }
 
 // K slices (CTAs of a cluster): the most with which all clusters are resident at
-// once and each CTA has `least` k-blocks (one for 128 tokens, whose store is long
-// enough to be worth sharing: 134 x 1920 x 272 5.5 against 6.6 us undivided; else
-// two).  A cluster lies within a GPC, so clusters of more than two leave some
-// slots empty: kFill is the share, in percent, that clusters of each size fill.
-// 12 x 9728 x 5632 (76 tiles): 11.7 us with 3 slices (228 CTAs), 15.1 with 4 (304);
-// 1 x 4864 x 14336 (38): 13.0 with 7, 17.0 with 8; 5 x 5088 x 2656 (40): 5.6 with 6,
-// 8.6 with 7; 1 x 4096 x 14336 (32): 11.4 with 8, 12.1 with 6.
-int split_count(int64_t tiles, int32_t k_blocks, int sms, int per_sm, int least) {
+// once and each CTA has four k-blocks (3 x 2360 x 432, four blocks: 3.0 us
+// undivided, 3.2 in two; 40 x 512 x 2048, sixteen: 4.2 us in four, 4.4 in five).
+// A cluster lies within a GPC, so clusters of more than two leave some slots empty:
+// kFill is the share, in percent, that clusters of each size fill.  12 x 9728 x 5632
+// (76 tiles): 11.7 us with 3 slices (228 CTAs), 15.1 with 4 (304); 1 x 4864 x 14336
+// (38): 13.0 with 7, 17.0 with 8; 5 x 5088 x 2656 (40): 5.6 with 6, 8.6 with 7;
+// 1 x 4096 x 14336 (32): 11.4 with 8, 12.1 with 6.
+int split_count(int64_t tiles, int32_t k_blocks, int sms, int per_sm) {
     constexpr int kFill[2][9] = {{0, 100, 100, 90, 94, 92, 90, 69, 79},    // one CTA per SM
                                  {0, 100, 100, 90, 94, 92, 90, 87, 92}};   // two
     for (int splits = 8; splits > 1; --splits)
-        if (tiles * splits * 100 <= static_cast<int64_t>(sms) * per_sm * kFill[per_sm - 1][splits] &&
-            k_blocks >= least * splits)
+        if (tiles * splits * 100 <= int64_t{sms} * per_sm * kFill[per_sm - 1][splits] &&
+            k_blocks >= 4 * splits)
             return splits;
     return 1;
 }
@@ -385,7 +410,7 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
     p.k_blocks = static_cast<int32_t>(ceil_div(g.K, C::BK));
     p.n_tiles = static_cast<int32_t>(ceil_div(g.N, C::BN));
     const int64_t tiles = p.n_tiles * ceil_div(g.M, C::NP);
-    p.splits = split_count(tiles, p.k_blocks, dev.sms, C::kCtasPerSm, C::NP < 128 ? 3 : 1);
+    p.splits = split_count(tiles, p.k_blocks, dev.sms, C::kCtasPerSm);
     const int splits = p.splits;
     static ContextMarks attr_done;
     auto kernel = few_rows_fp8_kernel<C>;
@@ -405,11 +430,12 @@ cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t st
 
 }  // namespace
 
-// One block of tokens, or more where the 128 x 128 tiles leave room to split K:
-// at 256 x 4096 x 4096 (64 tiles) 10.8 us against 14.8 us for the tile kernel,
-// at 512 x 4096 x 4096 (128 tiles, no split) 16.9 against 15.2 us.
-bool few_rows_fp8(int64_t M, int64_t N, int sms) {
-    return M <= 128 || 2 * ceil_div(M, 128) * ceil_div(N, 128) <= sms;
+// One block of tokens, or more where the 128 x 128 tiles leave room to split a
+// long enough K: 256 x 4096 x 4096 (64 tiles) 10.1 us against 12.2 us for the tile
+// kernel and 512 x 4096 x 4096 (128 tiles, no split) 12.7 against 12.5; 256 x 4096
+// x 2048 7.5 against 8.0 and 256 x 4096 x 1536 6.8 against 6.8.
+bool few_rows_fp8(int64_t M, int64_t N, int64_t K, int sms) {
+    return M <= 128 || (K >= 2048 && 2 * ceil_div(M, 128) * ceil_div(N, 128) <= sms);
 }
 
 cudaError_t launch_few_rows_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {

@@ -24,13 +24,15 @@
 // What bounds it.  Per k-block of a pair's 256 x 256 tile each SM has 256 cycles
 // of MMAs, 256 of TMEM reads (128 lanes x 256 columns, at 32 lanes x 4 bytes per
 // cycle and quarter) and 128 packed multiply-adds in each of the two warps of a
-// scheduler (256 cycles more or less under the reads), and brings 64 KB per
-// pair from L2.  8192^3 runs in 368 to 376 us (2.9 to 3.0 PFLOP/s): without the multiply-adds
-// the same kernel takes 306 us, without the operand loads 343 and without both
-// 261, and with sums left to the tensor cores over all of K (no scales) 306, so
-// what is left is that these three share an SM's time, and L2 (about 14 TB/s
-// into the SMs) is next.  A CTA's own 128 x 128 tile needs 32 KB per k-block
-// and SM for half the work and is bound by L2 (13.4 TB/s).
+// scheduler (256 cycles, more or less under the reads), and takes in 32 KB of
+// operands.  8192^3 runs in 368 to 376 us (2.9 to 3.0 PFLOP/s, 0.41 us per
+// k-block): without the multiply-adds the same kernel takes 306 us, without the
+// operand loads 343 and without both 261, and with sums left to the tensor cores
+// over all of K (no scales) 306.  All SMs together take in about 13.4 TB/s through
+// TMA (128 x 128 tiles: 0.36 us per k-block of 32 KB on 152 SMs, 0.25 on 32),
+// which bounds those tiles and makes 0.36 us per k-block the pair tile's bound
+// too; the multiply-adds are not quite hidden under it.
+// Sixteen epilogue warps of 64 columns (104 registers each) took 621 us.
 //
 // CTA pairs (PAIR): cta_group::2 MMAs on 256 x 256 tiles, each CTA holding 128
 // rows of A and half of B, as in the 16-bit kernel.

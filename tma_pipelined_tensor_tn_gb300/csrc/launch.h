@@ -212,9 +212,9 @@ struct Fp8Device {
 };
 cudaError_t launch_gemm_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
 
-// The same where few_rows_fp8(M, N, sms) (few_rows_fp8.cu): tcgen05 with the
+// The same where few_rows_fp8(M, N, K, sms) (few_rows_fp8.cu): tcgen05 with the
 // weights as the 128-row operand, K split over clusters.
-bool few_rows_fp8(int64_t M, int64_t N, int sms);
+bool few_rows_fp8(int64_t M, int64_t N, int64_t K, int sms);
 cudaError_t launch_few_rows_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
 
 // Map of an e4m3 operand {K, rows, mats} (mats 0: a single matrix, rank 2) in

@@ -623,10 +623,14 @@ template <bool BF16, bool POST>
 cudaError_t backward_gated(const NormArgs& p, int64_t ctas, int threads, bool pdl,
                            cudaStream_t stream) {
     switch (p.gate_mode) {
-        case kGateChannel: return backward_rows<BF16, POST, kGateChannel>(p, ctas, threads, pdl, stream);
-        case kGateToken: return backward_rows<BF16, POST, kGateToken>(p, ctas, threads, pdl, stream);
-        case kGateElement: return backward_rows<BF16, POST, kGateElement>(p, ctas, threads, pdl, stream);
-        default: return backward_rows<BF16, POST, kGateNone>(p, ctas, threads, pdl, stream);
+        case kGateChannel:
+            return backward_rows<BF16, POST, kGateChannel>(p, ctas, threads, pdl, stream);
+        case kGateToken:
+            return backward_rows<BF16, POST, kGateToken>(p, ctas, threads, pdl, stream);
+        case kGateElement:
+            return backward_rows<BF16, POST, kGateElement>(p, ctas, threads, pdl, stream);
+        default:
+            return backward_rows<BF16, POST, kGateNone>(p, ctas, threads, pdl, stream);
     }
 }
 

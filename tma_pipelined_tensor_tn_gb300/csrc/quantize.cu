@@ -4,7 +4,9 @@
 //
 // Bound by memory: each value is read once (2 bytes) and written once (1
 // byte); a block's values stay in registers between the maximum and the
-// rounding.
+// rounding.  Measured on GB300 (device time, cold): rows of 8192 x 14336 57.5 us
+// (6.2 TB/s), 128 x 128 blocks of 4100 x 4096 9.8 us (5.2 TB/s), one row of 4096
+// values 1.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
