@@ -139,3 +139,17 @@ def test_binding_refuses_host_tensors():
         tg.gemm_fp8_grouped(q, s, q[None], s[None], torch.zeros(2, dtype=torch.int32))
     with pytest.raises(TypeError):
         tg.norm_residual(x, x)
+
+
+@pytest.mark.parametrize("source", ["few_rows_fp8.cu", "gemm_fp8.cu"])
+def test_aligned_barriers_follow_a_reconvergence(source):
+    """barrier.cluster.*.aligned and bar.red need the lanes of a warp together: right
+    before each, whatever per-lane branches came earlier, the warp is brought together."""
+    with open(os.path.join(_build.CSRC, source), encoding="utf-8") as f:
+        code = [line.split("//")[0].strip() for line in f]
+    code = [line for line in code if line]
+    at = [i for i, line in enumerate(code) if "cluster_sync" in line or "named_bar_and(" in line]
+    assert at
+    for i in at:
+        before = code[i - 3:i]
+        assert any("__syncwarp()" in b or "__syncthreads()" in b for b in before), code[i - 3:i + 1]

@@ -288,6 +288,7 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sc[j * C::NP + tid] = now[j];
                 }
+                __syncwarp();   // (the barrier is an aligned one)
                 // Also ends the loop in every warp once a wait has failed in one.
                 if (!named_bar_and(1, C::kEpiThreads, ok)) break;
             } else if (!ok) {
@@ -332,6 +333,7 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
         // Every block has been multiplied, so every stage has been read: the
         // partial tile goes over the ring, a column (token) per row of it.
         // (After a failed wait stages may still be written: leave them alone.)
+        __syncwarp();
         if (named_bar_and(1, C::kEpiThreads, ok)) {
             float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -352,6 +354,8 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
         }
     }
 
+    // The cluster barriers are aligned ones: all lanes of a warp arrive together.
+    __syncwarp();
     tc_fence_before();
     if (prob.splits > 1) cluster_sync(); else __syncthreads();
     if (warp == 1) {
@@ -372,6 +376,7 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
         add_and_store<C, 2, 8>(prob, part, m0, n0, first, end, err);
     if (threadIdx.x == 0 && !*abort_flag)
         check_count_unit(err, static_cast<int32_t>(blockIdx.x));
+    __syncwarp();   // (lanes past N left add_and_store early)
     // Peers' shared memory stays alive until every CTA has read it.
     if (prob.splits > 1) cluster_sync();
 }

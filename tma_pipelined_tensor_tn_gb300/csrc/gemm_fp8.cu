@@ -631,6 +631,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                                          y0);
                     bulk_commit_group();
                 }
+                __syncwarp();
             } else {
                 // The group ends inside these 32 rows: plain stores of the rows
                 // that exist, a lane per 16-byte chunk (the next rows are another
@@ -652,10 +653,14 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                 }
                 __syncwarp();
             }
-            if (warp == 4 && lane == 0 && rank == 0) check_count_unit(err, u);
+            if constexpr (kChecked) {
+                if (warp == 4 && lane == 0 && rank == 0) check_count_unit(err, u);
+                __syncwarp();
+            }
         }
     stop:
         if (lane == 0) bulk_wait_group<0>();
+        __syncwarp();
     }
 
     // ---- teardown ----
@@ -665,6 +670,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         if (threadIdx.x == 0 && rank == 0 && !*abort_flag)
             for (int h = 0; h < C::kParts; ++h)
                 check_ok(ring_count[0] == ring_count[1 + h], err, kSiteCheckRing);
+        __syncwarp();
     }
     if constexpr (C::kPair) cluster_sync();
     if (warp == 1) {
