@@ -340,8 +340,9 @@ int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, const float* SA,
  * stream and be captured in a CUDA graph.
  *   G         : 1 <= G <= 384 (more: TMAGEMM_ERR_UNSUPPORTED).
  *   m_offsets : device pointer, G + 1 int32, non-decreasing, within [0, M].
- *               The kernels clamp each to [the previous one, M], so other
- *               values give undefined rows but never an access out of range.
+ *               Any other list counts as each offset raised to the largest
+ *               before it (and 0) and lowered to M, so groups never overlap
+ *               and no access is out of range.
  *   M         : rows of A and D.  Rows outside every group are not written.
  *   B, SB     : G matrices of gemm_fp8's layout, back to back.
  * Other arguments, requirements and results as gemm_fp8; m_offsets 4-byte

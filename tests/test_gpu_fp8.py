@@ -308,6 +308,31 @@ def test_grouped_offsets_out_of_range_are_clamped(tg):
     assert np.array_equal(big[52:92].double().cpu().numpy(), rounded(want, torch.bfloat16))
 
 
+@pytest.mark.parametrize("M,off", [
+    (60, [0, 50, 20, 60]),                          # group 2 starts where group 0 ends
+    (60, [-7, 20, 1 << 30, -(1 << 31), 5]),
+    (60, [40, 10, -3, 7, 55, 12, 90]),
+    (900, [0, 700, 130, 300, 800, 260, 900]),       # rows enough for pair tiles
+    (300, None)])                                   # 384 random offsets
+def test_grouped_offsets_out_of_order_count_as_the_largest_so_far(tg, M, off):
+    """Groups never overlap: each row has one owner, rows without one are left."""
+    rng = np.random.default_rng(14)
+    if off is None:
+        off = rng.integers(-50, M + 50, 385)
+        off[:300] = np.sort(off[:300])
+    off = np.asarray(off)
+    G, N, K = len(off) - 1, 136, 144
+    a, sa, b, sb = grouped_integers(rng, G, M, N, K)
+    out = torch.full((M, N), 5.0, device="cuda", dtype=torch.bfloat16)
+    tg.gemm_fp8_grouped(f8(a), torch.from_numpy(sa).cuda(), f8(b), torch.from_numpy(sb).cuda(),
+                        torch.tensor(off, dtype=torch.int32, device="cuda"), out=out)
+    eff = np.clip(np.maximum.accumulate(off), 0, M)
+    got = out.double().cpu().numpy()
+    for g, (want, _) in enumerate(grouped_reference(a, sa, b, sb, eff)):
+        assert np.array_equal(got[eff[g]:eff[g + 1]], rounded(want, torch.bfloat16)), g
+    assert np.all(got[:eff[0]] == 5.0) and np.all(got[eff[-1]:] == 5.0)
+
+
 def test_grouped_most_groups(tg):
     rng = np.random.default_rng(9)
     G, N, K = 384, 136, 144

@@ -159,20 +159,26 @@ struct Fp8Unit {
     int32_t n0, group;
 };
 
-// Rows [lo, hi) of group g.  Offsets outside [0, rows] or decreasing ones are
-// clamped, so that no offset can lead outside the operands.
+// Rows [lo, hi) of group g.  `ordered`: no offset is outside [0, rows] or below the
+// one before it.  Otherwise each counts as the largest so far, within [0, rows], so
+// that groups neither overlap nor lead outside the operands.
 struct RowRange {
     int32_t lo, hi;
 };
-__device__ __forceinline__ RowRange group_rows(const Fp8Problem& p, int32_t g) {
-    RowRange r;
-    r.lo = min(max(p.offsets[g], 0), p.rows);
-    r.hi = min(max(p.offsets[g + 1], r.lo), p.rows);
+__device__ __forceinline__ RowRange group_rows(const Fp8Problem& p, int32_t g, bool ordered) {
+    RowRange r = {p.offsets[g], p.offsets[g + 1]};
+    if (!ordered) {
+#pragma unroll 1
+        for (int32_t i = 0; i < g; ++i) r.lo = max(r.lo, p.offsets[i]);
+        r.lo = min(max(r.lo, 0), p.rows);
+        r.hi = min(max(r.hi, r.lo), p.rows);
+    }
     return r;
 }
 
 template <class C>
-__device__ __forceinline__ Fp8Unit unit_of(const Fp8Problem& p, const int32_t* start, int32_t u) {
+__device__ __forceinline__ Fp8Unit unit_of(const Fp8Problem& p, const int32_t* start, bool ordered,
+                                           int32_t u) {
     Fp8Unit t;
     if constexpr (C::kGrouped) {
         int32_t lo = 0, hi = p.groups;   // the last group whose first tile is <= u
@@ -180,7 +186,7 @@ __device__ __forceinline__ Fp8Unit unit_of(const Fp8Problem& p, const int32_t* s
             const int32_t mid = (lo + hi) >> 1;
             if (start[mid] <= u) lo = mid; else hi = mid;
         }
-        const RowRange r = group_rows(p, lo);
+        const RowRange r = group_rows(p, lo, ordered);
         const TileCoord tc = tile_coord(u - start[lo], (r.hi - r.lo + C::kTileM - 1) / C::kTileM,
                                         p.grid_n, p.group_m);
         t.row0 = r.lo + tc.m_blk * C::kTileM;
@@ -268,13 +274,24 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
     grid_dependency_wait();
 
     int32_t num_units = prob.num_tiles;
+    bool ordered = true;
     if constexpr (C::kGrouped) {
         // Tiles of each group, then their running sum by one warp.
-        for (int32_t g = static_cast<int32_t>(threadIdx.x); g < prob.groups; g += C::kThreads) {
-            const RowRange r = group_rows(prob, g);
+        auto count_tiles = [&](int32_t g, RowRange r) {
             start[g + 1] = (r.hi - r.lo + C::kTileM - 1) / C::kTileM * prob.grid_n;
+        };
+        for (int32_t g = static_cast<int32_t>(threadIdx.x); g < prob.groups; g += C::kThreads) {
+            const RowRange r = group_rows(prob, g, true);
+            const bool good = 0 <= r.lo && r.lo <= r.hi && r.hi <= prob.rows;
+            if (good) count_tiles(g, r);
+            ordered = ordered && good;
         }
-        __syncthreads();
+        ordered = __syncthreads_and(ordered);
+        if (!ordered) {
+            for (int32_t g = static_cast<int32_t>(threadIdx.x); g < prob.groups; g += C::kThreads)
+                count_tiles(g, group_rows(prob, g, false));
+            __syncthreads();
+        }
         if (warp == 0) {
             int32_t carry = 0;
             for (int32_t g0 = 0; g0 < prob.groups; g0 += 32) {
@@ -303,7 +320,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         uint32_t s = 0, phase = 0, it = 0;
         bool ok = true;
         for (int32_t u = unit0; ok && u < num_units; u += unit_step) {
-            const Fp8Unit t = unit_of<C>(prob, start, u);
+            const Fp8Unit t = unit_of<C>(prob, start, ordered, u);
             // Boxes of A with at least one row, in this CTA and in all.
             int32_t boxes = 1, all_boxes = C::kPair ? 2 : 1;
             if constexpr (C::kGrouped) {
@@ -487,7 +504,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         // the tile before it is stored.
         auto begin_tile = [&](int32_t u) {
             if (u >= num_units) return;
-            const Fp8Unit t = unit_of<C>(prob, start, u);
+            const Fp8Unit t = unit_of<C>(prob, start, ordered, u);
             y = t.row0 + static_cast<int32_t>(rank * C::BM + quarter * 32u);
             x = t.n0 + static_cast<int32_t>(col);
             row_end = t.row_end;
