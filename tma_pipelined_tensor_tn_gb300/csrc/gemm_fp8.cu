@@ -104,7 +104,7 @@ struct Fp8Cfg {
     static constexpr uint32_t kOffBar = kOffD + kEpiWarps * kBoxes * kBoxBytes;
     static constexpr uint32_t kNumBars = 2 * STAGES + 2 * kAccs + kParts;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr uint32_t kOffStart = kOffMisc + 32;   // grouped: tile starts
+    static constexpr uint32_t kOffStart = kOffMisc + 32;   // grouped: tile starts, a flag before
     static constexpr uint32_t kSmemBytes =
         kOffStart + (GROUPED_ ? (kMaxFp8Groups + 1) * 4 : 0) + 1024;
     static_assert(kSmemBytes <= 232448, "fits the 227 KB opt-in shared memory");
@@ -177,8 +177,7 @@ __device__ __forceinline__ RowRange group_rows(const Fp8Problem& p, int32_t g, b
 }
 
 template <class C>
-__device__ __forceinline__ Fp8Unit unit_of(const Fp8Problem& p, const int32_t* start, bool ordered,
-                                           int32_t u) {
+__device__ __forceinline__ Fp8Unit unit_of(const Fp8Problem& p, const int32_t* start, int32_t u) {
     Fp8Unit t;
     if constexpr (C::kGrouped) {
         int32_t lo = 0, hi = p.groups;   // the last group whose first tile is <= u
@@ -186,7 +185,7 @@ __device__ __forceinline__ Fp8Unit unit_of(const Fp8Problem& p, const int32_t* s
             const int32_t mid = (lo + hi) >> 1;
             if (start[mid] <= u) lo = mid; else hi = mid;
         }
-        const RowRange r = group_rows(p, lo, ordered);
+        const RowRange r = group_rows(p, lo, start[-1] == 0);
         const TileCoord tc = tile_coord(u - start[lo], (r.hi - r.lo + C::kTileM - 1) / C::kTileM,
                                         p.grid_n, p.group_m);
         t.row0 = r.lo + tc.m_blk * C::kTileM;
@@ -274,12 +273,12 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
     grid_dependency_wait();
 
     int32_t num_units = prob.num_tiles;
-    bool ordered = true;
     if constexpr (C::kGrouped) {
         // Tiles of each group, then their running sum by one warp.
         auto count_tiles = [&](int32_t g, RowRange r) {
             start[g + 1] = (r.hi - r.lo + C::kTileM - 1) / C::kTileM * prob.grid_n;
         };
+        bool ordered = true;
         for (int32_t g = static_cast<int32_t>(threadIdx.x); g < prob.groups; g += C::kThreads) {
             const RowRange r = group_rows(prob, g, true);
             const bool good = 0 <= r.lo && r.lo <= r.hi && r.hi <= prob.rows;
@@ -304,7 +303,10 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
                 if (g0 + lane < prob.groups) start[g0 + lane + 1] = carry + v;
                 carry += __shfl_sync(0xffffffffu, v, 31);
             }
-            if (lane == 0) start[0] = 0;
+            if (lane == 0) {
+                start[0] = 0;
+                start[-1] = !ordered;   // (a word of shared memory: no register to spare)
+            }
         }
         __syncthreads();
         num_units = start[prob.groups];
@@ -320,7 +322,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         uint32_t s = 0, phase = 0, it = 0;
         bool ok = true;
         for (int32_t u = unit0; ok && u < num_units; u += unit_step) {
-            const Fp8Unit t = unit_of<C>(prob, start, ordered, u);
+            const Fp8Unit t = unit_of<C>(prob, start, u);
             // Boxes of A with at least one row, in this CTA and in all.
             int32_t boxes = 1, all_boxes = C::kPair ? 2 : 1;
             if constexpr (C::kGrouped) {
@@ -504,7 +506,7 @@ gemm_fp8_kernel(const __grid_constant__ Fp8Problem prob, const uint64_t limit_ns
         // the tile before it is stored.
         auto begin_tile = [&](int32_t u) {
             if (u >= num_units) return;
-            const Fp8Unit t = unit_of<C>(prob, start, ordered, u);
+            const Fp8Unit t = unit_of<C>(prob, start, u);
             y = t.row0 + static_cast<int32_t>(rank * C::BM + quarter * 32u);
             x = t.n0 + static_cast<int32_t>(col);
             row_end = t.row_end;
