@@ -343,7 +343,8 @@ int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, const float* SA,
  *               Any other list counts as each offset raised to the largest
  *               before it (and 0) and lowered to M, so groups never overlap
  *               and no access is out of range.
- *   M         : rows of A and D.  Rows outside every group are not written.
+ *   M         : rows of A and D, at most 2^31 - 256 (more:
+ *               TMAGEMM_ERR_UNSUPPORTED).  Rows outside every group are not written.
  *   B, SB     : G matrices of gemm_fp8's layout, back to back.
  * Other arguments, requirements and results as gemm_fp8; m_offsets 4-byte
  * aligned.

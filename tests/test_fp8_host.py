@@ -59,6 +59,13 @@ def test_grouped_refusals(change, expect):
     assert tg.lib().gemm_fp8_grouped(*a.values(), None) == expect
 
 
+def test_grouped_rows_whose_tiles_pass_32_bits_are_refused():
+    """A group of more than 2^31 - 256 rows has a last tile that ends past 2^31."""
+    a = {**dict(G=3, offsets=P), **GEMM, "N": 8, "K": 16}
+    for M in ((1 << 31) - 255, (1 << 31) - 1):
+        assert tg.lib().gemm_fp8_grouped(*{**a, "M": M}.values(), None) == UNSUPPORTED
+
+
 def norm_struct(**fields):
     p = tg.TmagemmNorm()
     for k, v in {**dict(T=4, C=256, alpha=1.0, eps=1e-6, h=P), **fields}.items():

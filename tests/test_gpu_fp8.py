@@ -247,6 +247,39 @@ def test_gemm_result_past_32_bit_offsets(tg):
     assert torch.equal(d[rows].float(), (A[rows].float() @ B.float().t()).bfloat16().float())
 
 
+@pytest.mark.parametrize("grouped", [False, True])
+def test_product_of_the_most_rows(tg, grouped):
+    """The last row whose index fits 32 bits (dense), and as many rows as groups may
+    have, in a last group that starts inside a tile: about 77 GB."""
+    M, N, K = (1 << 31) - (256 if grouped else 1), 8, 16
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of device memory")
+    rng = np.random.default_rng(15)
+    b, _ = integer_operand(rng, N, K, False)
+    B, SB = f8(b), torch.ones((1, 1), device="cuda")
+    A = f8(ref.encode_e4m3(np.arange(16) % 5 - 2)).view(torch.uint8).expand(M, K).contiguous()
+    marks = torch.tensor([0, 1, 4, 5, 6, 300, M // 2, M - 257, M - 129, M - 2, M - 1])
+    A[marks.cuda()] = f8(ref.encode_e4m3(rng.integers(-4, 5, (len(marks), K)))).view(torch.uint8)
+    A = A.view(torch.float8_e4m3fn)
+    SA = torch.ones((M, 1), device="cuda")
+    out = torch.full((M, N), float("nan"), device="cuda", dtype=torch.float16)
+    if grouped:
+        off = torch.tensor([0, 5, M], dtype=torch.int32, device="cuda")
+        tg.gemm_fp8_grouped(A, SA, B.view(torch.uint8).expand(2, N, K).contiguous().view(B.dtype),
+                            SB.expand(2, 1, 1).contiguous(), off, out=out)
+    else:
+        tg.gemm_fp8(A, SA, B, SB, out=out)
+    del SA
+    W = B.float()
+    assert torch.equal(out[marks.cuda()].float(),
+                       A.view(torch.uint8)[marks.cuda()].view(A.dtype).float() @ W.t())
+    row = (f8(ref.encode_e4m3(np.arange(16) % 5 - 2)).float() @ W.t()).half()
+    other = 0
+    for lo in range(0, M, 1 << 27):
+        other += int((out[lo:lo + (1 << 27)] != row).any(dim=1).sum())
+    assert other <= len(marks)
+
+
 # ----------------------------------------------------------------- grouped ----
 
 def grouped_reference(a, sa, b, sb, off):

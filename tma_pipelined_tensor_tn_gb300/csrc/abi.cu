@@ -632,7 +632,9 @@ int gemm_fp8_impl(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
     if ((K % 16) != 0 || (N % 8) != 0 || !aligned16(A) || !aligned16(B) || !aligned16(D) ||
         !aligned4(SA) || !aligned4(SB) || !aligned4(offsets))
         return TMAGEMM_ERR_ALIGN;
-    // Tiles are counted in 32 bits.
+    // Tiles are counted in 32 bits.  A group's last tile may start at any row and end
+    // up to 255 past it, in 32 bits too.
+    if (offsets && M > (int64_t(1) << 31) - 256) return TMAGEMM_ERR_UNSUPPORTED;
     if (G * N > (int64_t(1) << 31) - 1 ||
         (ceil_div(M, 128) + G) * ceil_div(N, 128) > (int64_t(1) << 31) - 1)
         return TMAGEMM_ERR_UNSUPPORTED;

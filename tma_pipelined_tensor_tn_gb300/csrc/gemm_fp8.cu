@@ -193,8 +193,7 @@ __device__ __forceinline__ Fp8Unit unit_of(const Fp8Problem& p, const int32_t* s
         t.n0 = tc.n_blk * C::BN;
         t.group = lo;
     } else {
-        const TileCoord tc = tile_coord(u, (p.rows + C::kTileM - 1) / C::kTileM, p.grid_n,
-                                        p.group_m);
+        const TileCoord tc = tile_coord(u, ceil_div(p.rows, C::kTileM), p.grid_n, p.group_m);
         t.row0 = tc.m_blk * C::kTileM;
         t.row_end = p.rows;
         t.n0 = tc.n_blk * C::BN;
