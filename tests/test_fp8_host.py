@@ -110,6 +110,14 @@ def test_norm_backward_refusals(fields, expect):
     assert tg.lib().norm_residual_backward(ctypes.byref(p), P, 1 << 30, None) == expect
 
 
+@pytest.mark.parametrize("gate_mode", [2, 3])
+def test_norm_backward_of_no_rows_needs_no_gate_gradient_per_row(gate_mode):
+    """With T = 0 a per-token or per-element gate and its gradient are empty (NULL):
+    the call is valid (and fails here only for want of a device)."""
+    p = norm_struct(T=0, h=None, y=None, gate_mode=gate_mode)
+    assert tg.lib().norm_residual_backward(ctypes.byref(p), None, 0, None) != INVALID
+
+
 def test_norm_workspace_refusals():
     f = tg.lib().norm_residual_backward_workspace_size
     assert f(-1, 256) == INVALID and f(4, 0) == INVALID and f(4, 16392) == UNSUPPORTED

@@ -203,6 +203,23 @@ def test_no_rows(tg):
         assert torch.all(t == 0)      # sums over no rows
 
 
+@pytest.mark.parametrize("cols", [1, 264])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, False)])
+def test_no_rows_with_a_gate_per_row(tg, cols, post, pre):
+    C = 264
+    w = torch.ones(C, dtype=torch.bfloat16, device="cuda")
+    e = torch.empty((0, C), dtype=torch.bfloat16, device="cuda")
+    gate = torch.empty((0, cols), dtype=torch.bfloat16, device="cuda")
+    args = {"gate": gate, "w_post": w if post else None, "w_pre": w if pre else None}
+    r = tg.norm_residual(e, e, save_rstd=True, **args)
+    d = tg.norm_residual_backward(e, e, dh=e, dx=e if pre else None, rstd_post=r.rstd_post,
+                                  rstd_pre=r.rstd_pre, **args)
+    assert d.dgate.shape == gate.shape and d.dh.shape == d.dy.shape == (0, C)
+    assert not post or torch.all(d.dw_post == 0)
+    assert not pre or torch.all(d.dw_pre == 0)
+    tg.check()
+
+
 def test_gradients_repeat_their_bits(tg):
     dev, _ = make(2000, 1032, "f16", "channel", True, True)
     r = tg.norm_residual(**dev, save_rstd=True)

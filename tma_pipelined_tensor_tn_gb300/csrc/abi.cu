@@ -773,7 +773,9 @@ int norm_residual_backward(const tmagemm_norm* p, void* workspace, int64_t works
     if (int s = norm_args(p, &a)) return s;
     if (p->T > 0 && (p->w_pre != nullptr) != (p->dx != nullptr)) return TMAGEMM_ERR_INVALID;
     if ((p->w_post && !p->dw_post) || (p->w_pre && !p->dw_pre)) return TMAGEMM_ERR_INVALID;
-    if (p->gate_mode != kGateNone && !p->dgate) return TMAGEMM_ERR_INVALID;
+    // (A gradient with a row per token has none with T = 0 and may be NULL then.)
+    if (p->gate_mode != kGateNone && !p->dgate && (p->T > 0 || p->gate_mode == kGateChannel))
+        return TMAGEMM_ERR_INVALID;
     if (p->T > 0 && (!p->dh || (p->y && !p->dy) || (p->w_post && !p->rstd_post) ||
                      (p->w_pre && !p->rstd_pre)))
         return TMAGEMM_ERR_INVALID;
