@@ -368,7 +368,8 @@ int gemm_fp8_grouped(int64_t G, const int32_t* m_offsets, int64_t M, int64_t N, 
  *   rstd_post, rstd_pre : T floats each, the two rsqrt factors; the forward
  *               writes them where not NULL, the backward reads them.
  * Zero the struct before filling it.  Requirements: 1 <= C <= 16384,
- * C % 8 == 0; T = 0 is OK (nothing is written but zero sums over rows);
+ * C % 8 == 0; T = 0 is OK (nothing is written but zero sums over rows, and
+ * operands with a row per token may be NULL);
  * pointers 16-byte aligned except scales, rstd_*, dw_* and a dgate of floats
  * (4) and a per-token gate (2).  y or w_pre must be given.
  */

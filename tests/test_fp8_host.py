@@ -110,6 +110,18 @@ def test_norm_backward_refusals(fields, expect):
     assert tg.lib().norm_residual_backward(ctypes.byref(p), P, 1 << 30, None) == expect
 
 
+def test_norm_of_no_rows_needs_its_channel_gate():
+    """A per-channel gate has no rows, so it is needed with T = 0 too: the column sums
+    would read it."""
+    p = norm_struct(**{**BACKWARD, "T": 0}, gate_mode=1, dgate=P)
+    assert tg.lib().norm_residual_backward(ctypes.byref(p), None, 0, None) == INVALID
+    assert tg.lib().norm_residual(ctypes.byref(p), None) == INVALID
+    p.gate = P
+    assert tg.lib().norm_residual_backward(ctypes.byref(p), None, 0, None) != INVALID
+    p.dgate = None
+    assert tg.lib().norm_residual_backward(ctypes.byref(p), None, 0, None) == INVALID
+
+
 @pytest.mark.parametrize("gate_mode", [2, 3])
 def test_norm_backward_of_no_rows_needs_no_gate_gradient_per_row(gate_mode):
     """With T = 0 a per-token or per-element gate and its gradient are empty (NULL):

@@ -220,6 +220,18 @@ def test_no_rows_with_a_gate_per_row(tg, cols, post, pre):
     tg.check()
 
 
+def test_sums_over_no_rows_are_zero_whatever_the_weights(tg):
+    C = 264
+    w = torch.full((C,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    gate = torch.full((C,), float("inf"), dtype=torch.bfloat16, device="cuda")
+    e = torch.empty((0, C), dtype=torch.bfloat16, device="cuda")
+    n = torch.empty(0, device="cuda")
+    d = tg.norm_residual_backward(e, e, dh=e, dx=e, gate=gate, w_post=w, w_pre=w, rstd_post=n,
+                                  rstd_pre=n)
+    for t in (d.dgate, d.dw_post, d.dw_pre):
+        assert torch.all(t == 0)
+
+
 def test_gradients_repeat_their_bits(tg):
     dev, _ = make(2000, 1032, "f16", "channel", True, True)
     r = tg.norm_residual(**dev, save_rstd=True)

@@ -667,10 +667,10 @@ int gemm_fp8_impl(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64
 int norm_args(const tmagemm_norm* p, NormArgs* a) {
     if (!p || p->T < 0 || p->C <= 0 || p->gate_mode < 0 || p->gate_mode > 3)
         return TMAGEMM_ERR_INVALID;
-    // (With no rows the T x C operands may be NULL: nothing is read.)
-    if (p->T > 0 &&
-        (!p->h || (!p->y && (!p->w_pre || p->w_post || p->gate_mode != kGateNone)) ||
-         (p->gate_mode != kGateNone && !p->gate)))
+    // (With no rows the operands that have a row per token may be NULL: nothing is read.)
+    if (p->T > 0 && (!p->h || (!p->y && (!p->w_pre || p->w_post || p->gate_mode != kGateNone))))
+        return TMAGEMM_ERR_INVALID;
+    if (p->gate_mode != kGateNone && !p->gate && (p->T > 0 || p->gate_mode == kGateChannel))
         return TMAGEMM_ERR_INVALID;
     if (p->C > 16384 || p->T > (int64_t(1) << 31) - 1) return TMAGEMM_ERR_UNSUPPORTED;
     const void* aligned[] = {p->h, p->y, p->w_post, p->w_pre,

@@ -528,13 +528,15 @@ __global__ void __launch_bounds__(kColumnThreads) norm_columns_kernel(const Norm
         if (p.dw_pre) p.dw_pre[col - C] = v;
         return;
     }
-    const bool channel = p.gate_mode == kGateChannel;
+    const bool channel = p.gate_mode == kGateChannel && ctas > 0;   // (no rows: all sums are 0)
     if (p.dw_post)
         p.dw_post[col] =
             channel ? v * to_float<BF16>(static_cast<const uint16_t*>(p.gate)[col]) : v;
-    if (channel)
+    if (p.gate_mode == kGateChannel)
         static_cast<float*>(p.dgate)[col] =
-            p.w_post ? v * to_float<BF16>(reinterpret_cast<const uint16_t*>(p.w_post)[col]) : v;
+            channel && p.w_post
+                ? v * to_float<BF16>(reinterpret_cast<const uint16_t*>(p.w_post)[col])
+                : v;
 }
 
 // Threads of a CTA whose threads own V vectors of each row.
