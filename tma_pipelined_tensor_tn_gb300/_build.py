@@ -4,7 +4,8 @@ Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into a
 shared library with the CUDA runtime linked statically, so the library loads
 (and its symbols can be listed) on a machine without a GPU driver.  The binding
 of the 8-bit operators (``csrc/torch_ops.cpp``, host code against torch's
-headers) is compiled beside them into ``_torch_ops.so``.
+headers) is compiled beside them into ``_torch_ops.so``, where torch is there to
+compile it against; the library itself needs no torch.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import platform
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -77,23 +79,38 @@ def _ops_stamp() -> str:
 
 
 def _start_ops(force: bool):
-    """Starts compiling _torch_ops.so; None if it is up to date."""
+    """Starts compiling _torch_ops.so; None if it is up to date or there is no torch
+    to compile it against."""
+    try:
+        import torch  # noqa: F401
+    except (ImportError, OSError):
+        return None
     if not force and os.path.exists(OPS) and os.path.exists(OPS + ".stamp"):
         with open(OPS + ".stamp") as f:
             if f.read().strip() == _ops_stamp():
                 return None
     cmd = _ops_command(OPS + ".tmp")
-    return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    try:
+        return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except OSError as e:     # no such compiler
+        return cmd, str(e)
 
 
 def _finish_ops(started) -> None:
+    """Puts the compiled binding in place.  Where it does not compile, the library is
+    still good for C callers: that is a warning, and no older binding is left behind,
+    so that the 8-bit operators raise when they are called."""
     if started is None:
         return
     cmd, p = started
-    out, _ = p.communicate()
-    if p.returncode != 0:
-        raise RuntimeError("compiling the torch binding failed:\n" + " ".join(cmd) + "\n"
-                           + out.decode(errors="replace"))
+    out = p if isinstance(p, str) else p.communicate()[0].decode(errors="replace")
+    if isinstance(p, str) or p.returncode != 0:
+        for f in (OPS + ".stamp", OPS):
+            if os.path.exists(f):
+                os.remove(f)
+        warnings.warn("compiling the torch binding failed:\n" + " ".join(cmd) + "\n" + out,
+                      RuntimeWarning, stacklevel=3)
+        return
     os.replace(OPS + ".tmp", OPS)
     with open(OPS + ".stamp", "w") as f:
         f.write(_ops_stamp() + "\n")
@@ -127,8 +144,8 @@ def up_to_date(lib: str = LIB, flags=None) -> bool:
 def build(force: bool = False, verbose: bool = False, extra_flags=None,
           checked: bool = False) -> str:
     """Compile every CUDA source and link libtmagemm.so (or, with checked=True,
-    libtmagemm_checked.so), and the torch binding beside it; returns the
-    library's path."""
+    libtmagemm_checked.so), and the torch binding beside it where there is a torch;
+    returns the library's path."""
     ops = _start_ops(force)
     try:
         return _build_library(force, verbose, extra_flags, checked)
