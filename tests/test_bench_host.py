@@ -73,6 +73,15 @@ def test_traffic_capture_survives_comment_edits_not_code_edits():
     assert keys and all(k.split("@")[0] in bench.KERNEL_SOURCES for k in keys)
 
 
+def test_traffic_captures_are_those_of_the_current_kernels():
+    """A helper added to a header that a captured kernel's key covers made the bench
+    leave its DRAM traffic out: what only other kernels use belongs elsewhere."""
+    with open(os.path.join(os.path.dirname(bench.__file__), "profiles", "dram_traffic.json")) as f:
+        keys = json.load(f)
+    for key in keys:
+        assert bench.load_traffic(key) == keys[key]["bytes_per_launch"] > 0, key
+
+
 def test_max_over_ranks_two_gloo_ranks(tmp_path):
     mp = pytest.importorskip("torch.multiprocessing")
     port = _free_port()

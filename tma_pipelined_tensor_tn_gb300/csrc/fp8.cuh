@@ -14,6 +14,8 @@
 #include <cstdint>
 #include <cuda_fp8.h>
 
+#include "ptx.cuh"
+
 namespace tmagemm {
 
 constexpr int kFp8Block = 128;              // values per scale along K
@@ -120,6 +122,30 @@ __device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
     return m;
+}
+
+// wait_or_abort for many warps that wait often: a few tries of three
+// instructions each before the first look at the abort flag and the clock, so
+// that the waiting warps leave the issue slots to the working ones.
+__device__ __forceinline__ bool wait_many(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          uint32_t* err_word, uint32_t site, uint64_t limit_ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P, Q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 64;\n"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 P, [%1], %2;\n\t"
+        "@P bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 Q, n, 0;\n\t"
+        "@Q bra TRY;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    return wait_or_abort(bar, parity, abort_flag, err_word, site, limit_ns);
 }
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 operands and FP32 sums

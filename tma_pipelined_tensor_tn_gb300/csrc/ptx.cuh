@@ -174,30 +174,6 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity,
     }
 }
 
-// wait_or_abort for many warps that wait often: a few tries of three
-// instructions each before the first look at the abort flag and the clock, so
-// that the waiting warps leave the issue slots to the working ones.
-__device__ __forceinline__ bool wait_many(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          uint32_t* err_word, uint32_t site, uint64_t limit_ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred P, Q;\n\t.reg .u32 n;\n\t"
-        "mov.u32 n, 64;\n"
-        "TRY:\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 P, [%1], %2;\n\t"
-        "@P bra DONE;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 Q, n, 0;\n\t"
-        "@Q bra TRY;\n"
-        "DONE:\n\t"
-        "selp.u32 %0, 1, 0, P;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    return wait_or_abort(bar, parity, abort_flag, err_word, site, limit_ns);
-}
-
 // Same, but ignores the abort flag: used while draining in-flight copies
 // before the CTA exits.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint32_t* err_word,
