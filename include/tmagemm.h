@@ -531,6 +531,16 @@ int tmagemm_grouped_plan(int64_t G, const int64_t* m_offsets, int64_t N, int64_t
                          int64_t num_pairs, int64_t* out);
 
 /*
+ * How gemm_fp8 runs few rows on a device of num_sms SMs that holds resident[s]
+ * clusters of s CTAs of its kernel at once (s = 2 .. 8; entries 0 and 1 are not
+ * read): out[0] the tokens of a block, out[1] the tiles (blocks of tokens x 128
+ * weight rows), out[2] the slices of K, or zeros where it is the tile kernel's.
+ * A pure function of its arguments.
+ */
+int tmagemm_gemm_fp8_few_rows_plan(int64_t M, int64_t N, int64_t K, int64_t num_sms,
+                                   const int64_t* resident, int64_t* out);
+
+/*
  * Programmatic dependent launch of the library's kernels: 1 (the default)
  * launches each kernel with CUDA's programmatic-stream-serialization
  * attribute, so a kernel queued behind another on the same stream is

@@ -168,6 +168,34 @@ def test_binding_refuses_host_tensors():
         tg.norm_residual(x, x)
 
 
+# Clusters of 2, 3, .. 8 CTAs that a GB300 with 152 SMs was seen to hold: of the
+# kernels for up to 64 tokens, two CTAs an SM, and of the one for 128.
+HELD = (152, 97, 74, 58, 46, 38, 36)
+HELD_128 = (76, 46, 36, 28, 23, 15, 15)
+
+
+@pytest.mark.parametrize("M,N,K,tokens,tiles,slices", [
+    (3, 2360, 432, 16, 19, 1), (33, 14336, 1040, 64, 112, 2), (12, 9664, 1584, 16, 76, 3),
+    (60, 8200, 2064, 64, 65, 4), (5, 5088, 2656, 16, 40, 5), (17, 5632, 3088, 32, 44, 6),
+    (9, 4864, 4112, 16, 38, 7), (2, 520, 4304, 16, 5, 8),                 # the largest that fit
+    (1, 4864, 14336, 16, 38, 7), (1, 4992, 14336, 16, 39, 6), (12, 9728, 5632, 16, 76, 3),
+    (1, 4096, 14336, 16, 32, 8), (9, 520, 3600, 16, 5, 7),                # 29 k-blocks
+    (100, 14336, 272, 128, 112, 1), (128, 9000, 1040, 128, 71, 2), (65, 3400, 2064, 128, 27, 4),
+    (128, 2568, 3344, 128, 21, 6), (300, 640, 4112, 128, 15, 8), (129, 8192, 1024, 0, 0, 0)])
+def test_slices_of_few_rows(M, N, K, tokens, tiles, slices):
+    held = HELD_128 if M > 64 else HELD
+    assert tg.tmagemm_gemm_fp8_few_rows_plan(M, N, K, 152, held) == {
+        "tokens": tokens, "tiles": tiles, "slices": slices}
+
+
+def test_slices_of_few_rows_follow_the_device():
+    plan = tg.tmagemm_gemm_fp8_few_rows_plan
+    assert plan(1, 4864, 14336, 152, [0] * 7)["slices"] == 1
+    assert plan(1, 4864, 14336, 152, [100, 38, 37, 0, 0, 0, 0])["slices"] == 3
+    with pytest.raises(tg.TmaGemmError):
+        plan(0, 128, 128, 152, HELD)
+
+
 @pytest.mark.parametrize("source", ["few_rows_fp8.cu", "gemm_fp8.cu"])
 def test_aligned_barriers_follow_a_reconvergence(source):
     """barrier.cluster.*.aligned and bar.red need the lanes of a warp together: right

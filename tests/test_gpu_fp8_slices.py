@@ -72,3 +72,21 @@ def test_sliced_parity_and_bits(tg, M, N, K):
                                            (None, False, True)])
 def test_norm_column_sums(tg, T, C, gate, post, pre):
     norms.test_forward_and_gradients(tg, T, C, "bf16", gate, post, pre)
+
+
+# One to eight slices whatever the device holds of the larger clusters: few tiles, and
+# four to 32 k-blocks and some more.
+@pytest.mark.parametrize("M", [9, 40, 100])
+@pytest.mark.parametrize("K,slices", [(880, 1), (912, 2), (1104, 2), (1552, 3), (2320, 4), (2800, 5),
+                                      (3216, 6), (3600, 7), (4240, 8)])
+def test_every_slice_count(tg, M, K, slices):
+    N = 520
+    plan = tg.tmagemm_gemm_fp8_few_rows_plan(M, N, K, 152, [5] * 7)
+    assert (plan["tiles"], plan["slices"]) == (5, slices)
+    rng = np.random.default_rng(M + K)
+    a, sa = products.integer_operand(rng, M, K, True)
+    b, sb = products.integer_operand(rng, N, K, False)
+    want, _ = ref.gemm(a, sa, b, sb)
+    cuda = lambda s: torch.from_numpy(s).cuda()  # noqa: E731
+    got = tg.gemm_fp8(products.f8(a), cuda(sa), products.f8(b), cuda(sb), dtype=torch.float16)
+    assert np.array_equal(got.double().cpu().numpy(), products.rounded(want, torch.float16))

@@ -43,6 +43,7 @@ from ._binding import (  # noqa: F401
     options,
     strerror,
     tmagemm_check,
+    tmagemm_gemm_fp8_few_rows_plan,
     tmagemm_gemm_plan,
     tmagemm_gemm_tail_plan,
     tmagemm_last_error_detail,

@@ -95,6 +95,7 @@ SIGNATURES = {
     "tmagemm_set_group_m": ([_int], _int),
     "tmagemm_set_grouped_transposed": ([_int], _int),
     "tmagemm_grouped_plan": ([_i64, _P64, _i64, _i64, _i64, _P64], _int),
+    "tmagemm_gemm_fp8_few_rows_plan": ([_i64, _i64, _i64, _i64, _P64, _P64], _int),
     "tmagemm_host_pipeline_create": ([_i64, _i64, _i64, _int, _int, ctypes.POINTER(_p)], _int),
     "tmagemm_host_pipeline_run": ([_p, _i64, _p, _p, _p], _int),
     "tmagemm_host_pipeline_synchronize": ([_p], _int),
@@ -332,6 +333,16 @@ def tmagemm_grouped_plan(m_offsets, N, num_sms, num_pairs=0):
     if s != TMAGEMM_OK:
         raise TmaGemmError(s, "tmagemm_grouped_plan")
     return dict(zip(("transposed", "pair", "bn", "maxw"), list(out)))
+
+
+def tmagemm_gemm_fp8_few_rows_plan(M, N, K, num_sms, resident):
+    """`resident`: clusters of 2, 3, ... 8 CTAs that the device holds at once."""
+    held = (ctypes.c_int64 * 9)(0, 0, *[int(v) for v in resident])
+    out = (ctypes.c_int64 * 3)()
+    s = lib().tmagemm_gemm_fp8_few_rows_plan(M, N, K, num_sms, held, out)
+    if s != TMAGEMM_OK:
+        raise TmaGemmError(s, "tmagemm_gemm_fp8_few_rows_plan")
+    return dict(zip(("tokens", "tiles", "slices"), list(out)))
 
 
 def tmagemm_set_group_m(g) -> int:

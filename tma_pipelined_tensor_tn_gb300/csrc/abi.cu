@@ -925,6 +925,18 @@ int tmagemm_grouped_plan(int64_t G, const int64_t* m_offsets, int64_t N, int64_t
     return TMAGEMM_OK;
 }
 
+int tmagemm_gemm_fp8_few_rows_plan(int64_t M, int64_t N, int64_t K, int64_t num_sms,
+                                   const int64_t* resident, int64_t* out) {
+    if (!out || !resident || num_sms <= 0) return TMAGEMM_ERR_INVALID;
+    if (int s = validate_common(M, N, K)) return s;
+    out[0] = out[1] = out[2] = 0;
+    if (!few_rows_fp8(M, N, K, static_cast<int>(num_sms))) return TMAGEMM_OK;
+    out[0] = few_rows_tokens(M);
+    out[1] = ceil_div(M, out[0]) * ceil_div(N, 128);
+    out[2] = few_rows_slices(out[1], ceil_div(K, kFp8Block), resident);
+    return TMAGEMM_OK;
+}
+
 int tmagemm_set_pdl(int on) {
     if (on != 0 && on != 1) return TMAGEMM_ERR_INVALID;
     __atomic_store_n(&g_pdl, on, __ATOMIC_RELEASE);

@@ -31,6 +31,7 @@
 // at one token and 19.7 us at 16.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "launch.h"
@@ -381,22 +382,50 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
     if (prob.splits > 1) cluster_sync();
 }
 
-// K slices (CTAs of a cluster): the most with which all clusters are resident at
-// once and each CTA has four k-blocks (3 x 2360 x 432, four blocks: 3.0 us
-// undivided, 3.2 in two; 40 x 512 x 2048, sixteen: 4.2 us in four, 4.4 in five).
-// A cluster lies within a GPC, so clusters of more than two leave some slots empty:
-// kFill is the share, in percent, that clusters of each size fill.  12 x 9728 x 5632
-// (76 tiles): 11.7 us with 3 slices (228 CTAs), 15.1 with 4 (304); 1 x 4864 x 14336
-// (38): 13.0 with 7, 17.0 with 8; 5 x 5088 x 2656 (40): 5.6 with 6, 8.6 with 7;
-// 1 x 4096 x 14336 (32): 11.4 with 8, 12.1 with 6.
-int split_count(int64_t tiles, int32_t k_blocks, int sms, int per_sm) {
-    constexpr int kFill[2][9] = {{0, 100, 100, 90, 94, 92, 90, 69, 79},    // one CTA per SM
-                                 {0, 100, 100, 90, 94, 92, 90, 87, 92}};   // two
-    for (int splits = 8; splits > 1; --splits)
-        if (tiles * splits * 100 <= int64_t{sms} * per_sm * kFill[per_sm - 1][splits] &&
-            k_blocks >= 4 * splits)
-            return splits;
-    return 1;
+// Never launched: CTAs of the size of C's, to ask how many clusters fit the device.
+// (Of a kernel that allocates TMEM the occupancy query counts one CTA per SM, whatever
+// it allocates: 36 clusters of 4 for 16 tokens, where 74 are resident.)
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtasPerSm) few_rows_size_kernel() {}
+
+// Clusters of 2 to 8 CTAs of C's kernel that the current device holds at once, asked
+// once per context.  (A cluster lies within a GPC, whose SMs differ from device to
+// device.)  `into` has kMaxFewSlices + 1 entries; a size that cannot be asked for is 0.
+template <class C>
+void resident_clusters(int64_t* into) {
+    static ContextMarks known, attr_done;
+    static std::atomic<int> held[64][kMaxFewSlices + 1];
+    auto kernel = few_rows_size_kernel<C>;
+    int dev = 0;
+    const uint64_t ctx = current_context_id();
+    const bool tracked = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && ctx != 0;
+    const bool asked = tracked && known[dev].load(std::memory_order_acquire) == ctx;
+    for (int size = 2; size <= kMaxFewSlices; ++size) {
+        int n = 0;
+        if (asked) {
+            n = held[dev][size].load(std::memory_order_relaxed);
+        } else {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(size));
+            cfg.blockDim = dim3(C::kThreads);
+            cfg.dynamicSmemBytes = C::kSmemBytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (smem_opt_in(kernel, static_cast<int>(C::kSmemBytes), attr_done) != cudaSuccess ||
+                cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            if (tracked) held[dev][size].store(n, std::memory_order_relaxed);
+        }
+        into[size] = n;
+    }
+    if (tracked && !asked) known[dev].store(ctx, std::memory_order_release);
 }
 
 template <class C>
@@ -415,11 +444,13 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
     p.k_blocks = static_cast<int32_t>(ceil_div(g.K, C::BK));
     p.n_tiles = static_cast<int32_t>(ceil_div(g.N, C::BN));
     const int64_t tiles = p.n_tiles * ceil_div(g.M, C::NP);
-    p.splits = split_count(tiles, p.k_blocks, dev.sms, C::kCtasPerSm);
-    const int splits = p.splits;
     static ContextMarks attr_done;
     auto kernel = few_rows_fp8_kernel<C>;
     if (cudaError_t e = smem_opt_in(kernel, static_cast<int>(C::kSmemBytes), attr_done)) return e;
+    int64_t resident[kMaxFewSlices + 1];
+    resident_clusters<C>(resident);
+    p.splits = few_rows_slices(tiles, p.k_blocks, resident);
+    const int splits = p.splits;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles * splits)), dim3(C::kThreads),
                          C::kSmemBytes, stream, static_cast<unsigned>(splits), dev.pdl, p,
                          dev.limit_ns, dev.err_word);
@@ -427,10 +458,12 @@ cudaError_t launch_cfg(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stre
 
 template <bool T>
 cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {
-    if (g.M <= 16) return launch_cfg<FewCfg<16, 6, 4, 2, T>>(g, dev, stream);
-    if (g.M <= 32) return launch_cfg<FewCfg<32, 5, 4, 2, T>>(g, dev, stream);
-    if (g.M <= 64) return launch_cfg<FewCfg<64, 4, 4, 2, T>>(g, dev, stream);
-    return launch_cfg<FewCfg<128, 6, 8, 1, T>>(g, dev, stream);
+    switch (few_rows_tokens(g.M)) {
+        case 16: return launch_cfg<FewCfg<16, 6, 4, 2, T>>(g, dev, stream);
+        case 32: return launch_cfg<FewCfg<32, 5, 4, 2, T>>(g, dev, stream);
+        case 64: return launch_cfg<FewCfg<64, 4, 4, 2, T>>(g, dev, stream);
+        default: return launch_cfg<FewCfg<128, 6, 8, 1, T>>(g, dev, stream);
+    }
 }
 
 }  // namespace
@@ -441,6 +474,23 @@ cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t st
 // x 2048 7.5 against 8.0 and 256 x 4096 x 1536 6.8 against 6.8.
 bool few_rows_fp8(int64_t M, int64_t N, int64_t K, int sms) {
     return M <= 128 || (K >= 2048 && 2 * ceil_div(M, 128) * ceil_div(N, 128) <= sms);
+}
+
+// Tokens of a block.
+int few_rows_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+// K slices (CTAs of a cluster): the most with which all clusters are resident at
+// once and each CTA has four k-blocks (3 x 2360 x 432, four blocks: 3.0 us
+// undivided, 3.2 in two; 40 x 512 x 2048, sixteen: 4.2 us in four, 4.4 in five).
+// With clusters left over a second round begins: 12 x 9728 x 5632 (76 tiles, 74
+// clusters of four) takes 11.2 us in 3 slices and 15.1 in 4, 5 x 5088 x 2656 (40, 38
+// of seven) 5.5 in 6 and 8.6 in 7.  Where they just fit: 1 x 12160 x 8192 (95 tiles)
+// 17.2 us in 3 and 19.6 in 2, 1 x 4864 x 14336 (38) 12.9 in 7 and 13.0 in 6, and with
+// four or five k-blocks a slice 40 x 4608 x 4096 (36) 8.3 in 8 and 7.8 in 7.
+int few_rows_slices(int64_t tiles, int64_t k_blocks, const int64_t* resident) {
+    for (int slices = kMaxFewSlices; slices > 1; --slices)
+        if (tiles <= resident[slices] && k_blocks >= 4 * slices) return slices;
+    return 1;
 }
 
 cudaError_t launch_few_rows_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream) {

@@ -216,6 +216,11 @@ cudaError_t launch_gemm_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t
 // weights as the 128-row operand, K split over clusters.
 bool few_rows_fp8(int64_t M, int64_t N, int64_t K, int sms);
 cudaError_t launch_few_rows_fp8(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t stream);
+// Its blocks of tokens, and in how many slices it cuts K: `resident[s]` clusters of s
+// CTAs (2 to kMaxFewSlices) fit the device at once.
+constexpr int kMaxFewSlices = 8;
+int few_rows_tokens(int64_t M);
+int few_rows_slices(int64_t tiles, int64_t k_blocks, const int64_t* resident);
 
 // Map of an e4m3 operand {K, rows, mats} (mats 0: a single matrix, rank 2) in
 // boxes of 128 k x box_rows, 128-byte swizzle.  0, or -1 on failure.
