@@ -232,6 +232,23 @@ def test_sums_over_no_rows_are_zero_whatever_the_weights(tg):
         assert torch.all(t == 0)
 
 
+@pytest.mark.parametrize("T", [1, 2, 5])
+def test_gate_gradient_type_goes_by_the_gates_shape(tg, T):
+    """Whatever the number of tokens; (1, C) names a gate per element of one token."""
+    C = 264
+    dt = torch.bfloat16
+    h = torch.randn((T, C), device="cuda").to(dt)
+    for shape, kind in (((C,), torch.float32), ((T, 1), torch.float32), ((T, C), dt)):
+        d = tg.norm_residual_backward(h, h, dh=h, gate=torch.ones(shape, device="cuda", dtype=dt))
+        assert d.dgate.dtype == kind and d.dgate.shape == shape, shape
+    if T > 1:
+        row = torch.ones((1, C), device="cuda", dtype=dt)
+        for call in (lambda: tg.norm_residual(h, h, gate=row),
+                     lambda: tg.norm_residual_backward(h, h, dh=h, gate=row)):
+            with pytest.raises(ValueError, match="gate must be"):
+                call()
+
+
 def test_gradients_repeat_their_bits(tg):
     dev, _ = make(2000, 1032, "f16", "channel", True, True)
     r = tg.norm_residual(**dev, save_rstd=True)

@@ -186,16 +186,17 @@ tmagemm_norm norm_operands(const Tensor& h, const MaybeTensor& y, const MaybeTen
     if (w_post) check("w_post", *w_post, type, {C}, device);
     if (w_pre) check("w_pre", *w_pre, type, {C}, device);
     if (gate) {
+        // (A per-channel gate has one dimension: as (1, C) it would be per element, with
+        // a gradient of another type, for one token.)
         const at::IntArrayRef shape = gate->sizes();
         if (shape == at::IntArrayRef({T, C}))
             p.gate_mode = kElement;
-        else if (shape == at::IntArrayRef({C}) || shape == at::IntArrayRef({1, C}))
+        else if (shape == at::IntArrayRef({C}))
             p.gate_mode = kChannel;
         else if (shape == at::IntArrayRef({T, 1}))
             p.gate_mode = kToken;
         else
-            throw py::value_error("gate must be (C,), (1, C), (T, 1) or (T, C), got " +
-                                  text(shape));
+            throw py::value_error("gate must be (C,), (T, 1) or (T, C), got " + text(shape));
         check("gate", *gate, type, shape, device);
     }
     p.h = h.data_ptr();

@@ -142,7 +142,8 @@ def norm_residual(h, y=None, gate=None, w_post=None, w_pre=None, alpha: float = 
         h' = h + alpha * gate * u                   (h' = h without y)
         x  = h' * rsqrt(mean(h'^2) + eps) * w_pre   (no x without w_pre)
 
-    h and y are (T, C) fp16 or bf16; gate is (C,), (T, 1), (T, C) or None.
+    h and y are (T, C) fp16 or bf16; gate is (C,), (T, 1), (T, C) or None.  (A gate
+    per channel has one dimension: (1, C) is a gate per element of one token.)
     ``quantize`` makes x float8_e4m3fn codes with row scales, the operands of
     gemm_fp8; ``save_rstd`` keeps the two rsqrt factors for the backward.
     """
