@@ -41,6 +41,7 @@ class Block:
         self.up = weight(experts, 2 * hidden, channels, fan_in=channels).bfloat16()
         self.down = weight(experts, channels, hidden, fan_in=hidden).bfloat16()
         self.head = weight(vocab, channels, fan_in=channels).bfloat16()
+        self.first = torch.arange(experts + 1, device="cuda")
         # Whole matrices of experts share the 128-row blocks when their rows are
         # a multiple of 128; each is quantised by itself to allow any size.
         self.up_q, self.up_s = self._stack(self.up)
@@ -58,9 +59,8 @@ class Block:
         their weights, and the experts' row offsets (int32, on the device)."""
         p, expert = torch.topk(torch.softmax((x @ self.router.t()).float(), dim=1), top)
         expert, order = torch.sort(expert.flatten(), stable=True)
-        counts = torch.bincount(expert, minlength=self.router.shape[0])
-        offsets = torch.zeros(len(counts) + 1, device="cuda", dtype=torch.int32)
-        offsets[1:] = torch.cumsum(counts, 0)
+        # First row of each expert (torch.bincount would wait for the device).
+        offsets = torch.searchsorted(expert, self.first, out_int32=True)
         return order // top, (p / p.sum(1, keepdim=True)).flatten()[order], offsets
 
     def __call__(self, h, top):
