@@ -308,3 +308,85 @@ def test_other_stream_than_the_current(tg):
         torch.empty((300, 1032), device="cuda", dtype=torch.bfloat16).fill_(9.0)
         side.synchronize()
         assert torch.equal(r.x, want.x) and all(torch.equal(a, b) for a, b in zip(d, grads))
+
+
+@pytest.mark.parametrize("T,C", [(1, 264), (300, 1032)])
+@pytest.mark.parametrize("gate,post,pre", [(None, True, False), ("token", True, False),
+                                           ("channel", True, True), ("element", False, True)])
+def test_gradients_without_one_of_the_residual_stream(tg, T, C, gate, post, pre):
+    """No dh (the residual stream ends here): with w_pre the gradients are those of x
+    alone, without it they are all zero."""
+    dev, v = make(T, C, "bf16", gate, post, pre)
+    r = tg.norm_residual(**dev, alpha=0.7, eps=EPS, save_rstd=True)
+    g = torch.Generator().manual_seed(T)
+    dx = torch.randn((T, C), generator=g).to(torch.bfloat16) if pre else None
+    hx = dx.double().numpy() if pre else None
+    d = tg.norm_residual_backward(**dev, dx=dx.cuda() if pre else None, alpha=0.7,
+                                  rstd_post=r.rstd_post, rstd_pre=r.rstd_pre)
+    if not pre:
+        assert all(t is None or torch.all(t == 0) for t in d)
+        return
+    _, s = sizes(v, 0.7, None, hx)
+    want = ref.norm_backward(v["h"], None, hx, **{k: v[k] for k in v if k != "h"}, alpha=0.7, eps=EPS)
+    near(d.dh, want["dh"], s["dh"], "bf16", "dh")
+    near(d.dy, want["dy"], s["dy"], "bf16", "dy")
+    near(d.dw_pre, want["dw_pre"], s["dw_pre"], "f32", "dw_pre")
+    if post:
+        near(d.dw_post, want["dw_post"], s["dw_post"], "f32", "dw_post")
+    near(d.dgate, want["dgate"], s["dgate"][gate[0]], "bf16" if gate == "element" else "f32", "dgate")
+
+
+def test_graph_follows_its_inputs(tg):
+    """A captured forward and backward replayed on other inputs give what calls give."""
+    dev, _ = make(300, 1032, "bf16", "channel", True, True)
+    dh = torch.randn((300, 1032), device="cuda").bfloat16()
+
+    def step():
+        r = tg.norm_residual(**dev, save_rstd=True)
+        q = tg.norm_residual(**dev, quantize=True)
+        d = tg.norm_residual_backward(**dev, dh=dh, dx=dh, rstd_post=r.rstd_post,
+                                      rstd_pre=r.rstd_pre)
+        return [r.h, r.x, q.x.view(torch.uint8), q.scales, *d]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(3):
+        for t in (dev["h"], dev["y"], dev["gate"], dh):
+            t.copy_(torch.randn_like(t))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, step()))
+
+
+def test_gradients_past_32_bit_offsets(tg):
+    """Six operands of 2.3e9 values; only a few rows, some past 2^31 values, are not zero,
+    so the column sums are those rows' sums."""
+    T, C = 140000, 16384
+    rows = [0, 65536, 131072, T - 1]
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def sparse():
+        t = torch.zeros((T, C), device="cuda", dtype=torch.bfloat16)
+        for r in rows:
+            t[r] = torch.randn(C, device="cuda", generator=g).bfloat16()
+        return t
+
+    h, y, dh, dx = (sparse() for _ in range(4))
+    w = torch.randn((2, C), device="cuda", generator=g).bfloat16()
+    r = tg.norm_residual(h, y, w_post=w[0], w_pre=w[1], eps=EPS, save_rstd=True)
+    d = tg.norm_residual_backward(h, y, dh=dh, dx=dx, w_post=w[0], w_pre=w[1],
+                                  rstd_post=r.rstd_post, rstd_pre=r.rstd_pre)
+    host = lambda t: t[rows].double().cpu().numpy()  # noqa: E731
+    v = {"h": host(h), "y": host(y), "gate": None, "w_post": w[0].double().cpu().numpy(),
+         "w_pre": w[1].double().cpu().numpy()}
+    _, s = sizes(v, 1.0, host(dh), host(dx))
+    want = ref.norm_backward(v["h"], host(dh), host(dx), y=v["y"], w_post=v["w_post"],
+                             w_pre=v["w_pre"], eps=EPS)
+    near(d.dh[rows], want["dh"], s["dh"], "bf16", "dh")
+    near(d.dy[rows], want["dy"], s["dy"], "bf16", "dy")
+    near(d.dw_post, want["dw_post"], s["dw_post"], "f32", "dw_post")
+    near(d.dw_pre, want["dw_pre"], s["dw_pre"], "f32", "dw_pre")
+    assert not d.dh[1:65536].any() and not d.dy[131073:T - 1].any()
