@@ -193,8 +193,11 @@ few_rows_fp8_kernel(const __grid_constant__ FewProblem prob, const uint64_t limi
         uint32_t s = 0, phase = 0, it = 0;
         for (int32_t kb = kb0; kb < kb1; ++kb, ++it) {
             if (!__all_sync(0xffffffffu, wait_many(empty_bar(s), phase ^ 1u, abort_flag, err,
-                                                   kSiteProducerEmpty, limit_ns)))
+                                                   kSiteProducerEmpty, limit_ns)) ||
+                !check_ok(n0 >= 0 && n0 < prob.N && m0 >= 0 && m0 < prob.M, err, kSiteCheckTma)) {
+                *abort_flag = 1;
                 break;
+            }
             if (lead) {
                 mbar_arrive_expect_tx(full_bar(s), C::kStageBytes);
                 const uint32_t w = sbase + s * C::kStageBytes;
