@@ -11,8 +11,8 @@
 // and a column a token, so a block's scale varies along the columns: the epilogue
 // threads keep SA[token] * SB (the tile's 128 weight rows share one SB per block) of
 // four blocks in shared memory, read as broadcasts.  Otherwise a lane is a token
-// and its scale one register (100 x 14336 x 4096 15.1 us, swapped 16.4: the
-// broadcast reads of 128 columns took longer than their MMAs).
+// and its scale one register (100 x 14336 x 4096, each call by itself: 15.1 us,
+// swapped 16.4: the broadcast reads of 128 columns took longer than their MMAs).
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer, then four scaling warps (eight
 // for 128 tokens, half of the columns each).  The CTAs of a cluster leave their
@@ -23,10 +23,11 @@
 // Up to 64 tokens two CTAs share an SM (half the ring and at most 256 TMEM
 // columns each): while one sets up or reduces, the other streams.
 //
-// Measured on GB300 (device time, weights colder than L2): 1 x 4096 x 14336
-// 11.4 us (5.1 TB/s of weights), 32 x 14336 x 4096 12.3 us, 12 x 9664 x 5584
-// 12.5 us; 100 x 14336 x 4096, 112 tiles undivided, 15.1 us (two CTAs an SM, with
-// half the accumulators and registers each: 22.3).  A kernel that streamed the
+// Measured on GB300 (calls in a graph, weights colder than L2): 1 x 4096 x 14336
+// 11.2 us (5.2 TB/s of weights), 32 x 14336 x 4096 12.1 us, 12 x 9664 x 5584
+// 11.9 us; 100 x 14336 x 4096, 112 tiles undivided, 12.8 us (each call by itself
+// 15.1, and with two CTAs an SM, half the accumulators and registers each, 22.3).
+// There 40 of 152 SMs have no tile, and a CTA takes in 0.9 MB.  A kernel that streamed the
 // weights into mma.sync fragments, as the 16-bit few-row kernel does, took 12.6 us
 // at one token and 19.7 us at 16.
 #include <cuda.h>
@@ -472,9 +473,10 @@ cudaError_t launch_typed(const Fp8Gemm& g, const Fp8Device& dev, cudaStream_t st
 }  // namespace
 
 // One block of tokens, or more where the 128 x 128 tiles leave room to split a
-// long enough K: 256 x 4096 x 4096 (64 tiles) 10.1 us against 12.2 us for the tile
-// kernel and 512 x 4096 x 4096 (128 tiles, no split) 12.7 against 12.5; 256 x 4096
-// x 2048 7.5 against 8.0 and 256 x 4096 x 1536 6.8 against 6.8.
+// long enough K: 256 x 4096 x 4096 (64 tiles) 10.1 us (9.1 in a graph of calls)
+// against 12.2 us for the tile kernel and 512 x 4096 x 4096 (128 tiles, no split)
+// 12.7 against 12.5; 256 x 4096 x 2048 7.5 against 8.0 and 256 x 4096 x 1536 6.8
+// against 6.8.
 bool few_rows_fp8(int64_t M, int64_t N, int64_t K, int sms) {
     return M <= 128 || (K >= 2048 && 2 * ceil_div(M, 128) * ceil_div(N, 128) <= sms);
 }

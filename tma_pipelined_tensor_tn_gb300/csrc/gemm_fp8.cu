@@ -21,14 +21,16 @@
 //               tile's columns.  Their FP32 sums (128 per thread for 256
 //               columns) take the registers that warps 0..3 (3, and 2 for one
 //               part, idle) give up.
-// What bounds it.  Per k-block of a pair's 256 x 256 tile each SM has 256 cycles
-// of MMAs, 256 of TMEM reads (128 lanes x 256 columns, at 32 lanes x 4 bytes per
-// cycle and quarter) and 128 packed multiply-adds in each of the two warps of a
-// scheduler (256 cycles, more or less under the reads), and takes in 32 KB of
-// operands.  8192^3 runs in 368 to 376 us (2.9 to 3.0 PFLOP/s, 0.41 us per
-// k-block): without the multiply-adds the same kernel takes 306 us, without the
-// operand loads 343 and without both 261, and with sums left to the tensor cores
-// over all of K (no scales) 306.  All SMs together take in about 13.4 TB/s through
+// What bounds it.  Per k-block of a pair's 256 x 256 tile each SM has 512 cycles
+// of MMAs (128 x 256 x 128 at 8192 multiply-adds a cycle: 0.25 us), 256 of TMEM
+// reads (128 lanes x 256 columns, at 32 lanes x 4 bytes per cycle and quarter) and
+// 64 packed multiply-adds in each of the two warps of a scheduler (256 cycles of
+// its FP32 lanes, more or less under the reads), and takes in 32 KB of operands.
+// A single call of 8192^3 takes 368 to 376 us (2.9 to 3.0 PFLOP/s, 0.41 us per
+// k-block; 415 to 424 back to back, at the power limit's clock): without the
+// multiply-adds the same kernel takes 306 us, without the operand loads 343 and
+// without both 261, and with sums left to the tensor cores over all of K (no
+// scales) 306.  All SMs together take in about 13.4 TB/s through
 // TMA (128 x 128 tiles: 0.36 us per k-block of 32 KB on 152 SMs, 0.25 on 32),
 // which bounds those tiles and makes 0.36 us per k-block the pair tile's bound
 // too; the multiply-adds are not quite hidden under it.

@@ -14,7 +14,10 @@
 // sums need a barrier.  The per-channel weights and gate lie in shared memory
 // too (in registers they made the compiler spill, and a spilled value's load
 // waits behind the row copies in flight: the backward at 4096 x 8192 took 95
-// us, and takes 69).  Vectors past the last channel are zeros, so that a
+// us, and takes 67).  Beyond 8192 channels the backward spills all the same (64 to
+// 304 bytes a thread: 1024 threads have 64 registers each, 32 of them column sums),
+// and shared memory holds one row, so that copies do not run ahead: 4096 x 12288
+// 172 us and 4096 x 16384 228 us (3.5 TB/s).  Vectors past the last channel are zeros, so that a
 // thread's vectors are worked on together, without branches between them.
 // Arithmetic is on packed pairs, half the instructions of scalar FP32.
 //
@@ -22,8 +25,8 @@
 // forward 8192 x 4096 with a (T, C) gate 53 us (6.3 TB/s), 4096 x 8192 into
 // codes 41 us (5.7 TB/s); backward 8192 x 4096 with both weights 68 us without a
 // gate (5.9 TB/s) and 100 us with a (T, C) gate (5.3 TB/s, where a kernel that
-// only copies the same five operands to three takes 91); one row of 4096
-// channels 3 us.
+// only copies the same five operands to three takes 91); 4096 x 16384 forward with
+// both weights 85 us (6.3 TB/s), into codes 99; one row of 4096 channels 2.7 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

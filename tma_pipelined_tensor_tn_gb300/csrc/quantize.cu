@@ -4,9 +4,11 @@
 //
 // Bound by memory: each value is read once (2 bytes) and written once (1
 // byte); a block's values stay in registers between the maximum and the
-// rounding.  Measured on GB300 (device time, cold): rows of 8192 x 14336 57.5 us
-// (6.2 TB/s), 128 x 128 blocks of 4100 x 4096 9.8 us (5.2 TB/s), one row of 4096
-// values 1.3 us.
+// rounding, but for what four CTAs an SM leave no room for (64 registers a thread:
+// 68 bytes spilled of an fp16 128 x 128 block, 12 of a tile of rows).  Measured on
+// GB300 (device time, cold): rows of 8192 x 14336 57.8 us (6.1 TB/s), 128 x 128
+// blocks of 4100 x 4096 9.6 us in fp16 (5.2 TB/s) and 9.3 in bf16, one row of 4096
+// values 1.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -111,7 +113,7 @@ quantize_rows_kernel(const uint4* X, uint2* Q, float* S, int32_t M, int32_t K8, 
 }
 
 // One scale per 128 x 128 values: one CTA per block, 16 rows at a time, the
-// whole block (8 x 16 bytes per thread) in registers.
+// whole block (8 x 16 bytes per thread) held between the two passes.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 4)
 quantize_tiles_kernel(const uint4* X, uint2* Q, float* S, int32_t M, int32_t K8, int64_t s_row,

@@ -6,6 +6,10 @@ allocated, and the C ABI called.  8-bit matrices are ``torch.float8_e4m3fn``
 with float32 scales, one per 128 values along K: per row for activations, per
 128 x 128 values for weights.
 
+No call is recorded by autograd: what it makes never requires gradients, whatever the
+inputs do.  The norms' gradients come from norm_residual_backward, for an
+autograd.Function of the caller's own; the products and the quantiser have none.
+
 Results are allocated on the stream the call runs on.  With an explicit
 ``stream`` that is not the current one, the inputs are recorded on it, so that
 the caching allocator does not hand their memory out again too early; ordering
