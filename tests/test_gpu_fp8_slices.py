@@ -90,3 +90,30 @@ def test_every_slice_count(tg, M, K, slices):
     cuda = lambda s: torch.from_numpy(s).cuda()  # noqa: E731
     got = tg.gemm_fp8(products.f8(a), cuda(sa), products.f8(b), cuda(sb), dtype=torch.float16)
     assert np.array_equal(got.double().cpu().numpy(), products.rounded(want, torch.float16))
+
+
+def test_first_call_inside_a_capture(tg):
+    """What is asked of the device once (how many clusters it holds) may be asked while
+    a graph is captured, in a process that has not called the product before."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+import tma_pipelined_tensor_tn_gb300 as tg
+A = torch.full((9, 528), 0x38, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+B = torch.full((264, 528), 0x38, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+SA, SB = torch.ones((9, 5), device="cuda"), torch.ones((3, 5), device="cuda")
+out = torch.zeros((9, 264), device="cuda", dtype=torch.float16)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    tg.gemm_fp8(A, SA, B, SB, out=out)
+graph.replay()
+tg.check()
+assert torch.all(out == 528)     # 0x38 is 1
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300, env=dict(os.environ, PYTHONPATH=root))
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
