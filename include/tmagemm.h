@@ -1,6 +1,7 @@
 /*
  * tmagemm — FP16 and BF16 "TN" GEMM D = A * B^T and M = 1 GEMV for sm_103a
- * (GB300), block-scaled 8-bit linear layers, and the norms between them.
+ * (GB300), block-scaled 8-bit linear layers and the norms between them, linear
+ * layers with 4-bit weights, and what stands around routed experts.
  *
  * C ABI of libtmagemm.so.  Plain pointers and sizes only.  Matrices are dense
  * row-major with no padding between rows: binary16 (IEEE fp16) for gemm_f16
@@ -406,6 +407,135 @@ int norm_residual(const tmagemm_norm* p, void* stream);
 int norm_residual_backward(const tmagemm_norm* p, void* workspace, int64_t workspace_bytes,
                            void* stream);
 int64_t norm_residual_backward_workspace_size(int64_t T, int64_t C);
+
+/*
+ * ---- Routed experts: the router's choice, rows by expert, and their sum ----
+ *
+ * What stands before and after gemm_fp8_grouped and gemm_w4_grouped: a router's
+ * logits -> experts and weights (route_topk), tokens -> rows sorted by expert
+ * with their offsets (dispatch_rows), rows -> tokens (combine_rows), and the
+ * gradients.  Choice j of token t is slot t * k + j.  Nothing is copied to the
+ * host.  The pages have no counterpart of these entry points.
+ */
+
+/*
+ * k experts for each of T tokens out of E logits.  With p = softmax(logits) or
+ * sigmoid(logits) and v = p + bias:
+ *   ids     : the k experts of largest v, largest first, ties to the lowest index.
+ *             groups > 1: the E experts are `groups` runs of E / groups; a group's
+ *             value is the sum of its group_sum (1 or 2) largest v, and only the
+ *             top_groups groups of largest value (ties to the lowest) are chosen from.
+ *   weights : scale * p of the chosen (without the bias), divided by the sum of the
+ *             token's chosen p when renormalize != 0.
+ * The order is that of exact arithmetic: values that FP32 cannot tell apart are
+ * compared in FP64.  A logit of minus infinity closes an expert to its token: it is
+ * never chosen, whatever its bias, and choices that no expert is left for get id -1
+ * and weight 0.  NaN ranks above every number and shows in the weights.
+ *   type    : of the logits, 0 fp16, 1 bf16, 2 FP32.
+ *   score   : 0 softmax, 1 sigmoid.
+ *   bias    : E floats, or NULL for none.
+ * The backward takes logits, ids, dweights (the gradient of the weights), score,
+ * renormalize and scale, and writes dlogits (T x E, in the logits' type) with the
+ * choice held fixed; bias and groups are not read.  ids outside 0 .. E - 1 have no
+ * gradient; a token's ids are different experts, as route_topk makes them.
+ * Zero the struct before filling it.  Requirements: 1 <= E <= 512, 1 <= k <= 32,
+ * k <= E / groups * top_groups, groups a divisor of E and at most 32, T * k < 2^31;
+ * pointers aligned to their elements.  T = 0 is OK and writes nothing.
+ */
+typedef struct tmagemm_route {
+    int64_t T, E;
+    int32_t k, type, score, groups, top_groups, group_sum, renormalize;
+    float scale;
+    const void* logits;
+    const float* bias;
+    int32_t* ids;      /* T x k: written by the forward, read by the backward */
+    float* weights;    /* T x k */
+    const float* dweights;
+    void* dlogits;
+} tmagemm_route;
+
+int route_topk(const tmagemm_route* p, void* stream);
+int route_topk_backward(const tmagemm_route* p, void* stream);
+
+/*
+ * Rows of x by expert: slot t * k + j, whose expert is ids[t][j], gets a row with
+ * x[t] in it.  Rows are in the order of their experts, those of one expert in the
+ * order of their slots.
+ *   ids     : T x k int32; slots whose id is not in 0 .. E - 1 get no row (padding,
+ *             or a choice route_topk left empty).
+ *   x       : T x C fp16 (bf16 when bf16 != 0), row-major.
+ *   rows    : T k x C: x itself (scales NULL), or e4m3 codes with one scale per
+ *             row and 128 columns as quantize_fp8 makes them (scales and their two
+ *             strides as there).  Rows past the last slot's are left as they are.
+ *   offsets : E + 1 int32, the first row of each expert and the number of rows:
+ *             the m_offsets of the grouped products.
+ *   row_of  : T x k int32, the row of each slot, -1 without one.
+ *   workspace : scratch of at least dispatch_rows_workspace_size(T, k, E) bytes,
+ *             16-byte aligned (NULL where that is 0), not shared by calls that
+ *             overlap on the GPU.
+ * The gradient of x is combine_rows of the rows' gradient, without weights.
+ * Requirements: 1 <= E <= 512, 1 <= k <= 32, C % 8 == 0, C <= 2^20,
+ * T * k < 2^31; x, rows 16-byte, scales, ids, offsets, row_of 4-byte aligned.  T = 0
+ * is OK and writes the offsets only.  Up to three kernels; deterministic.
+ */
+int dispatch_rows(int64_t T, int64_t k, int64_t E, int64_t C, const int32_t* ids, const void* x,
+                  int bf16, void* rows, float* scales, int64_t s_row_stride,
+                  int64_t s_block_stride, int32_t* offsets, int32_t* row_of, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+int64_t dispatch_rows_workspace_size(int64_t T, int64_t k, int64_t E);
+
+/*
+ * y[t] = sum_j weights[t][j] rows[row_of[t][j]], in FP32 in the order of j, rounded
+ * once to fp16 (bf16 when bf16 != 0).
+ *   rows    : R x C; row_of outside 0 .. R - 1 adds nothing (and is not read).
+ *   weights : T x k floats, or NULL for ones.
+ * Requirements: 1 <= k <= 32, C % 8 == 0, C <= 2^20, T * k and R < 2^31; rows, y
+ * 16-byte, row_of, weights 4-byte aligned.  T = 0 is OK and writes nothing.
+ */
+int combine_rows(int64_t T, int64_t k, int64_t C, int64_t R, const void* rows,
+                 const int32_t* row_of, const float* weights, void* y, int bf16, void* stream);
+
+/*
+ * Gradients of combine_rows from dy (T x C): drows[row_of[t][j]] = weights[t][j]
+ * dy[t], rounded once, and dweights[t][j] = sum over columns of dy[t] times that row,
+ * in FP32 (0 for slots without a row).  Rows of no slot are left as they are in drows;
+ * no row may have two slots.  Requirements as combine_rows (drows, dy 16-byte, dweights
+ * 4-byte aligned); deterministic.
+ */
+int combine_rows_backward(int64_t T, int64_t k, int64_t C, int64_t R, const void* dy,
+                          const void* rows, const int32_t* row_of, const float* weights,
+                          void* drows, float* dweights, int bf16, void* stream);
+
+/*
+ * ---- Linear layers with 4-bit weights ----
+ *
+ * D[m][n] = sum_k A[m][k] (q[n][k] - z[n][g]) s[n][g] with g = k / group: products of
+ * a few tokens with weights of four bits, summed in FP32 (the scales applied to the
+ * sums of whole groups) and rounded once.  Meant for decoding, where reading the
+ * weights is what takes the time; any M works.
+ *   A     : device pointer, M x K fp16 (bf16 when bf16 != 0), row-major.
+ *   B     : device pointer, N x K / 2 bytes, row-major: codes q of 0 .. 15, column 2 i
+ *           in the low half of byte i and column 2 i + 1 in the high half.
+ *   SB    : device pointer, N x ceil(K / group) scales in the type of A, row-major.
+ *   ZB    : device pointer, N x ceil(K / group) bytes, the zero points (0 .. 15), or
+ *           NULL: 8 everywhere.
+ *   D     : device pointer, M x N in the type of A; written, never read.
+ *   group : 32, 64 or 128.
+ * Requirements: A, B 16-byte, SB, D 2-byte aligned; K % 32 == 0.  M = 0 is OK and
+ * writes nothing.  Deterministic.  Status codes as gemm_f16.
+ */
+int gemm_w4(int64_t M, int64_t N, int64_t K, int64_t group, const void* A, const void* B,
+            const void* SB, const void* ZB, void* D, int bf16, void* stream);
+
+/*
+ * G such products that share N, K and group, with the row offsets in DEVICE memory:
+ * the rows [m_offsets[g], m_offsets[g + 1]) of A and D with B[g], SB[g] and ZB[g].
+ * G, m_offsets and rows outside every group as for gemm_fp8_grouped; other arguments
+ * as gemm_w4.
+ */
+int gemm_w4_grouped(int64_t G, const int32_t* m_offsets, int64_t M, int64_t N, int64_t K,
+                    int64_t group, const void* A, const void* B, const void* SB, const void* ZB,
+                    void* D, int bf16, void* stream);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's sticky

@@ -1,5 +1,6 @@
-"""FP16/BF16 TN GEMM (D = A @ B.T), M=1 GEMV and block-scaled 8-bit linear layers
-with the norms between them, for GB300 (sm_103a).
+"""FP16/BF16 TN GEMM (D = A @ B.T), M=1 GEMV, block-scaled 8-bit linear layers with the
+norms between them, linear layers with 4-bit weights, and what stands around routed
+experts, for GB300 (sm_103a).
 
 The compute path is the CUDA library ``libtmagemm.so`` built from ``csrc/``;
 this package only marshals arguments to its C ABI (``include/tmagemm.h``).
@@ -21,6 +22,7 @@ from ._binding import (  # noqa: F401
     TmaGemmError,
     TmagemmNorm,
     TmagemmOptions,
+    TmagemmRoute,
     check,
     gemm,
     gemm_bf16,
@@ -70,6 +72,17 @@ from .fp8 import (  # noqa: F401
     norm_residual_backward,
     quantize_fp8,
 )
+from .experts import (  # noqa: F401
+    CombineGrads,
+    DispatchOut,
+    RouteOut,
+    combine_rows,
+    combine_rows_backward,
+    dispatch_rows,
+    route_topk,
+    route_topk_backward,
+)
+from .w4 import gemm_w4, gemm_w4_grouped  # noqa: F401
 
 
 def build(force: bool = False) -> str:

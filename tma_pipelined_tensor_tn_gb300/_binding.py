@@ -50,11 +50,23 @@ class TmagemmNorm(ctypes.Structure):
                     "dh_out", "dx", "dh", "dy", "dgate", "dw_post", "dw_pre")])
 
 
+class TmagemmRoute(ctypes.Structure):
+    """struct tmagemm_route: the operands and results of route_topk and
+    route_topk_backward."""
+    _fields_ = ([(name, ctypes.c_int64) for name in ("T", "E")]
+                + [(name, ctypes.c_int32) for name in (
+                    "k", "type", "score", "groups", "top_groups", "group_sum", "renormalize")]
+                + [("scale", ctypes.c_float)]
+                + [(name, ctypes.c_void_p) for name in (
+                    "logits", "bias", "ids", "weights", "dweights", "dlogits")])
+
+
 # Every symbol include/tmagemm.h declares, with (argtypes, restype).
 _i64, _p, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 _P64 = ctypes.POINTER(ctypes.c_int64)
 _POPT = ctypes.POINTER(TmagemmOptions)
 _PNORM = ctypes.POINTER(TmagemmNorm)
+_PROUTE = ctypes.POINTER(TmagemmRoute)
 SIGNATURES = {
     "gemm_f16": ([_i64, _i64, _i64, _p, _p, _p, _p], _int),
     "gemm_f16_ex": ([_i64, _i64, _i64, _p, _p, _p, _POPT, _p], _int),
@@ -76,6 +88,15 @@ SIGNATURES = {
     "norm_residual": ([_PNORM, _p], _int),
     "norm_residual_backward": ([_PNORM, _p, _i64, _p], _int),
     "norm_residual_backward_workspace_size": ([_i64, _i64], _i64),
+    "route_topk": ([_PROUTE, _p], _int),
+    "route_topk_backward": ([_PROUTE, _p], _int),
+    "dispatch_rows": ([_i64, _i64, _i64, _i64, _p, _p, _int, _p, _p, _i64, _i64, _p, _p, _p, _i64,
+                       _p], _int),
+    "dispatch_rows_workspace_size": ([_i64, _i64, _i64], _i64),
+    "combine_rows": ([_i64, _i64, _i64, _i64, _p, _p, _p, _p, _int, _p], _int),
+    "combine_rows_backward": ([_i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _int, _p], _int),
+    "gemm_w4": ([_i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _int, _p], _int),
+    "gemm_w4_grouped": ([_i64, _p, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _int, _p], _int),
     "tmagemm_check": ([_p], _int),
     "tmagemm_last_error_detail": ([], _int),
     "tmagemm_checked_unit_counts": ([ctypes.POINTER(ctypes.c_uint32), _i64, _p], _int),

@@ -805,6 +805,229 @@ int norm_residual_backward(const tmagemm_norm* p, void* workspace, int64_t works
 
 }  // extern "C"
 
+namespace {
+
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+constexpr int64_t kMax32 = (int64_t(1) << 31) - 1;
+
+// The checks route_topk and its backward share, and the kernels' arguments.
+int route_args(const tmagemm_route* p, RouteArgs* a) {
+    if (!p || p->T < 0 || p->E <= 0 || p->k <= 0 || p->k > p->E || p->type < 0 || p->type > 2 ||
+        p->score < 0 || p->score > 1 || (p->T > 0 && !p->logits))
+        return TMAGEMM_ERR_INVALID;
+    if (p->E > kMaxExperts || p->k > kMaxChoices || p->T > kMax32 / p->k)
+        return TMAGEMM_ERR_UNSUPPORTED;
+    if (p->type == kLogitsF32 ? !aligned4(p->logits) : !aligned2(p->logits))
+        return TMAGEMM_ERR_ALIGN;
+    if (!aligned4(p->ids)) return TMAGEMM_ERR_ALIGN;
+    *a = RouteArgs{};
+    a->T = p->T;
+    a->E = static_cast<int32_t>(p->E);
+    a->k = p->k;
+    a->score = p->score;
+    a->renormalize = p->renormalize != 0;
+    a->scale = p->scale;
+    a->logits = p->logits;
+    a->ids = p->ids;
+    return TMAGEMM_OK;
+}
+
+// The sizes that dispatch_rows and combine_rows share.
+int rows_sizes(int64_t T, int64_t k, int64_t C) {
+    if (T < 0 || k <= 0 || C <= 0) return TMAGEMM_ERR_INVALID;
+    if (k > kMaxChoices || T > kMax32 / k || C > (1 << 20)) return TMAGEMM_ERR_UNSUPPORTED;
+    return (C % 8) != 0 ? TMAGEMM_ERR_ALIGN : TMAGEMM_OK;
+}
+
+int combine_args(int64_t T, int64_t k, int64_t C, int64_t R, const void* rows,
+                 const int32_t* row_of, const float* weights, CombineArgs* a) {
+    if (int s = rows_sizes(T, k, C)) return s;
+    if (R < 0 || (T > 0 && (!row_of || (R > 0 && !rows)))) return TMAGEMM_ERR_INVALID;
+    if (R > kMax32) return TMAGEMM_ERR_UNSUPPORTED;
+    if (!aligned16(rows) || !aligned4(row_of) || !aligned4(weights)) return TMAGEMM_ERR_ALIGN;
+    *a = CombineArgs{};
+    a->T = T;
+    a->R = R;
+    a->k = static_cast<int32_t>(k);
+    a->C8 = static_cast<int32_t>(C / 8);
+    a->rows = static_cast<const uint4*>(rows);
+    a->row_of = row_of;
+    a->weights = weights;
+    return TMAGEMM_OK;
+}
+
+// gemm_w4 (offsets == NULL, G = 1) and gemm_w4_grouped.
+int gemm_w4_impl(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                 int64_t group, const void* A, const void* B, const void* SB, const void* ZB,
+                 void* D, int bf16, void* stream) {
+    if (M < 0 || !B || !SB || (M > 0 && (!A || !D)) || (group != 32 && group != 64 && group != 128))
+        return TMAGEMM_ERR_INVALID;
+    if (int s = validate_common(M > 0 ? M : 1, N, K)) return s;
+    if ((K % 32) != 0 || !aligned16(A) || !aligned16(B) || !aligned2(SB) || !aligned2(D) ||
+        !aligned4(offsets))
+        return TMAGEMM_ERR_ALIGN;
+    if (M == 0) return TMAGEMM_OK;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    W4Args a{};
+    a.A = static_cast<const uint4*>(A);
+    a.B = static_cast<const uint4*>(B);
+    a.S = static_cast<const uint16_t*>(SB);
+    a.Z = static_cast<const uint8_t*>(ZB);
+    a.D = static_cast<uint16_t*>(D);
+    a.offsets = offsets;
+    a.M = static_cast<int32_t>(M);
+    a.N = static_cast<int32_t>(N);
+    a.K = static_cast<int32_t>(K);
+    a.groups = static_cast<int32_t>(G);
+    a.group = static_cast<int32_t>(group);
+    a.scale_groups = static_cast<int32_t>(ceil_div(K, group));
+    const W4Device dev{d->sms, wait_limit_ns(), d->err_word, process_tuning().pdl()};
+    return launch_gemm_w4(a, bf16 != 0, dev, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int route_topk(const tmagemm_route* p, void* stream) {
+    RouteArgs a;
+    if (int s = route_args(p, &a)) return s;
+    if (p->groups <= 0 || p->E % p->groups != 0 || p->top_groups <= 0 ||
+        p->top_groups > p->groups || (p->groups > 1 && p->group_sum != 1 && p->group_sum != 2) ||
+        p->k > p->E / p->groups * p->top_groups || (p->T > 0 && (!p->ids || !p->weights)))
+        return TMAGEMM_ERR_INVALID;
+    if (p->groups > 32) return TMAGEMM_ERR_UNSUPPORTED;
+    if (!aligned4(p->bias) || !aligned4(p->weights)) return TMAGEMM_ERR_ALIGN;
+    if (p->T == 0) return TMAGEMM_OK;
+    a.groups = p->groups;
+    a.top_groups = p->top_groups;
+    a.group_sum = p->group_sum;
+    a.bias = p->bias;
+    a.weights = p->weights;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return launch_route(a, p->type, process_tuning().pdl(), static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+int route_topk_backward(const tmagemm_route* p, void* stream) {
+    RouteArgs a;
+    if (int s = route_args(p, &a)) return s;
+    if (p->T > 0 && (!p->ids || !p->dweights || !p->dlogits)) return TMAGEMM_ERR_INVALID;
+    if (!aligned4(p->dweights) ||
+        (p->type == kLogitsF32 ? !aligned4(p->dlogits) : !aligned2(p->dlogits)))
+        return TMAGEMM_ERR_ALIGN;
+    if (p->T == 0) return TMAGEMM_OK;
+    a.dweights = p->dweights;
+    a.dlogits = p->dlogits;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return launch_route_backward(a, p->type, process_tuning().pdl(),
+                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+int64_t dispatch_rows_workspace_size(int64_t T, int64_t k, int64_t E) {
+    if (E <= 0) return TMAGEMM_ERR_INVALID;
+    if (int s = rows_sizes(T, k, 8)) return s;
+    if (E > kMaxExperts) return TMAGEMM_ERR_UNSUPPORTED;
+    return dispatch_workspace(T * k, E);
+}
+
+int dispatch_rows(int64_t T, int64_t k, int64_t E, int64_t C, const int32_t* ids, const void* x,
+                  int bf16, void* rows, float* scales, int64_t s_row_stride,
+                  int64_t s_block_stride, int32_t* offsets, int32_t* row_of, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
+    const int64_t need = dispatch_rows_workspace_size(T, k, E);
+    if (need < 0) return static_cast<int>(need);
+    if (int s = rows_sizes(T, k, C)) return s;
+    if (!offsets || (T > 0 && (!ids || !x || !rows || !row_of)) ||
+        (scales && (s_row_stride <= 0 || s_block_stride <= 0)))
+        return TMAGEMM_ERR_INVALID;
+    if (!aligned16(x) || !aligned16(rows) || !aligned4(ids) || !aligned4(scales) ||
+        !aligned4(offsets) || !aligned4(row_of))
+        return TMAGEMM_ERR_ALIGN;
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+        return TMAGEMM_ERR_WORKSPACE;
+    DispatchArgs a{};
+    a.T = T;
+    a.k = static_cast<int32_t>(k);
+    a.E = static_cast<int32_t>(E);
+    a.C8 = static_cast<int32_t>(C / 8);
+    a.ids = ids;
+    a.x = static_cast<const uint4*>(x);
+    a.rows = rows;
+    a.scales = scales;
+    a.s_row = s_row_stride;
+    a.s_blk = s_block_stride;
+    a.offsets = offsets;
+    a.row_of = row_of;
+    a.counts = static_cast<int32_t*>(workspace);
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return launch_dispatch(a, bf16 != 0, process_tuning().pdl(),
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+int combine_rows(int64_t T, int64_t k, int64_t C, int64_t R, const void* rows,
+                 const int32_t* row_of, const float* weights, void* y, int bf16, void* stream) {
+    CombineArgs a;
+    if (int s = combine_args(T, k, C, R, rows, row_of, weights, &a)) return s;
+    if (T > 0 && !y) return TMAGEMM_ERR_INVALID;
+    if (!aligned16(y)) return TMAGEMM_ERR_ALIGN;
+    if (T == 0) return TMAGEMM_OK;
+    a.y = static_cast<uint4*>(y);
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return launch_combine(a, bf16 != 0, process_tuning().pdl(),
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+int combine_rows_backward(int64_t T, int64_t k, int64_t C, int64_t R, const void* dy,
+                          const void* rows, const int32_t* row_of, const float* weights,
+                          void* drows, float* dweights, int bf16, void* stream) {
+    CombineArgs a;
+    if (int s = combine_args(T, k, C, R, rows, row_of, weights, &a)) return s;
+    if (T > 0 && (!dy || !weights || !dweights || (R > 0 && !drows))) return TMAGEMM_ERR_INVALID;
+    if (!aligned16(dy) || !aligned16(drows) || !aligned4(dweights)) return TMAGEMM_ERR_ALIGN;
+    if (T == 0) return TMAGEMM_OK;
+    a.dy = static_cast<const uint4*>(dy);
+    a.drows = static_cast<uint4*>(drows);
+    a.dweights = dweights;
+    DeviceState* d = nullptr;
+    if (int s = device_state(&d)) return s;
+    return launch_combine_backward(a, bf16 != 0, process_tuning().pdl(),
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? TMAGEMM_OK
+               : TMAGEMM_ERR_CUDA;
+}
+
+int gemm_w4(int64_t M, int64_t N, int64_t K, int64_t group, const void* A, const void* B,
+            const void* SB, const void* ZB, void* D, int bf16, void* stream) {
+    return gemm_w4_impl(1, nullptr, M, N, K, group, A, B, SB, ZB, D, bf16, stream);
+}
+
+int gemm_w4_grouped(int64_t G, const int32_t* m_offsets, int64_t M, int64_t N, int64_t K,
+                    int64_t group, const void* A, const void* B, const void* SB, const void* ZB,
+                    void* D, int bf16, void* stream) {
+    if (!m_offsets || G <= 0) return TMAGEMM_ERR_INVALID;
+    if (G > kMaxFp8Groups) return TMAGEMM_ERR_UNSUPPORTED;
+    return gemm_w4_impl(G, m_offsets, M, N, K, group, A, B, SB, ZB, D, bf16, stream);
+}
+
+}  // extern "C"
+
 extern "C" {
 
 int tmagemm_check(void* stream) {
@@ -849,7 +1072,8 @@ const char* tmagemm_strerror(int status) {
         case TMAGEMM_ERR_INVALID: return "invalid argument (non-positive size or NULL pointer)";
         case TMAGEMM_ERR_ALIGN:
             return "alignment: pointers must be 16-byte aligned, K % 8 == 0 and N % 8 == 0 "
-                   "(e4m3 products: K % 16 == 0; norms: C % 8 == 0)";
+                   "(e4m3 products: K % 16 == 0; 4-bit ones: K % 32 == 0; norms and rows of "
+                   "experts: C % 8 == 0)";
         case TMAGEMM_ERR_UNSUPPORTED: return "unsupported size or device";
         case TMAGEMM_ERR_CUDA: return "CUDA runtime or driver call failed";
         case TMAGEMM_ERR_TIMEOUT: return "device-side pipeline wait timed out";

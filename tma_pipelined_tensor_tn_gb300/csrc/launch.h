@@ -256,6 +256,77 @@ cudaError_t launch_norm_forward(const NormArgs& p, bool bf16, int sms, bool pdl,
 cudaError_t launch_norm_backward(const NormArgs& p, bool bf16, int sms, bool pdl,
                                  cudaStream_t stream);
 
+// The router (route.cu).
+enum LogitsType : int { kLogitsF16 = 0, kLogitsBf16 = 1, kLogitsF32 = 2 };
+enum RouteScore : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
+constexpr int kMaxExperts = 512;
+constexpr int kMaxChoices = 32;       // a lane each
+struct RouteArgs {
+    int64_t T;
+    int32_t E, k, groups, top_groups, group_sum;
+    int32_t group_lanes;              // lanes that hold a group (set by the launch)
+    int score;
+    bool renormalize;
+    float scale;
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    const float* dweights;
+    void* dlogits;
+};
+cudaError_t launch_route(RouteArgs a, int type, bool pdl, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouteArgs& a, int type, bool pdl, cudaStream_t stream);
+
+// Rows by expert and back (dispatch.cu).  Rows of 8 C8 columns.
+struct DispatchArgs {
+    int64_t T;
+    int32_t k, E, C8;
+    const int32_t* ids;
+    const uint4* x;
+    void* rows;
+    float* scales;                    // NULL: rows in 16 bits
+    int64_t s_row, s_blk;
+    int32_t *offsets, *row_of;
+    int32_t* counts;                  // workspace
+};
+int64_t dispatch_workspace(int64_t slots, int64_t E);
+cudaError_t launch_dispatch(const DispatchArgs& a, bool bf16, bool pdl, cudaStream_t stream);
+
+struct CombineArgs {
+    int64_t T, R;
+    int32_t k, C8;
+    const uint4* rows;
+    const int32_t* row_of;
+    const float* weights;             // NULL: ones
+    uint4* y;                         // forward
+    const uint4* dy;                  // backward
+    uint4* drows;
+    float* dweights;
+};
+cudaError_t launch_combine(const CombineArgs& a, bool bf16, bool pdl, cudaStream_t stream);
+cudaError_t launch_combine_backward(const CombineArgs& a, bool bf16, bool pdl,
+                                    cudaStream_t stream);
+
+// Products with 4-bit weights (gemm_w4.cu).  offsets == NULL: one group of all rows.
+struct W4Args {
+    const uint4* A;
+    const uint4* B;                   // [groups][N][K / 32] blocks of 32 codes
+    const uint16_t* S;                // [groups][N][scale_groups]
+    const uint8_t* Z;                 // the same, or NULL
+    uint16_t* D;
+    const int32_t* offsets;
+    int32_t M, N, K, groups;
+    int32_t group, scale_groups;      // k per scale, scales per row
+};
+struct W4Device {
+    int sms;
+    uint64_t limit_ns;
+    uint32_t* err_word;
+    bool pdl;
+};
+cudaError_t launch_gemm_w4(const W4Args& a, bool bf16, const W4Device& dev, cudaStream_t stream);
+
 // cudaLaunchKernelEx with a cluster of `cluster_x` CTAs along x (1 = none)
 // and, when `pdl` is set, the programmatic-stream-serialization attribute
 // (programmatic dependent launch): the next kernel on the stream is scheduled

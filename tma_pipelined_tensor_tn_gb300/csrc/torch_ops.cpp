@@ -1,4 +1,5 @@
-// Binding of the 8-bit operators and the norms for torch tensors: checks the
+// Binding of the 8-bit and 4-bit operators, the norms and the router's operators for
+// torch tensors: checks the
 // operands, allocates the results on the current stream of their device and
 // calls the C ABI (include/tmagemm.h) there.  Native because these calls are
 // often smaller than their own marshalling: at one token a kernel takes 1 to 3
@@ -32,6 +33,14 @@ struct Library {
     decltype(&::norm_residual) norm;
     decltype(&::norm_residual_backward) norm_backward;
     decltype(&::norm_residual_backward_workspace_size) norm_workspace;
+    decltype(&::route_topk) route;
+    decltype(&::route_topk_backward) route_backward;
+    decltype(&::dispatch_rows) dispatch;
+    decltype(&::dispatch_rows_workspace_size) dispatch_workspace;
+    decltype(&::combine_rows) combine;
+    decltype(&::combine_rows_backward) combine_backward;
+    decltype(&::gemm_w4) w4;
+    decltype(&::gemm_w4_grouped) w4_grouped;
 } lib;
 
 struct StatusError {
@@ -283,6 +292,179 @@ std::tuple<Tensor, MaybeTensor, MaybeTensor, MaybeTensor, MaybeTensor> norm_back
     return {dh_in, dy, dgate, dw_post, dw_pre};
 }
 
+// ---- routed experts ----
+
+// The operands that route_topk and its backward share.
+tmagemm_route route_operands(const Tensor& logits, int64_t k, bool sigmoid, bool renormalize,
+                             double scale) {
+    check_first("logits", logits, 2);
+    const at::ScalarType type = logits.scalar_type();
+    tmagemm_route p{};
+    p.type = type == at::kFloat ? 2 : -1;
+    if (p.type < 0) {
+        if (type != at::kBFloat16 && type != at::kHalf)
+            throw py::type_error(std::string("logits must be float32, float16 or bfloat16, got ") +
+                                 c10::toString(type));
+        p.type = type == at::kBFloat16;
+    }
+    if (!logits.is_contiguous()) throw py::value_error("logits must be contiguous (row-major)");
+    p.T = logits.size(0);
+    p.E = logits.size(1);
+    if (k < 1 || k > p.E)
+        throw py::value_error("k must be from 1 to the number of experts, got " +
+                              std::to_string(k));
+    p.k = static_cast<int32_t>(std::min<int64_t>(k, INT32_MAX));
+    p.score = sigmoid;
+    p.renormalize = renormalize;
+    p.scale = static_cast<float>(scale);
+    p.logits = logits.data_ptr();
+    return p;
+}
+
+std::tuple<Tensor, Tensor> route(const Tensor& logits, int64_t k, bool sigmoid,
+                                 const MaybeTensor& bias, int64_t groups, int64_t top_groups,
+                                 int64_t group_sum, bool renormalize, double scale) {
+    tmagemm_route p = route_operands(logits, k, sigmoid, renormalize, scale);
+    if (groups < 1 || groups > p.E || p.E % groups != 0)
+        throw py::value_error("groups must divide the number of experts");
+    if (top_groups < 1 || top_groups > groups || k > p.E / groups * top_groups)
+        throw py::value_error("top_groups must be from 1 to groups and hold k experts");
+    if (group_sum != 1 && group_sum != 2) throw py::value_error("group_sum must be 1 or 2");
+    if (bias) check("bias", *bias, at::kFloat, {p.E}, logits.device());
+    const c10::cuda::CUDAGuard guard(logits.device());
+    Tensor ids = empty({p.T, k}, at::kInt, logits), weights = empty({p.T, k}, at::kFloat, logits);
+    p.groups = static_cast<int32_t>(groups);
+    p.top_groups = static_cast<int32_t>(top_groups);
+    p.group_sum = static_cast<int32_t>(group_sum);
+    p.bias = static_cast<const float*>(ptr(bias));
+    p.ids = static_cast<int32_t*>(ids.data_ptr());
+    p.weights = static_cast<float*>(weights.data_ptr());
+    require(lib.route(&p, stream_of(logits.device())), "route_topk");
+    return {ids, weights};
+}
+
+Tensor route_backward(const Tensor& logits, const Tensor& ids, const Tensor& dweights,
+                      bool sigmoid, bool renormalize, double scale) {
+    check_first("ids", ids, 2);
+    tmagemm_route p = route_operands(logits, ids.size(1), sigmoid, renormalize, scale);
+    check("ids", ids, at::kInt, {p.T, p.k}, logits.device());
+    check("dweights", dweights, at::kFloat, {p.T, p.k}, logits.device());
+    const c10::cuda::CUDAGuard guard(logits.device());
+    Tensor dlogits = same(logits);
+    p.ids = static_cast<int32_t*>(ids.data_ptr());
+    p.dweights = static_cast<const float*>(dweights.data_ptr());
+    p.dlogits = dlogits.data_ptr();
+    require(lib.route_backward(&p, stream_of(logits.device())), "route_topk_backward");
+    return dlogits;
+}
+
+std::tuple<Tensor, MaybeTensor, Tensor, Tensor> dispatch(const Tensor& x, const Tensor& ids,
+                                                         int64_t experts, bool quantize) {
+    check_first("x", x, 2);
+    check_first("ids", ids, 2);
+    const at::ScalarType type = x.scalar_type();
+    const at::Device device = x.device();
+    const int bf16 = bf16_flag(type);
+    const int64_t T = x.size(0), C = x.size(1), k = ids.size(1);
+    check("x", x, type, x.sizes(), device);
+    check("ids", ids, at::kInt, {T, k}, device);
+    const c10::cuda::CUDAGuard guard(device);
+    const int64_t need = lib.dispatch_workspace(T, k, experts);
+    if (need < 0) require(static_cast<int>(need), "dispatch_rows_workspace_size");
+    Tensor workspace, rows = empty({T * k, C}, quantize ? at::kFloat8_e4m3fn : type, x);
+    if (need > 0) workspace = empty({need}, at::kByte, x);
+    MaybeTensor scales;
+    if (quantize) scales = row_scales(T * k, C, x);
+    Tensor offsets = empty({experts + 1}, at::kInt, x), row_of = empty({T, k}, at::kInt, x);
+    require(lib.dispatch(T, k, experts, C, static_cast<const int32_t*>(ids.data_ptr()),
+                         x.data_ptr(), bf16, rows.data_ptr(), static_cast<float*>(ptr(scales)), 1,
+                         std::max<int64_t>(T * k, 1), static_cast<int32_t*>(offsets.data_ptr()),
+                         static_cast<int32_t*>(row_of.data_ptr()),
+                         need > 0 ? workspace.data_ptr() : nullptr, need, stream_of(device)),
+            "dispatch_rows");
+    return {rows, scales, offsets, row_of};
+}
+
+// The checked operands of combine_rows and its backward.
+struct Rows {
+    int64_t T, k, C, R;
+    int bf16;
+};
+Rows combine_operands(const Tensor& rows, const Tensor& row_of, const MaybeTensor& weights) {
+    check_first("rows", rows, 2);
+    check_first("row_of", row_of, 2);
+    const Rows n{row_of.size(0), row_of.size(1), rows.size(1), rows.size(0),
+                 bf16_flag(rows.scalar_type())};
+    check("rows", rows, rows.scalar_type(), rows.sizes(), rows.device());
+    check("row_of", row_of, at::kInt, row_of.sizes(), rows.device());
+    if (weights) check("weights", *weights, at::kFloat, {n.T, n.k}, rows.device());
+    return n;
+}
+
+Tensor combine(const Tensor& rows, const Tensor& row_of, const MaybeTensor& weights) {
+    const Rows n = combine_operands(rows, row_of, weights);
+    const c10::cuda::CUDAGuard guard(rows.device());
+    Tensor y = empty({n.T, n.C}, rows.scalar_type(), rows);
+    require(lib.combine(n.T, n.k, n.C, n.R, rows.data_ptr(),
+                        static_cast<const int32_t*>(row_of.data_ptr()),
+                        static_cast<const float*>(ptr(weights)), y.data_ptr(), n.bf16,
+                        stream_of(rows.device())),
+            "combine_rows");
+    return y;
+}
+
+std::tuple<Tensor, Tensor> combine_backward(const Tensor& dy, const Tensor& rows,
+                                            const Tensor& row_of, const Tensor& weights) {
+    const Rows n = combine_operands(rows, row_of, weights);
+    check("dy", dy, rows.scalar_type(), {n.T, n.C}, rows.device());
+    const c10::cuda::CUDAGuard guard(rows.device());
+    Tensor drows = same(rows), dweights = empty({n.T, n.k}, at::kFloat, rows);
+    require(lib.combine_backward(n.T, n.k, n.C, n.R, dy.data_ptr(), rows.data_ptr(),
+                                 static_cast<const int32_t*>(row_of.data_ptr()),
+                                 static_cast<const float*>(weights.data_ptr()), drows.data_ptr(),
+                                 static_cast<float*>(dweights.data_ptr()), n.bf16,
+                                 stream_of(rows.device())),
+            "combine_rows_backward");
+    return {drows, dweights};
+}
+
+// ---- 4-bit weights ----
+
+// gemm_w4 (no offsets) and gemm_w4_grouped.
+Tensor product_w4(const Tensor& A, const Tensor& B, const Tensor& SB, const MaybeTensor& ZB,
+                  const MaybeTensor& offsets, int64_t group, const MaybeTensor& out) {
+    check_first("A", A, 2);
+    check_first("B", B, offsets ? 3 : 2);
+    const at::ScalarType type = A.scalar_type();
+    const at::Device device = A.device();
+    const int bf16 = bf16_flag(type);
+    const int64_t M = A.size(0), K = A.size(1), N = B.size(-2), G = offsets ? B.size(0) : 1;
+    if (group != 32 && group != 64 && group != 128)
+        throw py::value_error("group must be 32, 64 or 128");
+    if (K % 32 != 0) throw py::value_error("A must have a multiple of 32 columns");
+    const int64_t kg = (K + group - 1) / group;
+    check("A", A, type, A.sizes(), device);
+    const int64_t codes[3] = {G, N, K / 2}, scales[3] = {G, N, kg};
+    const int skip = offsets ? 0 : 1;
+    check("B", B, at::kByte, at::IntArrayRef(codes + skip, 3 - skip), device);
+    check("SB", SB, type, at::IntArrayRef(scales + skip, 3 - skip), device);
+    if (ZB) check("ZB", *ZB, at::kByte, at::IntArrayRef(scales + skip, 3 - skip), device);
+    if (offsets) check("m_offsets", *offsets, at::kInt, {G + 1}, device);
+    if (out) check("out", *out, type, {M, N}, device);
+    const c10::cuda::CUDAGuard guard(device);
+    Tensor D = out ? *out : empty({M, N}, type, A);
+    if (offsets)
+        require(lib.w4_grouped(G, static_cast<const int32_t*>(offsets->data_ptr()), M, N, K, group,
+                               A.data_ptr(), B.data_ptr(), SB.data_ptr(), ptr(ZB), D.data_ptr(),
+                               bf16, stream_of(device)),
+                "gemm_w4_grouped");
+    else
+        require(lib.w4(M, N, K, group, A.data_ptr(), B.data_ptr(), SB.data_ptr(), ptr(ZB),
+                       D.data_ptr(), bf16, stream_of(device)),
+                "gemm_w4");
+    return D;
+}
+
 py::object& error_class() {
     static py::object* cls = new py::object();   // lives as long as the process
     return *cls;
@@ -301,6 +483,14 @@ void bind(const py::dict& functions, py::object error) {
     take(lib.norm, functions, "norm_residual");
     take(lib.norm_backward, functions, "norm_residual_backward");
     take(lib.norm_workspace, functions, "norm_residual_backward_workspace_size");
+    take(lib.route, functions, "route_topk");
+    take(lib.route_backward, functions, "route_topk_backward");
+    take(lib.dispatch, functions, "dispatch_rows");
+    take(lib.dispatch_workspace, functions, "dispatch_rows_workspace_size");
+    take(lib.combine, functions, "combine_rows");
+    take(lib.combine_backward, functions, "combine_rows_backward");
+    take(lib.w4, functions, "gemm_w4");
+    take(lib.w4_grouped, functions, "gemm_w4_grouped");
     error_class() = std::move(error);
 }
 
@@ -320,4 +510,10 @@ PYBIND11_MODULE(_torch_ops, m) {
     m.def("product", &product);
     m.def("norm_residual", &norm);
     m.def("norm_residual_backward", &norm_backward);
+    m.def("route_topk", &route);
+    m.def("route_topk_backward", &route_backward);
+    m.def("dispatch_rows", &dispatch);
+    m.def("combine_rows", &combine);
+    m.def("combine_rows_backward", &combine_backward);
+    m.def("product_w4", &product_w4);
 }

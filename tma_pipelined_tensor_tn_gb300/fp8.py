@@ -26,7 +26,9 @@ from ._binding import TmaGemmError, lib
 
 FP8_BLOCK = 128
 _FUNCTIONS = ("quantize_fp8", "gemm_fp8", "gemm_fp8_grouped", "norm_residual",
-              "norm_residual_backward", "norm_residual_backward_workspace_size")
+              "norm_residual_backward", "norm_residual_backward_workspace_size",
+              "route_topk", "route_topk_backward", "dispatch_rows", "dispatch_rows_workspace_size",
+              "combine_rows", "combine_rows_backward", "gemm_w4", "gemm_w4_grouped")
 _lock = threading.Lock()
 _native = None
 
