@@ -521,8 +521,10 @@ int combine_rows_backward(int64_t T, int64_t k, int64_t C, int64_t R, const void
  *           NULL: 8 everywhere.
  *   D     : device pointer, M x N in the type of A; written, never read.
  *   group : 32, 64 or 128.
- * Requirements: A, B 16-byte, SB, D 2-byte aligned; K % 32 == 0.  M = 0 is OK and
- * writes nothing.  Deterministic.  Status codes as gemm_f16.
+ * Requirements: A, B 16-byte, SB, D 2-byte aligned; K % 32 == 0.  K <= 2^26, M <= 2^31 -
+ * 256, the rows of all weight matrices together and M / 8 times N / 16 below 2^31 (else
+ * TMAGEMM_ERR_UNSUPPORTED).  M = 0 is OK and writes nothing.  Deterministic.  Status codes
+ * as gemm_f16.
  */
 int gemm_w4(int64_t M, int64_t N, int64_t K, int64_t group, const void* A, const void* B,
             const void* SB, const void* ZB, void* D, int bf16, void* stream);

@@ -125,7 +125,8 @@ W4_REFUSALS = [
     (dict(SB=None), INVALID), (dict(D=None), INVALID), (dict(M=1 << 31), UNSUPPORTED),
     (dict(N=1 << 31), UNSUPPORTED), (dict(K=272), ALIGN), (dict(A=P + 8), ALIGN),
     (dict(B=P + 8), ALIGN), (dict(SB=P + 1), ALIGN), (dict(D=P + 1), ALIGN),
-    (dict(M=0, A=None, D=None), OK)]
+    (dict(M=(1 << 31) - 255), UNSUPPORTED), (dict(K=(1 << 26) + 32), UNSUPPORTED),
+    (dict(M=1 << 22, N=1 << 20), UNSUPPORTED), (dict(M=0, A=None, D=None), OK)]
 
 
 @pytest.mark.parametrize("change,expect", W4_REFUSALS)
@@ -135,7 +136,7 @@ def test_w4_refusals(change, expect):
 
 @pytest.mark.parametrize("change,expect", W4_REFUSALS + [
     (dict(G=0), INVALID), (dict(offsets=None), INVALID), (dict(G=385), UNSUPPORTED),
-    (dict(offsets=P + 2), ALIGN)])
+    (dict(offsets=P + 2), ALIGN), (dict(G=300, N=1 << 23), UNSUPPORTED)])
 def test_w4_grouped_refusals(change, expect):
     a = {**dict(G=3, offsets=P), **W4, **change}
     assert tg.lib().gemm_w4_grouped(*a.values(), None) == expect

@@ -867,6 +867,10 @@ int gemm_w4_impl(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64_
     if ((K % 32) != 0 || !aligned16(A) || !aligned16(B) || !aligned2(SB) || !aligned2(D) ||
         !aligned4(offsets))
         return TMAGEMM_ERR_ALIGN;
+    // Rows, units and a row's scales are counted in 32 bits; a block of tokens may end past M.
+    if (M > (int64_t(1) << 31) - 256 || K > (int64_t(1) << 26) || G * N > kMax32 ||
+        (ceil_div(M, 8) + G) * ceil_div(N, 16) > kMax32)
+        return TMAGEMM_ERR_UNSUPPORTED;
     if (M == 0) return TMAGEMM_OK;
     DeviceState* d = nullptr;
     if (int s = device_state(&d)) return s;
@@ -883,7 +887,7 @@ int gemm_w4_impl(int64_t G, const int32_t* offsets, int64_t M, int64_t N, int64_
     a.groups = static_cast<int32_t>(G);
     a.group = static_cast<int32_t>(group);
     a.scale_groups = static_cast<int32_t>(ceil_div(K, group));
-    const W4Device dev{d->sms, wait_limit_ns(), d->err_word, process_tuning().pdl()};
+    const W4Device dev{g_encode, d->sms, wait_limit_ns(), d->err_word, process_tuning().pdl()};
     return launch_gemm_w4(a, bf16 != 0, dev, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TMAGEMM_OK
                : TMAGEMM_ERR_CUDA;

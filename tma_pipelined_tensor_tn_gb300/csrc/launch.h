@@ -320,6 +320,7 @@ struct W4Args {
     int32_t group, scale_groups;      // k per scale, scales per row
 };
 struct W4Device {
+    EncodeTiled encode;
     int sms;
     uint64_t limit_ns;
     uint32_t* err_word;
