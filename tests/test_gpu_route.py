@@ -123,6 +123,23 @@ def test_values_that_32_bits_cannot_tell_apart(tg, score, groups, top_groups):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_sum,top_groups", [(0, 0), (1, 3), (2, 3), (2, 5)])
+def test_pairs_that_32_bits_cannot_tell_apart(tg, score, group_sum, top_groups):
+    """Runs of eight experts in pairs whose values are equal to FP32 rounding, one run far
+    from the next: neighbours in doubt, and groups, with the rest well apart."""
+    T, E = 200, 64
+    logits = make(1, E, "f32", seed=3).expand(T, E).contiguous()
+    p = ref.scores(logits.double().cpu().numpy(), score)[0]
+    v = p + 0.25 * np.arange(E) / E
+    for g in range(1, 8, 2):
+        v[8 * g:8 * g + 8] = v[8 * g - 8:8 * g]
+    bias = torch.from_numpy((v - p).astype(np.float32)).cuda()
+    logits = logits + (1e-7 * torch.randn((T, E), device="cuda"))
+    kw = dict(groups=8, top_groups=top_groups, group_sum=group_sum) if group_sum else {}
+    check(tg, logits, 7, score=score, bias=bias, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalize", [False, True])
 def test_closed_experts(tg, score, renormalize):
     """-inf closes an expert, whatever its bias; a token without any gets ids of -1."""

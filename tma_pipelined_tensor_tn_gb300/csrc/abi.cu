@@ -914,8 +914,8 @@ int route_topk(const tmagemm_route* p, void* stream) {
     a.weights = p->weights;
     DeviceState* d = nullptr;
     if (int s = device_state(&d)) return s;
-    return launch_route(a, p->type, process_tuning().pdl(), static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
+    return launch_route(a, p->type, d->sms, process_tuning().pdl(),
+                        static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TMAGEMM_OK
                : TMAGEMM_ERR_CUDA;
 }
@@ -932,7 +932,7 @@ int route_topk_backward(const tmagemm_route* p, void* stream) {
     a.dlogits = p->dlogits;
     DeviceState* d = nullptr;
     if (int s = device_state(&d)) return s;
-    return launch_route_backward(a, p->type, process_tuning().pdl(),
+    return launch_route_backward(a, p->type, d->sms, process_tuning().pdl(),
                                  static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TMAGEMM_OK
                : TMAGEMM_ERR_CUDA;
@@ -976,7 +976,7 @@ int dispatch_rows(int64_t T, int64_t k, int64_t E, int64_t C, const int32_t* ids
     a.counts = static_cast<int32_t*>(workspace);
     DeviceState* d = nullptr;
     if (int s = device_state(&d)) return s;
-    return launch_dispatch(a, bf16 != 0, process_tuning().pdl(),
+    return launch_dispatch(a, bf16 != 0, d->sms, process_tuning().pdl(),
                            static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TMAGEMM_OK
                : TMAGEMM_ERR_CUDA;
@@ -992,7 +992,7 @@ int combine_rows(int64_t T, int64_t k, int64_t C, int64_t R, const void* rows,
     a.y = static_cast<uint4*>(y);
     DeviceState* d = nullptr;
     if (int s = device_state(&d)) return s;
-    return launch_combine(a, bf16 != 0, process_tuning().pdl(),
+    return launch_combine(a, bf16 != 0, d->sms, process_tuning().pdl(),
                           static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? TMAGEMM_OK
                : TMAGEMM_ERR_CUDA;

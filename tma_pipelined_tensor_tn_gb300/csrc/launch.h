@@ -264,7 +264,8 @@ constexpr int kMaxChoices = 32;       // a lane each
 struct RouteArgs {
     int64_t T;
     int32_t E, k, groups, top_groups, group_sum;
-    int32_t group_lanes;              // lanes that hold a group (set by the launch)
+    int32_t group_size, lanes_shift;  // experts of a group, its lanes (1 << shift); these
+    bool aligned, bias_aligned;       // four are set by the launch: vector loads are possible
     int score;
     bool renormalize;
     float scale;
@@ -275,8 +276,9 @@ struct RouteArgs {
     const float* dweights;
     void* dlogits;
 };
-cudaError_t launch_route(RouteArgs a, int type, bool pdl, cudaStream_t stream);
-cudaError_t launch_route_backward(const RouteArgs& a, int type, bool pdl, cudaStream_t stream);
+cudaError_t launch_route(RouteArgs a, int type, int sms, bool pdl, cudaStream_t stream);
+cudaError_t launch_route_backward(const RouteArgs& a, int type, int sms, bool pdl,
+                                  cudaStream_t stream);
 
 // Rows by expert and back (dispatch.cu).  Rows of 8 C8 columns.
 struct DispatchArgs {
@@ -291,7 +293,8 @@ struct DispatchArgs {
     int32_t* counts;                  // workspace
 };
 int64_t dispatch_workspace(int64_t slots, int64_t E);
-cudaError_t launch_dispatch(const DispatchArgs& a, bool bf16, bool pdl, cudaStream_t stream);
+cudaError_t launch_dispatch(const DispatchArgs& a, bool bf16, int sms, bool pdl,
+                            cudaStream_t stream);
 
 struct CombineArgs {
     int64_t T, R;
@@ -304,7 +307,8 @@ struct CombineArgs {
     uint4* drows;
     float* dweights;
 };
-cudaError_t launch_combine(const CombineArgs& a, bool bf16, bool pdl, cudaStream_t stream);
+cudaError_t launch_combine(const CombineArgs& a, bool bf16, int sms, bool pdl,
+                           cudaStream_t stream);
 cudaError_t launch_combine_backward(const CombineArgs& a, bool bf16, bool pdl,
                                     cudaStream_t stream);
 
