@@ -357,7 +357,7 @@ __device__ __forceinline__ uint32_t sort_lanes(uint32_t key, int lane) {
 }
 
 template <int TYPE, int V>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_constant__ RouteArgs a) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = static_cast<int>(threadIdx.x) & 31;
