@@ -1,10 +1,11 @@
 """An expert feed-forward block in 8-bit floating point, with the library's
 operators used together as in serving:
 
-  residual stream --norm_residual(quantize)--> codes + row scales
-    --route (top-k)--> rows sorted by expert, offsets on the device
+  residual stream --norm_residual--> block input
+    --route_topk--> experts and weights of each token
+    --dispatch_rows(quantize)--> codes + row scales by expert, offsets on the device
     --gemm_fp8_grouped--> gate and up --silu * mul, quantize_fp8-->
-    --gemm_fp8_grouped--> down --weighted sum--> block output
+    --gemm_fp8_grouped--> down --combine_rows--> block output
     --norm_residual--> next residual stream and next block's input
     --gemm_fp8--> logits of the last token
 
@@ -41,6 +42,7 @@ class Block:
         self.up = weight(experts, 2 * hidden, channels, fan_in=channels).bfloat16()
         self.down = weight(experts, channels, hidden, fan_in=hidden).bfloat16()
         self.head = weight(vocab, channels, fan_in=channels).bfloat16()
+        self.experts = experts
         self.first = torch.arange(experts + 1, device="cuda")
         # Whole matrices of experts share the 128-row blocks when their rows are
         # a multiple of 128; each is quantised by itself to allow any size.
@@ -55,8 +57,8 @@ class Block:
             torch.stack([s for _, s in pairs])
 
     def route(self, x, top):
-        """Expert of each (token, choice) row, sorted by expert: source rows,
-        their weights, and the experts' row offsets (int32, on the device)."""
+        """The plain block's routing: source rows sorted by expert, their weights, and the
+        experts' row offsets."""
         p, expert = torch.topk(torch.softmax((x @ self.router.t()).float(), dim=1), top)
         expert, order = torch.sort(expert.flatten(), stable=True)
         # First row of each expert (torch.bincount would wait for the device).
@@ -67,17 +69,16 @@ class Block:
         """(next residual stream, next block's input, logits of the last token)."""
         # The router reads the 16-bit norm, the experts its codes.
         x = tg.norm_residual(h, w_pre=self.w_pre).x
-        codes, scales = tg.quantize_fp8(x)
-        rows, share, offsets = self.route(x, top)
-        a, sa = codes.view(torch.uint8)[rows].view(torch.float8_e4m3fn), scales[rows]
-        gate, up = tg.gemm_fp8_grouped(a, sa, self.up_q, self.up_s, offsets).chunk(2, dim=1)
+        ids, share = tg.route_topk(x @ self.router.t(), top)
+        r = tg.dispatch_rows(x, ids, self.experts, quantize=True)
+        gate, up = tg.gemm_fp8_grouped(r.rows, r.scales, self.up_q, self.up_s,
+                                       r.offsets).chunk(2, dim=1)
         act, act_s = tg.quantize_fp8(torch.nn.functional.silu(gate) * up)
-        out = tg.gemm_fp8_grouped(act, act_s, self.down_q, self.down_s, offsets)
-        y = torch.zeros(h.shape, device="cuda").index_add_(0, rows, out * share[:, None])
-        r = tg.norm_residual(h, y.to(h.dtype), w_post=self.w_post, w_pre=self.w_next,
-                             quantize=True)
-        logits = tg.gemm_fp8(r.x[-1:], r.scales[-1:], self.head_q, self.head_s)
-        return r.h, r.x, logits
+        out = tg.gemm_fp8_grouped(act, act_s, self.down_q, self.down_s, r.offsets)
+        y = tg.combine_rows(out, r.row_of, share)
+        n = tg.norm_residual(h, y, w_post=self.w_post, w_pre=self.w_next, quantize=True)
+        logits = tg.gemm_fp8(n.x[-1:], n.scales[-1:], self.head_q, self.head_s)
+        return n.h, n.x, logits
 
     def plain(self, h, top):
         """The same block with 16-bit weights in 32-bit arithmetic."""
