@@ -174,3 +174,17 @@ def test_binding_refuses_host_tensors():
             call()
     with pytest.raises(ValueError):
         tg.route_topk(logits, 2, score="relu")
+
+
+@pytest.mark.parametrize("source", ["gemm_w4.cu", "gemm_w4_many.cu"])
+def test_aligned_barriers_follow_a_reconvergence(source):
+    """bar.sync, bar.red and barrier.cluster.*.aligned need the lanes of a warp together:
+    right before each the warp is brought together."""
+    with open(os.path.join(_build.CSRC, source), encoding="utf-8") as f:
+        code = [line.split("//")[0].strip() for line in f]
+    code = [line for line in code if line]
+    at = [i for i, line in enumerate(code) if "cluster_sync" in line or "named_bar_" in line]
+    assert at
+    for i in at:
+        before = code[i - 3:i]
+        assert any("__syncwarp()" in b or "__syncthreads()" in b for b in before), code[i - 3:i + 1]

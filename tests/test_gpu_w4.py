@@ -149,6 +149,46 @@ def test_nan_stays_in_its_row(tg):
         assert not torch.isnan(d[keep.cuda()][:, :69]).any()
 
 
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [3, 12])
+def test_infinite_scales_where_k_ends_inside_a_block(tg, name, M):
+    """An infinite scale makes its row infinite (or NaN where the group's sum is zero), also
+    when the row's last scales are fewer than the k of a step."""
+    N, K, group = 40, 2208, 32
+    rng = np.random.default_rng(M)
+    codes, s, z = weights(rng, N, K, group, True, name)
+    a = torch.from_numpy(rng.integers(1, 5, (M, K))).to(TYPES[name]).cuda()
+    for g in range(K // group):
+        s[g % N, g] = float("inf")
+    d = tg.gemm_w4(a, *gpu(codes, s, z), group=group).double().cpu().numpy()
+    w = ref.weights_w4(codes, np.ones(s.shape), z, group)
+    x = a.double().cpu().numpy()
+    for n in range(N):
+        mine = [g for g in range(K // group) if g % N == n]
+        sums = [x[:, g * group:(g + 1) * group] @ w[n, g * group:(g + 1) * group] for g in mine]
+        want = np.sum([np.where(v == 0, np.nan, np.copysign(np.inf, v)) for v in sums], axis=0) \
+            if mine else None
+        assert want is None or np.array_equal(d[:, n], want, equal_nan=True), n
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (9, 128, 32), (33, 129, 96), (16, 127, 8224), (17, 300, 16384), (12, 4100, 1056),
+    (65, 20000, 160), (24, 1, 12320), (300, 257, 544), (10, 390, 2944)])
+@pytest.mark.parametrize("group,zeros,name", [(32, True, "bf16"), (64, True, "f16"),
+                                              (128, False, "f16"), (128, True, "bf16")])
+def test_more_than_eight_tokens(tg, M, N, K, group, zeros, name):
+    """Short and long K (split over CTAs, or no block of it for some warps), one to many
+    blocks of rows and of tokens, twice with one result."""
+    rng = np.random.default_rng(M * N + K)
+    codes, s, z = weights(rng, N, K, group, zeros, name)
+    a = torch.from_numpy(rng.normal(size=(M, K))).to(TYPES[name]).cuda()
+    b = gpu(codes, s, z)
+    d = tg.gemm_w4(a, *b, group=group)
+    check(d, a, codes, s, z, group, name)
+    assert torch.equal(d, tg.gemm_w4(a, *b, group=group))
+    tg.check()
+
+
 def test_unaligned_scales_and_results(tg):
     """Scales and results need the alignment of their elements only."""
     rng = np.random.default_rng(5)
