@@ -425,25 +425,25 @@ cudaError_t launch_cfg(const W4Args& a, const W4Device& dev, cudaStream_t stream
                          stream, 1, dev.pdl, p, dev.limit_ns, dev.err_word);
 }
 
-template <bool BF16, int GB>
-cudaError_t launch_groups(const W4Args& a, const W4Device& dev, cudaStream_t stream) {
-    return a.offsets ? launch_cfg<W4Cfg<BF16, GB, true>>(a, dev, stream)
-                     : launch_cfg<W4Cfg<BF16, GB, false>>(a, dev, stream);
-}
 template <bool BF16>
 cudaError_t launch_scales(const W4Args& a, const W4Device& dev, cudaStream_t stream) {
-    return a.group == 32   ? launch_groups<BF16, 1>(a, dev, stream)
-           : a.group == 64 ? launch_groups<BF16, 2>(a, dev, stream)
-                           : launch_groups<BF16, 4>(a, dev, stream);
+    return a.offsets         ? launch_cfg<W4Cfg<BF16, 1, true>>(a, dev, stream)
+           : a.group == 32   ? launch_cfg<W4Cfg<BF16, 1, false>>(a, dev, stream)
+           : a.group == 64   ? launch_cfg<W4Cfg<BF16, 2, false>>(a, dev, stream)
+                             : launch_cfg<W4Cfg<BF16, 4, false>>(a, dev, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_w4(const W4Args& a, bool bf16, const W4Device& dev, cudaStream_t stream) {
-    // Up to eight tokens (of a group, on average; more are taken in several units) here, more
-    // on tcgen05: N x K = 4096 x 4096, groups of 128, 6.9 us here and 8.1 there with 8 tokens,
-    // 9.4 and 8.2 with 12; 14336 x 4096, groups of 32, 15.7 and 22.5, 28.6 and 22.5.
-    if (ceil_div(a.M, a.offsets ? a.groups : 1) > 8) return launch_gemm_w4_many(a, bf16, dev, stream);
+    // Up to eight tokens here, more on tcgen05: N x K = 4096 x 4096, groups of 128, 6.9 us here
+    // and 8.1 there with 8 tokens, 9.4 and 8.2 with 12; 14336 x 4096, groups of 32, 15.7 and
+    // 22.5, 28.6 and 22.5.  By group of rows, with N x K = 4096 x 2048: scales of 32 k up to four
+    // rows on average (64 groups with 128 rows 76 and 89 us, 8 with 64 rows 30 and 24), of 64
+    // and 128 none (68 and 59, 65 and 52; 64 groups with 8 rows 19 and 18, 18 and 17).
+    const int64_t few = !a.offsets ? 8 : a.group == 32 ? 4 : 0;
+    if (ceil_div(a.M, a.offsets ? a.groups : 1) > few)
+        return launch_gemm_w4_many(a, bf16, dev, stream);
     return bf16 ? launch_scales<true>(a, dev, stream) : launch_scales<false>(a, dev, stream);
 }
 

@@ -12,7 +12,7 @@
 
 namespace tmagemm {
 
-// Products of more than eight tokens.
+// Products of more tokens, on tcgen05.
 cudaError_t launch_gemm_w4_many(const W4Args& a, bool bf16, const W4Device& dev,
                                 cudaStream_t stream);
 
