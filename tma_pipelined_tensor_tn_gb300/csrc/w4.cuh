@@ -34,14 +34,12 @@ struct Unit {
     int32_t n, m, g, rows, tokens;
 };
 
-// The units of a cluster, in order: token block by token block of each group, and row
-// block by row block of each.
+// Every `step`-th unit from `id` on, in order: token block by token block of each group, and
+// row block by row block of each.
 template <class C, class P>
 struct Units {
-    int32_t left, block, m, g;          // the next unit is a later one if block >= row_blocks
-    __device__ Units(const P& p, const W4Groups& groups) {
-        const int32_t id = static_cast<int32_t>(blockIdx.x) / C::clusters(p);
-        const int32_t step = static_cast<int32_t>(gridDim.x) / C::clusters(p);
+    int32_t left, step, block, m, g;    // the next unit is a later one if block >= row_blocks
+    __device__ Units(const P& p, const W4Groups& groups, int32_t id, int32_t every) : step(every) {
         const int32_t chunks =
             C::kGrouped ? groups.chunks : (p.a.M + C::kTokens - 1) / C::kTokens;
         const int64_t all = static_cast<int64_t>(chunks) * p.row_blocks;
@@ -69,7 +67,7 @@ struct Units {
         }
         const Unit t{block * p.box, m, g, min(p.box, p.a.N - block * p.box),
                      min(C::kTokens, end - m)};
-        block += static_cast<int32_t>(gridDim.x) / C::clusters(p);
+        block += step;
         --left;
         return t;
     }
