@@ -82,6 +82,15 @@ def test_rows_by_expert(tg, T, k, E, C, kind, name, quantize):
         assert r.scales is None and same_bytes(r.rows[:n], x[token])
 
 
+@pytest.mark.parametrize("T,k,E,C", [
+    (256, 1, 9, 8), (257, 1, 512, 8), (8192, 1, 3, 8), (1025, 8, 33, 8), (5000, 4, 512, 16),
+    (4100, 8, 64, 8), (8190, 8, 7, 8), (4096, 32, 500, 8), (4097, 32, 300, 8)])
+@pytest.mark.parametrize("kind", ["some", "one", "padded"])
+def test_many_slots(tg, T, k, E, C, kind):
+    """As many as each way of placing them takes."""
+    test_rows_by_expert(tg, T, k, E, C, kind, "bf16", False)
+
+
 def test_codes_against_the_reference(tg):
     x = random((20, 272), "bf16") * torch.logspace(-6, 6, 20, device="cuda").bfloat16()[:, None]
     x[3] = 0

@@ -2,14 +2,15 @@
 //
 // Slot t k + j (choice j of token t) gets the row  offsets[expert] + slots of the same
 // expert before it: a counting sort, stable and without atomics whose order could
-// change it.  Up to 768 slots every CTA sorts them all for itself and copies its tokens:
-// one launch, whose first loads travel while it sorts.  More slots are cut into
-// chunks, a CTA each: count_kernel counts each chunk's slots by expert, place_kernel adds
-// up the chunks before its own and ranks its slots warp by warp, and the rows
-// are copied by a third kernel.  Each token is read once and written to all of its rows.
+// change it.  Up to 256 slots every CTA sorts them all for itself and copies its tokens:
+// one launch, whose first loads travel while it sorts.  Up to 131072 slots are sorted by one
+// cluster, which holds them in registers; more are cut into chunks, a CTA each: count_kernel
+// counts each chunk's slots by expert, place_kernel adds up the chunks before its own and
+// ranks its slots warp by warp.  Then the rows are copied by another kernel.  Each token is
+// read once and written to all of its rows.
 //
 // The copies and sums are bound by memory: 4099 x 4096 FP16 tokens to 8 rows of codes each
-// 31 us (172 MB), and 8 us before them to place the slots; the sums of 8 rows of 8192 x 2048 BF16
+// 31 us (172 MB), and 5 us before them to place the slots; the sums of 8 rows of 8192 x 2048 BF16
 // 46.7 us (6.5 TB/s), their gradients 87 (6.5 TB/s).  Writes alone run slower than copies, at
 // 3.8 to 5 TB/s.  16 tokens of 4096 columns to 4 rows each take 3.2 us, their sums 1.8.
 #include <cuda_bf16.h>
@@ -57,6 +58,25 @@ struct Places {
     int32_t warp_total[kWarps];
 };
 
+// The lanes of the same expert, N times, a bit of the ids at a time (a match instruction
+// takes several times as long); ids outside the experts become E.
+template <int N>
+__device__ __forceinline__ void same_expert(int32_t (&e)[N], uint32_t (&same)[N], int32_t E) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        if (static_cast<uint32_t>(e[u]) >= static_cast<uint32_t>(E)) e[u] = E;
+        same[u] = kAll;
+    }
+#pragma unroll 1
+    for (int i = 0; E >> i != 0; ++i)
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const bool bit = (e[u] >> i & 1) != 0;
+            const uint32_t set = __ballot_sync(kAll, bit);
+            same[u] &= bit ? set : ~set;
+        }
+}
+
 // From totals (and slots in the chunks before) by expert: offsets, and the row of each slot
 // of this chunk, slots s0 .. s1 - 1, left in rows[slot].  All threads; `len` is the slots of
 // a warp, a multiple of 32.
@@ -93,15 +113,16 @@ __device__ __forceinline__ void place(Places& m, const int32_t* ids, int32_t* of
         int32_t e[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) e[u] = expert(s + 32 * u);
+        uint32_t same[kAhead];
+        same_expert(e, same, E);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (s - lane + 32 * u >= w1) break;
-            const bool have = static_cast<uint32_t>(e[u]) < static_cast<uint32_t>(E);
-            const uint32_t same = __match_any_sync(kAll, have ? e[u] : -1);
+            const bool have = e[u] < E;
             int32_t row = 0;
-            if (have) row = m.next[warp][e[u]] + __popc(same & ((1u << lane) - 1u));
+            if (have) row = m.next[warp][e[u]] + __popc(same[u] & ((1u << lane) - 1u));
             __syncwarp();
-            if (have && lane == __ffs(same) - 1) m.next[warp][e[u]] += __popc(same);
+            if (have && lane == __ffs(same[u]) - 1) m.next[warp][e[u]] = row + __popc(same[u]);
             __syncwarp();
             if (s + 32 * u < w1) rows[s + 32 * u] = row;
         }
@@ -154,6 +175,101 @@ place_kernel(const int32_t* ids, const int32_t* counts, int32_t* offsets, int32_
     const int64_t s0 = static_cast<int64_t>(blockIdx.x) * chunk;
     place(m, ids, blockIdx.x == 0 ? offsets : nullptr, row_of, s0, min(s0 + chunk, slots),
           chunk / kWarps, E);
+}
+
+// All of it in one launch of one cluster: a warp has BATCHES times 32 slots, ranked in
+// registers; the counts of the CTAs meet through distributed shared memory.
+// (64 columns, with the copies: 8192 slots 4.7 us, in chunks 6.9; 32792 8.1 and 11.4; 131072
+// 17.0 and 18.9.)
+constexpr int kClusterSlots = 131072;
+constexpr int kClusterCtas = 8, kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+template <int BATCHES>
+__global__ void __launch_bounds__(kClusterThreads)
+place_cluster_kernel(const int32_t* ids, int32_t* offsets, int32_t* row_of, int32_t slots,
+                     int32_t E) {
+    __shared__ uint16_t next[kClusterWarps][kMaxExperts];   // slots of each warp, then before it
+    __shared__ int32_t count[kMaxExperts], first[kMaxExperts], warp_total[kMaxExperts / 32];
+    grid_launch_dependents();
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_ctarank();
+    for (int e = lane; e < E; e += 32) next[warp][e] = 0;
+    __syncwarp();
+    grid_dependency_wait();
+    const int32_t s0 =
+        (static_cast<int32_t>(rank) * kClusterWarps + warp) * (32 * BATCHES) + lane;
+    int32_t e[BATCHES];
+#pragma unroll
+    for (int b = 0; b < BATCHES; ++b) e[b] = s0 + 32 * b < slots ? ids[s0 + 32 * b] : -1;
+    // The expert and the slots of this warp before it with the same, in the two halves.
+    uint32_t place[BATCHES];
+    uint32_t same[BATCHES];
+    same_expert(e, same, E);
+#pragma unroll
+    for (int b = 0; b < BATCHES; ++b) {
+        const bool have = e[b] < E;
+        uint32_t before = 0;
+        if (have) before = next[warp][e[b]] + __popc(same[b] & ((1u << lane) - 1u));
+        __syncwarp();
+        if (have && lane == __ffs(same[b]) - 1)
+            next[warp][e[b]] = static_cast<uint16_t>(before + __popc(same[b]));
+        __syncwarp();
+        place[b] = have ? static_cast<uint32_t>(e[b]) << 16 | before : ~0u;
+    }
+    __syncthreads();
+    if (tid < E) {
+        uint32_t sum = 0;
+#pragma unroll 16
+        for (int w = 0; w < kClusterWarps; ++w) {
+            const uint32_t n = next[w][tid];
+            next[w][tid] = static_cast<uint16_t>(sum);
+            sum += n;
+        }
+        count[tid] = static_cast<int32_t>(sum);
+    }
+    __syncwarp();
+    cluster_sync();
+    int32_t total = 0, before = 0;
+    if (tid < E) {
+#pragma unroll
+        for (uint32_t q = 0; q < kClusterCtas; ++q) {
+            int32_t n;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                         : "=r"(n)
+                         : "r"(map_to_rank(smem_u32(&count[tid]), q))
+                         : "memory");
+            total += n;
+            if (q < rank) before += n;
+        }
+    }
+    __syncwarp();
+    cluster_arrive_release();             // this CTA has read its peers' counts
+    int32_t upto = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int32_t v = __shfl_up_sync(kAll, upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 31 && warp < kMaxExperts / 32) warp_total[warp] = upto;
+    __syncthreads();
+    if (tid < E) {
+        for (int w = 0; w < warp; ++w) upto += warp_total[w];
+        first[tid] = upto - total + before;
+        if (rank == 0) {
+            offsets[tid] = upto - total;
+            if (tid == E - 1) offsets[E] = upto;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < BATCHES; ++b) {
+        const int32_t at = static_cast<int32_t>(place[b] >> 16);
+        if (s0 + 32 * b < slots)
+            row_of[s0 + 32 * b] =
+                place[b] == ~0u ? -1
+                                : first[at] + next[warp][at] + static_cast<int32_t>(place[b] & 0xffffu);
+    }
+    __syncwarp();
+    cluster_wait_acquire();
 }
 
 // ------------------------------------------------------------------- rows ----
@@ -241,7 +357,9 @@ __device__ __forceinline__ void spread(const Spread& to, const Piece& p, int32_t
 }
 
 // All of it for up to kSmallSlots slots.
-constexpr int kSmallSlots = 768;
+// (4096 columns, 64 experts: 64 slots 3.6 us, placed by a launch before 4.1; 256 slots 4.2 and
+// 4.1, 768 7.3 and 4.8.)
+constexpr int kSmallSlots = 256;
 template <bool BF16, bool QUANTIZE>
 __global__ void __launch_bounds__(kThreads)
 small_dispatch_kernel(const uint4* x, const int32_t* ids, int32_t* offsets, int32_t* row_of,
@@ -433,6 +551,30 @@ unsigned grid_for(int64_t items) {
     return static_cast<unsigned>(ctas < (1 << 30) ? ctas : (1 << 30));
 }
 
+cudaError_t launch_places(const DispatchArgs& a, int64_t slots, bool pdl, cudaStream_t stream) {
+    if (slots <= kClusterSlots) {
+        const int32_t batches =
+            static_cast<int32_t>(ceil_div(slots, kClusterCtas * kClusterThreads));
+        auto kernel = batches <= 1   ? place_cluster_kernel<1>
+                      : batches <= 2 ? place_cluster_kernel<2>
+                      : batches <= 3 ? place_cluster_kernel<3>
+                      : batches <= 5 ? place_cluster_kernel<5>
+                      : batches <= 8 ? place_cluster_kernel<8>
+                                     : place_cluster_kernel<16>;
+        return launch_kernel(kernel, dim3(kClusterCtas), dim3(kClusterThreads), 0, stream,
+                             static_cast<unsigned>(kClusterCtas), pdl, a.ids, a.offsets, a.row_of,
+                             static_cast<int32_t>(slots), a.E);
+    }
+    const int32_t chunk = chunk_slots(slots);
+    const int32_t chunks = static_cast<int32_t>(ceil_div(slots, chunk));
+    if (cudaError_t e = launch_kernel(count_kernel, dim3(chunks), dim3(kThreads), 0, stream, 1u,
+                                      pdl, a.ids, a.counts, slots, chunk, a.E))
+        return e;
+    return launch_kernel(place_kernel, dim3(chunks), dim3(kThreads), 0, stream, 1u, pdl, a.ids,
+                         static_cast<const int32_t*>(a.counts), a.offsets, a.row_of, slots, chunk,
+                         chunks, a.E);
+}
+
 template <bool BF16, bool QUANTIZE>
 cudaError_t launch_dispatch_typed(const DispatchArgs& a, int sms, bool pdl, cudaStream_t stream) {
     const int64_t slots = a.T * a.k;
@@ -444,15 +586,7 @@ cudaError_t launch_dispatch_typed(const DispatchArgs& a, int sms, bool pdl, cuda
                              dim3(kThreads), 0, stream, 1u, pdl, a.x, a.ids, a.offsets, a.row_of,
                              to, static_cast<int32_t>(a.T), a.k, a.E, a.C8);
     }
-    const int32_t chunk = chunk_slots(slots);
-    const int32_t chunks = static_cast<int32_t>(ceil_div(slots, chunk));
-    cudaError_t e = launch_kernel(count_kernel, dim3(chunks), dim3(kThreads), 0, stream, 1u, pdl,
-                                  a.ids, a.counts, slots, chunk, a.E);
-    if (e != cudaSuccess) return e;
-    e = launch_kernel(place_kernel, dim3(chunks), dim3(kThreads), 0, stream, 1u, pdl, a.ids,
-                      static_cast<const int32_t*>(a.counts), a.offsets, a.row_of, slots, chunk,
-                      chunks, a.E);
-    if (e != cudaSuccess) return e;
+    if (cudaError_t e = launch_places(a, slots, pdl, stream)) return e;
     constexpr int kVecs = 4;
     const bool wide = a.T * ceil_div(a.C8, 32 * kVecs) >= 16ll * sms;
     auto kernel = wide ? spread_rows_kernel<BF16, QUANTIZE, kVecs>
@@ -465,7 +599,7 @@ cudaError_t launch_dispatch_typed(const DispatchArgs& a, int sms, bool pdl, cuda
 }  // namespace
 
 int64_t dispatch_workspace(int64_t slots, int64_t E) {
-    if (slots <= kSmallSlots) return 0;
+    if (slots <= kClusterSlots) return 0;
     return ceil_div(ceil_div(slots, chunk_slots(slots)) * E * 4, 16) * 16;
 }
 
