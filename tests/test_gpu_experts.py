@@ -95,6 +95,39 @@ def test_decoding_with_4_bit_experts(tg, T):
         assert np.all(np.abs(y[t] - total) <= bound + 2.0 ** -8 * (np.abs(total) + bound))
 
 
+def test_calls_on_two_streams_at_once(tg):
+    """Calls that overlap on the GPU, of the same and of other operators, as one by one."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    T, E, k, C, N = 3000, 16, 4, 512, 1000
+    x = torch.randn((2, T, C), device="cuda", generator=g).half()
+    logits = torch.randn((2, T, E), device="cuda", generator=g)
+    B = torch.randint(0, 256, (E, N, C // 2), device="cuda", generator=g).to(torch.uint8)
+    S = torch.rand((E, N, C // 64), device="cuda", generator=g).half()
+
+    def layer(i, few):
+        n = 40 if few else T
+        ids, w = tg.route_topk(logits[i, :n], k)
+        r = tg.dispatch_rows(x[i, :n], ids, E)
+        out = tg.gemm_w4_grouped(r.rows, B, S, r.offsets, group=64)
+        return tg.combine_rows(out, r.row_of, w), tg.gemm_w4(x[i, :9 if few else 3], B[i], S[i],
+                                                             group=64)
+
+    want = [[layer(i, few) for few in (False, True)] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append([layer(i, few) for few in (False, True)])
+    torch.cuda.synchronize()
+    tg.check()
+    for i in range(2):
+        for once in got[i]:
+            for (y, d), (y0, d0) in zip(once, want[i]):
+                assert torch.equal(y, y0) and torch.equal(d, d0)
+
+
 def test_first_calls_inside_a_capture(tg, tmp_path):
     """What the kernels ask of the device once is asked while a graph is captured."""
     import subprocess
