@@ -123,6 +123,22 @@ def test_values_that_32_bits_cannot_tell_apart(tg, score, groups, top_groups):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,groups", [(64, 8), (512, 8), (512, 32)])
+def test_equal_values_across_groups(tg, score, biased, E, groups):
+    """Logits of a few values only: groups whose best are equal, and more equal experts in a
+    group than count for its value; with biases of two values, and next to each other's."""
+    g = torch.Generator().manual_seed(E + groups)
+    logits = torch.randint(0, 3, (300, E), generator=g).float()
+    logits[100:200] *= 2.0 ** -22       # next to each other's in FP32
+    logits[200:] = 14 + logits[200:] / 8     # sigmoid: the same FP32 score
+    bias = 2.0 ** -24 * torch.randint(0, 2, (E,), generator=g).float() if biased else None
+    for kind in (logits, logits.bfloat16()):
+        check(tg, kind.cuda(), 6, score=score, bias=None if bias is None else bias.cuda(),
+              groups=groups, top_groups=groups // 2, group_sum=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("group_sum,top_groups", [(0, 0), (1, 3), (2, 3), (2, 5)])
 def test_pairs_that_32_bits_cannot_tell_apart(tg, score, group_sum, top_groups):
     """Runs of eight experts in pairs whose values are equal to FP32 rounding, one run far

@@ -293,19 +293,33 @@ __device__ __noinline__ bool group_value64(const RouteArgs& a, const LaneExperts
     for (int j = 0; j < V; ++j)
         if (key[j] == best) i1 = min(i1, at.first + j);
     for (int d = 1; d < at.lanes; d <<= 1) i1 = min(i1, __shfl_xor_sync(kAll, i1, d));
-    uint32_t third = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j)
         if (key[j] == second && at.first + j != i1) i2 = min(i2, at.first + j);
     for (int d = 1; d < at.lanes; d <<= 1) i2 = min(i2, __shfl_xor_sync(kAll, i2, d));
+    const double sum = a.score == kScoreSoftmax ? sum64<TYPE>(a, row, lane, m) : 1.0;
+    // Those left out are below the last of those counted, or equal to it (as in 16 bits they
+    // often are) where the other one counted is above or equal too.
+    const int32_t last = a.group_sum == 2 ? i2 : i1;
+    const uint32_t in = a.group_sum == 2 ? second : best;
+    const auto below = [&](uint32_t lower, uint32_t upper) {
+        const float x = key_value(upper), y = key_value(lower);
+        return x - y > near + 0x1p-22f * (fabsf(x) + fabsf(y));
+    };
+    const auto equal = [&](int32_t e) {
+        return load_logit<TYPE>(a.logits, row + e) == load_logit<TYPE>(a.logits, row + last) &&
+               (!a.bias || a.bias[e] == a.bias[last]);
+    };
+    uint32_t others = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        if (at.first + j != i1 && at.first + j != i2) third = max(third, key[j]);
-    const double sum = a.score == kScoreSoftmax ? sum64<TYPE>(a, row, lane, m) : 1.0;
-    // (The closest of those left out to the last of those counted.)
-    const uint32_t in = a.group_sum == 2 ? second : best, next = a.group_sum == 2 ? third : second;
-    const float x = key_value(in), y = key_value(next);
-    const bool clear = next == 0 || x - y > near + 0x1p-22f * (fabsf(x) + fabsf(y));
+        if (key[j] != 0 && in != 0 && at.first + j != i1 && at.first + j != last && !below(key[j], in))
+            others |= 1u << j;
+    bool clear = true;
+    for (; others != 0; others &= others - 1)
+        clear = clear && equal(at.first + __ffs(others) - 1) &&
+                (i1 == last || below(in, best) || equal(i1));
+    __syncwarp();
     value = 0;
     if (best != 0 && at.group < a.groups) {
         double v = value64<TYPE>(a, row, i1, m, sum);
