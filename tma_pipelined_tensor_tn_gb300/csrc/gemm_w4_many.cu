@@ -176,6 +176,9 @@ __device__ __forceinline__ void add_sums(Worker<C>& w, uint32_t at, const float 
         tmem_ld_32x32b_x16(at + j * C::NT, lo);
         if (tokens > 16) tmem_ld_32x32b_x16(at + j * C::NT + 16, hi);
         tmem_ld_wait();
+        // (Nothing that uses them comes earlier.)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(lo[e]), "+r"(hi[e]));
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             w.acc[e] = fmaf(__uint_as_float(lo[e]), scale[j], w.acc[e]);
