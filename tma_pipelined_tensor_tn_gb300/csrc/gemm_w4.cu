@@ -3,8 +3,7 @@
 //
 // q - z is a whole number of five bits, exact in 16 bits, so the inner sums run on
 // mma.sync with FP32 accumulators and the scale is applied to a whole group's sum in
-// FP32.  (With eight tokens tcgen05 would do sixteen columns' work on weights that have to
-// be widened into TMEM first; from nine on that is faster, in gemm_w4_many.cu.)
+// FP32.  (gemm_w4_many.cu has more tokens, groups of rows, and many rows of weights.)
 //
 // A unit is a block of weight rows and up to eight tokens.  The warps of a CTA are WR along
 // the rows, 16 MT each, and WK along K, 128 k of a stage each.  One thread keeps a ring of
@@ -436,11 +435,14 @@ cudaError_t launch_scales(const W4Args& a, const W4Device& dev, cudaStream_t str
 cudaError_t launch_gemm_w4(const W4Args& a, bool bf16, const W4Device& dev, cudaStream_t stream) {
     // Up to eight tokens here, more on tcgen05: N x K = 4096 x 4096, groups of 128, 6.9 us here
     // and 8.1 there with 8 tokens, 9.4 and 8.2 with 12; 14336 x 4096, groups of 32, 15.7 and
-    // 22.5, 28.6 and 22.5.  By group of rows, with N x K = 4096 x 2048: scales of 32 k up to two
-    // rows on average (64 groups with two each 91 and 100 us, with 256 rows in 50 of them 115
-    // and 100), of 64 and 128 none (64 groups, 128 rows: 68 and 44, 65 and 43; 8 rows 19 and
-    // 18, 18 and 16).
-    const int64_t few = !a.offsets ? 8 : a.group == 32 ? 2 : 0;
+    // 22.5, 28.6 and 22.5.  With groups of 128, whose sums are read back least, there too where
+    // its blocks of 128 rows take more than half the SMs: one token, 8192 x 4096 9.5 and 11.2,
+    // 11008 x 4096 13.4 and 11.3, 19456 x 4096 15.3 and 13.0, 28672 x 8192 35.6 and 35.9.
+    // By group of rows, with N x K = 4096 x 2048: scales of 32 k up to two rows on average (64
+    // groups with two each 91 and 100 us, with 256 rows in 50 of them 115 and 100), of 64 and
+    // 128 none (64 groups, 128 rows: 68 and 44, 65 and 43; 8 rows 19 and 18, 18 and 16).
+    const bool wide = a.group == 128 && 2 * ceil_div(a.N, 128) > dev.sms;
+    const int64_t few = a.offsets ? (a.group == 32 ? 2 : 0) : wide ? 0 : 8;
     if (ceil_div(a.M, a.offsets ? a.groups : 1) > few)
         return launch_gemm_w4_many(a, bf16, dev, stream);
     return bf16 ? launch_scales<true>(a, dev, stream) : launch_scales<false>(a, dev, stream);
