@@ -1,0 +1,97 @@
+"""GPU tests of route_topk's order where FP32 cannot tell values apart: the ids are those of
+64 bits."""
+import numpy as np
+import pytest
+
+from tests import experts_reference as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def tg():
+    import tma_pipelined_tensor_tn_gb300 as m
+    m.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return m
+
+
+def ordered(values, count):
+    """The lowest indices of the largest values that are not None, largest first."""
+    open_ = [i for i, v in enumerate(values) if v is not None]
+    return sorted(open_, key=lambda i: (-values[i], i))[:count]
+
+
+def choose(logits, values, k, groups=1, top_groups=1, group_sum=1):
+    """ids (T, k) by float64 values; a logit of -inf closes, a value of -inf does not."""
+    T, E = logits.shape
+    ids, size = np.full((T, k), -1), E // groups
+    for t in range(T):
+        v = [None if np.isneginf(l) else float(x) for l, x in zip(logits[t], values[t])]
+        if groups > 1:
+            sums = []
+            for g in range(groups):
+                part = v[g * size:(g + 1) * size]
+                best = ordered(part, group_sum)
+                sums.append(sum(part[i] for i in best) if best else None)
+            keep = ordered(sums, top_groups)
+            v = [x if e // size in keep else None for e, x in enumerate(v)]
+        best = ordered(v, k)
+        ids[t, :len(best)] = best
+    return ids
+
+
+def check(tg, logits, k, score, bias, values=None, **groups):
+    """The ids against those of 64 bits (or by the values given), and the weights."""
+    l = logits.double().cpu().numpy()
+    if values is None:
+        values = ref.scores(l, score) + (0.0 if bias is None else bias.double().cpu().numpy())
+    want = choose(l, values, k, **groups)
+    r = tg.route_topk(logits, k, score=score, bias=bias, **groups)
+    ids = r.ids.cpu().numpy()
+    assert np.array_equal(ids, want), np.flatnonzero((ids != want).any(axis=1))[:10]
+    have = want >= 0
+    c = np.where(have, np.take_along_axis(ref.scores(l, score), np.maximum(want, 0), axis=1), 0.0)
+    # (Scores of these tests are far from the smallest numbers; the bound is that of
+    # test_gpu_route.py with logits up to 100 apart.)
+    share = c / np.where(have.any(axis=1), c.sum(axis=1), 1.0)[:, None]
+    assert np.all(np.abs(r.weights.double().cpu().numpy() - share) <= 300 * 2.0 ** -24 * share)
+
+
+# ------------------------------------------- ties in front of a larger value ----
+
+@pytest.mark.parametrize("score,logits,bias,k,expect", [
+    ("sigmoid", (20.0, 20.0, 21.0, -5.0), 0.0, 1, [2]),
+    ("sigmoid", (-17.0, -17.0, -16.5, -20.0), 0.5, 1, [2]),
+    ("sigmoid", (20.0, 20.0, 20.0, 20.0, 21.0, 20.5), 0.0, 2, [4, 5]),
+    ("sigmoid", (30.0, 20.0, 20.0, 20.0, 21.0, 30.0), 0.0, 3, [0, 5, 4]),
+    ("softmax", (0.0, -17.0, -17.0, -16.5, -20.0), 0.5, 2, [0, 3]),
+    ("softmax", (0.0, -17.0, -17.0, -17.0, -16.5, -16.0), 0.5, 3, [0, 5, 4])])
+def test_ties_across_the_last_choice(tg, score, logits, bias, k, expect):
+    """The k-th and the next are equal, and one behind them is larger by less than FP32
+    shows."""
+    l = torch.tensor([logits], device="cuda")
+    b = torch.full((len(logits),), bias, device="cuda")
+    assert tg.route_topk(l, k, score=score, bias=b).ids.tolist() == [expect]
+    check(tg, l, k, score, b)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups", [(6, 1, 1), (20, 1, 1), (64, 1, 1), (64, 8, 3),
+                                                 (330, 1, 1)])
+@pytest.mark.parametrize("k", [1, 2, 5])
+def test_runs_of_ties(tg, score, E, groups, top_groups, k):
+    """Logits of a few values whose scores FP32 cannot tell apart next to the bias."""
+    g = torch.Generator().manual_seed(E + k)
+    logits = -17.0 + 0.25 * torch.randint(0, 6, (400, E), generator=g).float()
+    logits[200:, ::7] = -1.0           # a few that stand out
+    if score == "softmax":
+        logits[:, 3] = 0.0             # so that the others stay small
+    bias = torch.full((E,), 0.5)
+    bias[E // 2] += 2.0 ** -24
+    kw = dict(groups=groups, top_groups=top_groups, group_sum=1) if groups > 1 else {}
+    for kind in (logits, logits.bfloat16()):
+        check(tg, kind.cuda(), k, score, bias.cuda(), **kw)

@@ -281,6 +281,27 @@ __device__ __noinline__ int32_t choose64(const RouteArgs& a, int64_t row, int la
     return id;
 }
 
+// The ids of the first `count` lanes in the order of their values in FP64.
+template <int TYPE>
+__device__ __noinline__ int32_t order64(const RouteArgs& a, int64_t row, int lane, float m,
+                                        int32_t id, int count) {
+    const double sum = a.score == kScoreSoftmax ? sum64<TYPE>(a, row, lane, m) : 1.0;
+    const uint64_t exact = id >= 0 ? order_key(value64<TYPE>(a, row, id, m, sum)) : 0ull;
+    int rank = 0;
+    for (int i = 0; i < count; ++i) {
+        const uint64_t other = __shfl_sync(kAll, exact, i);
+        const int32_t oid = __shfl_sync(kAll, id, i);
+        rank += other > exact || (other == exact && oid < id);
+    }
+    int32_t placed = -1;
+    for (int i = 0; i < count; ++i) {
+        const int r = __shfl_sync(kAll, rank, i);
+        const int32_t oid = __shfl_sync(kAll, id, i);
+        if (r == lane) placed = oid;
+    }
+    return placed;
+}
+
 // The exact value of a lane's group from its two best experts (by FP32 keys), or false where
 // a third is too close to them to say which the two are.
 template <int TYPE, int V>
@@ -510,33 +531,21 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_cons
         float logit = -kInf;
         if (id >= 0) logit = load_logit<TYPE>(a.logits, row + id);
         if (!by_logits) {
-            // Neighbours too close to order (experts with the same logit and bias are ties).
+            // Neighbours too close to order, the first of them a choice, or a tie of the last
+            // choice (experts with the same logit and bias are ties, in order as they are).
             const float x = key_value(mine), y = __shfl_down_sync(kAll, x, 1);
             const float b = id >= 0 && a.bias ? a.bias[id] : 0.0f;
             const float next_logit = __shfl_down_sync(kAll, logit, 1);
             const float next_b = __shfl_down_sync(kAll, b, 1);
-            const bool same = next_logit == logit && next_b == b;
-            const bool doubt = lane < a.k && lane + 1 < count && !same &&
-                               !(x - y > near + 0x1p-22f * (fabsf(x) + fabsf(y)));
+            const bool pair = lane + 1 < count, same = next_logit == logit && next_b == b;
+            const bool doubt = pair && !same && !(x - y > near + 0x1p-22f * (fabsf(x) + fabsf(y)));
+            // (Lane 31 is no tie: there is one that is not.)
+            const int last_tie =
+                a.k - 2 + __ffs(~__ballot_sync(kAll, pair && same) >> (a.k - 1));
             if (whole) {
                 id = choose64<TYPE, V>(a, row, lane, m, c.sorted_id);
-            } else if (__any_sync(kAll, doubt)) {
-                const double sum = softmax ? sum64<TYPE>(a, row, lane, m) : 1.0;
-                const uint64_t exact =
-                    id >= 0 ? order_key(value64<TYPE>(a, row, id, m, sum)) : 0ull;
-                int rank = 0;
-                for (int i = 0; i < count; ++i) {
-                    const uint64_t other = __shfl_sync(kAll, exact, i);
-                    const int32_t oid = __shfl_sync(kAll, id, i);
-                    rank += other > exact || (other == exact && oid < id);
-                }
-                int32_t placed = -1;
-                for (int i = 0; i < count; ++i) {
-                    const int r = __shfl_sync(kAll, rank, i);
-                    const int32_t oid = __shfl_sync(kAll, id, i);
-                    if (r == lane) placed = oid;
-                }
-                id = placed;
+            } else if (__any_sync(kAll, doubt && lane <= last_tie)) {
+                id = order64<TYPE>(a, row, lane, m, id, count);
             }
             if (id >= 0) logit = load_logit<TYPE>(a.logits, row + id);
         }
