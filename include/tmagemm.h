@@ -433,7 +433,8 @@ int64_t norm_residual_backward_workspace_size(int64_t T, int64_t C);
  * and weight 0.  NaN ranks above every number and shows in the weights.
  *   type    : of the logits, 0 fp16, 1 bf16, 2 FP32.
  *   score   : 0 softmax, 1 sigmoid.
- *   bias    : E floats, or NULL for none.
+ *   bias    : E floats, or NULL for none.  Experts at +inf come before all others and
+ *             those at -inf after them (open all the same), in the order of their indices.
  * The backward takes logits, ids, dweights (the gradient of the weights), score,
  * renormalize and scale, and writes dlogits (T x E, in the logits' type) with the
  * choice held fixed; bias and groups are not read.  ids outside 0 .. E - 1 have no

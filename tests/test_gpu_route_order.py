@@ -1,5 +1,7 @@
-"""GPU tests of route_topk's order where FP32 cannot tell values apart: the ids are those of
-64 bits."""
+"""GPU tests of route_topk's order where FP32 cannot tell values apart and where they are
+infinite: the ids are those of 64 bits."""
+import itertools
+
 import numpy as np
 import pytest
 
@@ -95,3 +97,37 @@ def test_runs_of_ties(tg, score, E, groups, top_groups, k):
     kw = dict(groups=groups, top_groups=top_groups, group_sum=1) if groups > 1 else {}
     for kind in (logits, logits.bfloat16()):
         check(tg, kind.cuda(), k, score, bias.cuda(), **kw)
+
+
+# ------------------------------------------------------------ infinite biases ----
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k,forced", [(1, 1), (1, 5), (4, 1), (4, 3), (4, 4), (4, 5), (4, 40),
+                                      (8, 64), (32, 33), (32, 32)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_biases(tg, score, k, forced, sign):
+    """+inf on fewer than, exactly and more than k experts puts these first, -inf on any
+    number of them last, in the order of their indices."""
+    E, rng = 64, np.random.default_rng(k + forced)
+    logits = torch.from_numpy(rng.normal(size=(20, E))).float().cuda()
+    logits[3, 1:] = -INF
+    bias = torch.from_numpy(0.1 * rng.normal(size=E)).float()
+    bias[torch.from_numpy(rng.permutation(E)[:forced])] = sign * INF
+    for group in ({}, dict(groups=8, top_groups=4, group_sum=1)):
+        check(tg, logits, k, score, bias.cuda(), **group)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_sum", [1, 2])
+def test_infinite_biases_of_some_groups(tg, score, group_sum):
+    """Groups with one, two or only experts at +inf or at -inf (never both in one)."""
+    E, rng = 48, np.random.default_rng(group_sum)
+    logits = torch.from_numpy(rng.normal(size=(50, E))).float().cuda()
+    for high, low in itertools.product(((), (7,), (7, 9), (40, 41, 42), (7, 21, 40)),
+                                       ((), (25,), tuple(range(24, 32)), tuple(range(25, 32)))):
+        bias = 0.1 * torch.from_numpy(rng.normal(size=E)).float()
+        bias[list(high)] = INF
+        bias[list(low)] = -INF
+        for top_groups in (1, 2, 5):
+            check(tg, logits, 4, score, bias.cuda(), groups=6, top_groups=top_groups,
+                  group_sum=group_sum)

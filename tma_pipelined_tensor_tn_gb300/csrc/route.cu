@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_cons
         bound = __shfl_sync(kAll, sort_lanes(bound, lane), a.k - 1);
         if (!by_logits && bound != 0) {
             const float v = key_value(bound);
-            bound = order_key(v - (near + 0x1p-20f * fabsf(v)));
+            // (An infinite one is what it is.)
+            if (fabsf(v) < kInf) bound = order_key(v - (near + 0x1p-20f * fabsf(v)));
             whole |= near != near;       // (a softmax with a NaN)
         }
         bound = max(bound, 1u);
