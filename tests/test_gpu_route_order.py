@@ -131,3 +131,31 @@ def test_infinite_biases_of_some_groups(tg, score, group_sum):
         for top_groups in (1, 2, 5):
             check(tg, logits, 4, score, bias.cuda(), groups=6, top_groups=top_groups,
                   group_sum=group_sum)
+
+
+# --------------------------------------------- groups whose two best cancel out ----
+
+def test_sum_that_cancels(tg):
+    l = torch.tensor([[1.4e-5, 0.0, 1.65e-5, -1.4e-5]], device="cuda")
+    b = torch.tensor([100.0, -100.0, 100.0, -100.0], device="cuda")
+    kw = dict(groups=2, top_groups=1, group_sum=2)
+    assert tg.route_topk(l, 1, score="sigmoid", bias=b, **kw).ids.tolist() == [[0]]
+    check(tg, l, 1, "sigmoid", b, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [1.0, 32.0, 100.0, 1000.0])
+@pytest.mark.parametrize("E,groups", [(16, 4), (512, 8), (256, 32)])
+def test_group_sums_of_opposite_biases(tg, score, size, E, groups):
+    """The two best of each group have biases of +-size, so that the groups' sums hold the
+    scores' differences and the rounding of the biases' size: a few 1e-6 apart."""
+    T, g = 300, torch.Generator().manual_seed(E)
+    per = E // groups
+    logits = 1e-5 * torch.randn((T, E), generator=g)
+    if score == "softmax":
+        logits *= E                    # scores of 1 / E: the same differences
+    bias = torch.full((E,), -4.0 * size)
+    bias[0::per], bias[per - 1::per] = size, -size
+    for top_groups in (1, groups // 2):
+        check(tg, logits.cuda(), 2, score, bias.cuda(), groups=groups, top_groups=top_groups,
+              group_sum=2)

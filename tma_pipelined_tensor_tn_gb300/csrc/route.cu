@@ -460,9 +460,17 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < V; ++j) open[j] = key[j];
             close_groups<V>(a, at, value, key, worst, out);
+            // Each value is rounded by 2^-24 of itself and of the one or two that it adds up,
+            // which may cancel out: by 2^-22 of the largest of all groups, twice for a
+            // difference.  (Infinite ones are not rounded.)
+            float size = best == 0 ? 0.0f : fabsf(key_value(best));
+            if (a.group_sum == 2 && second != 0) {
+                const float other = fabsf(key_value(second));
+                size = fmaxf(size < kInf ? size : 0.0f, other < kInf ? other : 0.0f);
+            }
+            const float most = __uint_as_float(warp_key_max(size < kInf ? __float_as_uint(size) : 0u));
             const float x = key_value(worst), y = key_value(out);
-            if (!by_logits && out != 0 &&
-                !(x - y > 2.0f * near + 0x1p-21f * (fabsf(x) + fabsf(y)))) {
+            if (!by_logits && out != 0 && !(x - y > 2.0f * near + 0x1p-20f * most)) {
                 uint64_t exact, w, o;
                 whole = !group_value64<TYPE, V>(a, at, row, lane, m, open, best, second, near, exact);
                 uint64_t kept[V];
