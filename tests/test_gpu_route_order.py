@@ -1,5 +1,5 @@
-"""GPU tests of route_topk's order where FP32 cannot tell values apart and where they are
-infinite: the ids are those of 64 bits."""
+"""GPU tests of route_topk's order where FP32 cannot tell values apart, where they are
+infinite, and where scores are all but 1: the ids are those of 64 bits."""
 import itertools
 
 import numpy as np
@@ -159,3 +159,34 @@ def test_group_sums_of_opposite_biases(tg, score, size, E, groups):
     for top_groups in (1, groups // 2):
         check(tg, logits.cuda(), 2, score, bias.cuda(), groups=groups, top_groups=top_groups,
               group_sum=2)
+
+
+# -------------------------------------------------------------- scores near 1 ----
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+def test_without_a_bias_by_logits(tg, score, name):
+    """Without a bias experts are in the order of their logits, also where their scores are
+    the same number in 64 bits, and whatever the groups are valued by."""
+    T, E, groups = 100, 64, 4
+    g = torch.Generator().manual_seed(0)
+    logits = 40.0 + 20.0 * torch.rand((T, E), generator=g)
+    logits[50:] -= 800.0 * torch.rand((50, E), generator=g)
+    logits = logits.to(getattr(torch, name)).cuda()
+    l = logits.double().cpu().numpy()
+    check(tg, logits[:50], 4, score, None, values=l[:50])
+    # (All groups are kept, so that their order does not matter.)
+    for group_sum in (1, 2):
+        r = tg.route_topk(logits, 4, score=score, groups=groups, top_groups=groups,
+                          group_sum=group_sum)
+        assert np.array_equal(r.ids.cpu().numpy(), choose(l, l, 4))
+    # One group ahead of the others: the order within it.
+    logits[:, :16] -= 100.0
+    logits[:, 32:] -= 100.0
+    l = logits.double().cpu().numpy()
+    sums = np.sort(ref.scores(l, score).reshape(T, groups, -1), axis=2)[:, :, -2:].sum(axis=2)
+    others = np.delete(sums, 1, axis=1).max(axis=1)
+    rows = np.flatnonzero(sums[:, 1] > others + 1e-6)
+    r = tg.route_topk(logits, 3, score=score, groups=groups, top_groups=1, group_sum=2)
+    want = 16 + choose(l[:, 16:32], l[:, 16:32], 3)
+    assert len(rows) >= 40 and np.array_equal(r.ids.cpu().numpy()[rows], want[rows])

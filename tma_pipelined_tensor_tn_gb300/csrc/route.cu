@@ -9,10 +9,11 @@
 // the register: the lowest lane that holds the largest value holds the lowest index
 // of a tie.
 //
-// The choice follows exact arithmetic.  Without a bias (and with groups valued by one
-// expert) it is made on the logits themselves, which order as their scores do.
-// Otherwise v is computed in FP32 with an error bound, and experts (or groups) whose order
-// hangs on values closer than that are compared in FP64: about one token in a thousand.
+// Without a bias experts are chosen by the logits themselves, which order as their scores
+// do.  Otherwise (and for sums of two scores of a group) v is computed in FP32 with an
+// error bound, and experts or groups whose order hangs on values closer than that are
+// compared in FP64: about one token in a thousand.  Values that FP64 makes equal (sigmoids
+// past 37 are 1) are ties.
 //
 // The k-th largest of the lanes' largest values bounds the k-th largest of all from below:
 // the experts above it, a few more than k, are brought together in shared memory and
@@ -302,8 +303,8 @@ __device__ __noinline__ int32_t order64(const RouteArgs& a, int64_t row, int lan
     return placed;
 }
 
-// The exact value of a lane's group from its two best experts (by FP32 keys), or false where
-// a third is too close to them to say which the two are.
+// The exact value of a lane's group from its two best experts (by their keys), or false where
+// a third is too close to them to say which the two are (keys of logits always say so).
 template <int TYPE, int V>
 __device__ __noinline__ bool group_value64(const RouteArgs& a, const LaneExperts& at, int64_t row,
                                            int lane, float m, const uint32_t (&key)[V],
@@ -334,7 +335,8 @@ __device__ __noinline__ bool group_value64(const RouteArgs& a, const LaneExperts
     uint32_t others = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        if (key[j] != 0 && in != 0 && at.first + j != i1 && at.first + j != last && !below(key[j], in))
+        if (a.bias && key[j] != 0 && in != 0 && at.first + j != i1 && at.first + j != last &&
+            !below(key[j], in))
             others |= 1u << j;
     bool clear = true;
     for (; others != 0; others &= others - 1)
@@ -414,10 +416,10 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_cons
         load_logits<TYPE, V>(a.logits, row + at.first, at.count, a.aligned, l);
         float m = -kInf;
         const bool softmax = a.score == kScoreSoftmax;
-        // Scores order as logits do.
-        const bool by_logits = !a.bias && (a.groups == 1 || a.group_sum == 1);
+        // Scores order as logits do; sums of two of them do not.
+        const bool by_logits = !a.bias, sums = a.groups > 1 && a.group_sum == 2;
         float inverse = 1.0f;   // of the sum over all experts
-        if (softmax && (!by_logits || !a.renormalize)) {
+        if (softmax && (!by_logits || sums || !a.renormalize)) {
 #pragma unroll
             for (int j = 0; j < V; ++j) m = fmaxf(m, l[j]);
             m = warp_max(m);
@@ -426,19 +428,21 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_cons
             for (int j = 0; j < V; ++j) sum += expf(l[j] - m);   // (no experts: NaN, not used)
             inverse = __fdividef(1.0f, warp_sum(sum));
         }
+        const auto score = [&](float x) {
+            // (A quotient by more than 2^126 would be 0 or NaN.)
+            return softmax ? expf(x - m) * inverse
+                           : x < -80.0f ? 0.0f : __fdividef(1.0f, 1.0f + expf(-x));
+        };
         uint32_t key[V];
         if (by_logits) {
 #pragma unroll
             for (int j = 0; j < V; ++j) key[j] = l[j] == -kInf ? 0u : order_key(l[j]);
         } else {
             float b[V] = {};
-            if (a.bias) load_logits<kLogitsF32, V>(a.bias, at.first, at.count, a.bias_aligned, b);
+            load_logits<kLogitsF32, V>(a.bias, at.first, at.count, a.bias_aligned, b);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float v = softmax ? expf(l[j] - m) * inverse : __fdividef(1.0f, 1.0f + expf(-l[j]));
-                // (A quotient by more than 2^126 would be 0 or NaN.)
-                if (!softmax && l[j] < -80.0f) v = 0.0f;
-                if (a.bias) v += b[j];
+                float v = score(l[j]) + b[j];
                 // (All scores are NaN: the logits, so that the one that made them so is chosen.)
                 if (inverse != inverse) v = l[j];
                 key[j] = l[j] == -kInf ? 0u : order_key(v);
@@ -453,9 +457,12 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_cons
         if (a.groups > 1) {
             uint32_t best, second, worst, out;
             group_best<V>(at, key, best, second);
-            const float v =
-                key_value(best) + (a.group_sum == 2 && second != 0 ? key_value(second) : 0.0f);
-            const uint32_t value = best == 0 ? 0u : order_key(v);
+            float v1 = key_value(best), v2 = sums && second != 0 ? key_value(second) : 0.0f;
+            if (by_logits && sums) {
+                v1 = score(v1);
+                if (second != 0) v2 = score(v2);
+            }
+            const uint32_t value = best == 0 ? 0u : order_key(v1 + v2);
             uint32_t open[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) open[j] = key[j];
@@ -463,14 +470,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_cons
             // Each value is rounded by 2^-24 of itself and of the one or two that it adds up,
             // which may cancel out: by 2^-22 of the largest of all groups, twice for a
             // difference.  (Infinite ones are not rounded.)
-            float size = best == 0 ? 0.0f : fabsf(key_value(best));
-            if (a.group_sum == 2 && second != 0) {
-                const float other = fabsf(key_value(second));
-                size = fmaxf(size < kInf ? size : 0.0f, other < kInf ? other : 0.0f);
-            }
-            const float most = __uint_as_float(warp_key_max(size < kInf ? __float_as_uint(size) : 0u));
+            const uint32_t size1 = best != 0 && fabsf(v1) < kInf ? __float_as_uint(fabsf(v1)) : 0u;
+            const uint32_t size2 = fabsf(v2) < kInf ? __float_as_uint(fabsf(v2)) : 0u;
+            const float most = __uint_as_float(warp_key_max(max(size1, size2)));
             const float x = key_value(worst), y = key_value(out);
-            if (!by_logits && out != 0 && !(x - y > 2.0f * near + 0x1p-20f * most)) {
+            if ((sums || !by_logits) && out != 0 && !(x - y > 2.0f * near + 0x1p-20f * most)) {
                 uint64_t exact, w, o;
                 whole = !group_value64<TYPE, V>(a, at, row, lane, m, open, best, second, near, exact);
                 uint64_t kept[V];
