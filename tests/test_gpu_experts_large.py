@@ -100,3 +100,32 @@ def test_several_units_of_a_cluster(tg, group, zeros, name):
     d = tg.gemm_w4(a, *w4_tests.gpu(codes, s, z), group=group)
     w4_tests.check(d, a, codes, s, z, group, name)
     tg.check()
+
+
+@pytest.mark.parametrize("M", [1, 4, 8])
+@pytest.mark.parametrize("blocks,K", [(0.5, 800), (0.5, 768), (0.55, 768), (0.55, 800), (2, 544),
+                                      (2.01, 544), (2.01, 96)])
+def test_few_tokens_where_the_kernels_change_over(tg, sms, M, blocks, K):
+    """Blocks of 128 rows around half an SM's and two, K around 768."""
+    N = 128 * int(blocks * sms + 0.99) - 3
+    rng = np.random.default_rng(M)
+    codes, s, z = w4_tests.weights(rng, N, K, 128, True, "bf16")
+    a = torch.from_numpy(rng.normal(size=(M, K))).bfloat16().cuda()
+    d = tg.gemm_w4(a, *w4_tests.gpu(codes, s, z))
+    w4_tests.check(d, a, codes, s, z, 128, "bf16")
+    tg.check()
+
+
+@pytest.mark.parametrize("group", [64, 128])
+def test_weights_past_32_bit_offsets_in_both_kernels(tg, group):
+    """Codes of more than 2^32 bytes: the last rows against a product of those rows alone."""
+    N, K = 300000, 32768
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB of device memory")
+    B = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda")
+    SB = torch.rand((N, K // group), device="cuda").half()
+    a = torch.randn((2, K), device="cuda").half()
+    d = tg.gemm_w4(a, B, SB, group=group)
+    for lo in (0, 262143, N - 70):
+        codes, s = B[lo:lo + 70].cpu().numpy(), SB[lo:lo + 70].cpu()
+        w4_tests.check(d[:, lo:lo + 70], a, codes, s, None, group, "f16")

@@ -3,7 +3,7 @@
 //
 // q - z is a whole number of five bits, exact in 16 bits, so the inner sums run on
 // mma.sync with FP32 accumulators and the scale is applied to a whole group's sum in
-// FP32.  (gemm_w4_many.cu has more tokens, groups of rows, and many rows of weights.)
+// FP32.  (gemm_w4_many.cu has more tokens, groups of rows, and many rows of weights with a long K.)
 //
 // A unit is a block of weight rows and up to eight tokens.  The warps of a CTA are WR along
 // the rows, 16 MT each, and WK along K, 128 k of a stage each.  One thread keeps a ring of
@@ -436,12 +436,17 @@ cudaError_t launch_gemm_w4(const W4Args& a, bool bf16, const W4Device& dev, cuda
     // Up to eight tokens here, more on tcgen05: N x K = 4096 x 4096, groups of 128, 6.9 us here
     // and 8.1 there with 8 tokens, 9.4 and 8.2 with 12; 14336 x 4096, groups of 32, 15.7 and
     // 22.5, 28.6 and 22.5.  With groups of 128, whose sums are read back least, there too where
-    // its blocks of 128 rows take more than half the SMs: one token, 8192 x 4096 9.5 and 11.2,
-    // 11008 x 4096 13.4 and 11.3, 19456 x 4096 15.3 and 13.0, 28672 x 8192 35.6 and 35.9.
+    // its blocks of 128 rows take more than half the SMs and K is long: one token, 8192 x 4096
+    // 8.9 and 9.9, 9856 x 1024 5.6 and 5.4, 11008 x 4096 12.8 and 10.8, 19456 x 8192 24.1 and
+    // 19.9; 14336 x 512 4.4 and 4.5, 28672 x 512 6.2 and 7.1, x 768 7.8 and 8.6, x 896 8.8 and
+    // 8.4, x 8192 35.2 and 33.7.  Past two blocks an SM whatever K is: 38912 x 512 6.7 and 7.4,
+    // 39040 x 512 8.9 and 7.4, x 256 6.8 and 5.0.  (The same with four and eight tokens.)
     // By group of rows, with N x K = 4096 x 2048: scales of 32 k up to two rows on average (64
     // groups with two each 91 and 100 us, with 256 rows in 50 of them 115 and 100), of 64 and
     // 128 none (64 groups, 128 rows: 68 and 44, 65 and 43; 8 rows 19 and 18, 18 and 16).
-    const bool wide = a.group == 128 && 2 * ceil_div(a.N, 128) > dev.sms;
+    const int64_t blocks = ceil_div(a.N, 128);
+    const bool wide =
+        a.group == 128 && 2 * blocks > dev.sms && (a.K > 768 || blocks > 2ll * dev.sms);
     const int64_t few = a.offsets ? (a.group == 32 ? 2 : 0) : wide ? 0 : 8;
     if (ceil_div(a.M, a.offsets ? a.groups : 1) > few)
         return launch_gemm_w4_many(a, bf16, dev, stream);
