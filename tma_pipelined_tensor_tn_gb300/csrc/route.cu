@@ -112,6 +112,13 @@ __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
+// part / sum: exactly 1 for all of it, so that one choice has its scale and no gradient
+// (a division rounded right does that too, and makes the backward of 16384 x 122 5.3 us
+// instead of 4.8).
+__device__ __forceinline__ float share(float part, float sum) {
+    return part == sum ? 1.0f : __fdividef(part, sum);
+}
+
 // Unsigned keys that order as the numbers do: 0 for a closed expert, zeros of both
 // signs alike, NaN above everything.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) route_kernel(const __grid_cons
                                   : 1.0f / (1.0f + expf(-logit));
             }
             const float sum = warp_sum(w);
-            w = id >= 0 ? a.scale * __fdividef(w, sum) : 0.0f;
+            w = id >= 0 ? a.scale * share(w, sum) : 0.0f;
         } else if (id >= 0) {
             w = a.scale * (softmax ? expf(logit - m) * inverse : 1.0f / (1.0f + expf(-logit)));
         }
@@ -649,7 +656,7 @@ route_backward_kernel(const __grid_constant__ RouteArgs a) {
                     s = logit <= 0.0f ? expf(logit - low) * p1 : 1.0f / (1.0f + expf(-logit));
                 }
                 const float sum = warp_sum(s);
-                s = id >= 0 ? __fdividef(s, sum) : 0.0f;
+                s = id >= 0 ? share(s, sum) : 0.0f;
                 const float mean = warp_sum(dw * s);
                 d = s * (dw - mean);
                 if (!softmax) d *= p1;
