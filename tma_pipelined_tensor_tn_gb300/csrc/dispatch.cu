@@ -178,9 +178,14 @@ place_kernel(const int32_t* ids, const int32_t* counts, int32_t* offsets, int32_
 }
 
 // All of it in one launch of one cluster: a warp has BATCHES times 32 slots, ranked in
-// registers; the counts of the CTAs meet through distributed shared memory.
+// registers; the counts of the CTAs meet through distributed shared memory.  Every batch
+// costs its ballots whether it has slots or not (0.5 to 0.7 us), so that each number of
+// slots runs the form with the fewest that hold it.
 // (64 columns, with the copies: 8192 slots 4.7 us, in chunks 6.9; 32792 8.1 and 11.4; 131072
 // 17.0 and 18.9.)
+// (64 experts: 8192 slots in one batch 4.6 us, in two 5.2; 16384 in two 5.4, in three 5.9; 24576
+// in three 6.6, in five 7.8; 32768 and 40960 in five 8.0, in eight 10.0; 49152 in eight 10.0,
+// in sixteen 14.0; 65536 10.6 and 14.7.)
 constexpr int kClusterSlots = 131072;
 constexpr int kClusterCtas = 8, kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
 template <int BATCHES>

@@ -13,7 +13,9 @@
 // so the pairs that one mask takes out of a word (nibbles i and i + 4) become the pairs of
 // an MMA operand, and the tokens' values are brought into the same order with byte
 // permutes.  The WK partial sums meet in shared memory in a fixed order.
-// What bounds it is the instructions, 9 of them to widen eight codes.
+// Its 358 instructions for 32 rows by 128 k, 9 to widen eight codes, are about as long as the
+// bytes (4.4 us at 4096 x 14336 if every slot issued); with 16 warps an SM half the slots do,
+// and what bounds it is the latency from a stage's arrival over widening to the sums.
 // The loop over stages is one loop for prologue and body, not unrolled: a kernel of a few
 // microseconds otherwise waits for its instructions.
 #include <cuda_bf16.h>

@@ -24,10 +24,11 @@
 // taken out of the quotient, so that scores that FP32 cannot hold cancel.
 //
 // The logits are read once and are a microsecond or two of bandwidth: what bounds the
-// kernels is instructions and the latency of shuffles.  8192 x 256 FP32, sigmoid, bias, four of
-// eight groups, k = 8: 12.7 us (1100 instructions a token; with a round of maxima for each
-// expert 29 us), 6.3 without bias and groups; 16384 x 122 BF16, softmax, k = 6: 9.2 us, its
-// backward 4.8.
+// kernels is instructions (60 % of the issue slots at 20 to 27 warps an SM) and the latency
+// of warp-wide steps, which do not get fewer with the experts.  8192 x 256 FP32, sigmoid, bias,
+// four of eight groups, k = 8: 13.7 us (1170 instructions a token; with a round of maxima for
+// each expert 29 us), 10.9 without a bias, 7.0 without groups either (590); 16384 x 122 BF16,
+// softmax, k = 6: 9.8 us (500), its backward 5.0 over all experts and 4.8 renormalised.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -669,9 +670,9 @@ route_backward_kernel(const __grid_constant__ RouteArgs a) {
     }
 }
 
-// CTAs, whose warps take tokens in turn: two waves of four to an SM (8192 x 256 in groups 12.7
-// us, one wave 13.8, a CTA for each eight tokens 12.7; 16384 x 122 9.2, 9.6 and 10.0); the
-// backward two of eight (4.8 us, one 5.4).
+// CTAs, whose warps take tokens in turn: two waves of four to an SM (8192 x 256 in groups 13.7
+// us, one wave 15.1, a CTA for each eight tokens 13.7; 16384 x 122 9.8, 10.2 and 10.4); the
+// backward two of eight (5.0 us, one 5.7).
 unsigned route_grid(int64_t T, int sms) {
     const int64_t ctas = ceil_div(T, kWarps);
     return static_cast<unsigned>(ctas < 8ll * sms ? ctas : 8ll * sms);

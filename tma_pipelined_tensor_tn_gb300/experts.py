@@ -57,7 +57,9 @@ def route_topk(logits, k: int, score: str = "softmax", bias=None, groups: int = 
     ``group_sum`` (1 or 2) best values have the largest sum are chosen from.  The weights
     are scale * p, without the bias, divided by their sum over the chosen with
     ``renormalize``.  A logit of -inf closes an expert; choices that none is left for get
-    id -1 and weight 0.
+    id -1 and weight 0.  A bias of +inf puts its expert first, -inf last.
+
+    E is at most 512 and k 32; the grouped products that follow take 384 experts.
     """
     args = (logits, k, _sigmoid(score), bias, groups, top_groups, group_sum, renormalize, scale)
     if stream is None:
@@ -68,7 +70,8 @@ def route_topk(logits, k: int, score: str = "softmax", bias=None, groups: int = 
 def route_topk_backward(logits, ids, dweights, score: str = "softmax", renormalize: bool = True,
                         scale: float = 1.0, stream=None):
     """The gradient of the logits (T, E), in their type, from that of route_topk's weights
-    (T, k) float32, with the choice ``ids`` held fixed."""
+    (T, k) float32, with the choice ``ids`` held fixed.  A token's ids are different experts,
+    as route_topk makes them; those outside 0 .. E - 1 have no gradient."""
     args = (logits, ids, dweights, _sigmoid(score), renormalize, scale)
     if stream is None:
         return _ops().route_topk_backward(*args)
