@@ -429,7 +429,8 @@ int64_t norm_residual_backward_workspace_size(int64_t T, int64_t C);
  *             token's chosen p when renormalize != 0.
  * The order is that of FP64: values (and groups' sums) that FP32 cannot tell apart are
  * compared in FP64, and those that FP64 makes equal (sigmoids past 37 are 1) are ties.
- * Without a bias experts are ordered by their logits, whose order is that of p exactly.
+ * Without a bias experts, and groups valued by one, are ordered by their logits, whose
+ * order is that of p exactly.
  * A logit of minus infinity closes an expert to its token: it is
  * never chosen, whatever its bias, and choices that no expert is left for get id -1
  * and weight 0.  NaN ranks above every number and shows in the weights.
