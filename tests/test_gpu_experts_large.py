@@ -106,7 +106,7 @@ def test_several_units_of_a_cluster(tg, group, zeros, name):
 @pytest.mark.parametrize("blocks,K", [(0.5, 800), (0.5, 768), (0.55, 768), (0.55, 800), (2, 544),
                                       (2.01, 544), (2.01, 96)])
 def test_few_tokens_where_the_kernels_change_over(tg, sms, M, blocks, K):
-    """Blocks of 128 rows around half an SM's and two, K around 768."""
+    """Blocks of 128 rows around half an SM and two an SM, K around 768."""
     N = 128 * int(blocks * sms + 0.99) - 3
     rng = np.random.default_rng(M)
     codes, s, z = w4_tests.weights(rng, N, K, 128, True, "bf16")
